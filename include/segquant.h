@@ -308,6 +308,113 @@ sq_status sq_linear_forward_codes_hadamard(const int8_t* q_pos, const int8_t* q_
                                            const float* s_neg, const float* bias, void* y,
                                            sq_dtype yt, int64_t ldy, sq_stream_t stream);
 
+/* ---- Group norm with an activation, channels last.  Diffusion U-Nets and
+ * image decoders put it in front of the layers this library quantizes.
+ * x: [B, S, C] fp32 or bf16, S positions (H*W) of C channels with unit stride,
+ * positions ldx and images xbs elements apart.  Channels form `groups` groups of
+ * C/groups; mean and (biased) variance over a group's S * C/groups values in
+ * fp32; z = (x - mean) / sqrt(var + eps) * gamma[c] + beta[c] (gamma, beta: device
+ * fp32 [C], NULL for 1 and 0); y = act(z), act 0 (none), SQ_ACT_SILU or SQ_ACT_GELU
+ * (exact, erf-based), rounded once to the output type.
+ * Requirements: C % 8 == 0 and C % groups == 0; the smallest block of whole
+ * groups that is a multiple of 16 bytes wide at most 8192 bytes
+ * (SQ_ERR_UNSUPPORTED); B <= 65535, S <= 2^30, C <= SQ_MAX_K (SQ_ERR_RANGE);
+ * pointers of maps and codes 16-byte aligned, their strides multiples of 16 bytes.
+ * B = 0 or S = 0 is a no-op (gradients of gamma and beta: zeros).  Infinities and
+ * NaN stay in their group.  Outputs must not overlap inputs, except that y may be
+ * x itself (same type and strides) and dx may be x or dy. */
+
+/* Host only: workspace bytes (0: none needed, NULL may be passed) of the forward
+ * calls (backward = 0) or the backward call (backward = 1) on the current device.
+ * The workspace needs no initial contents and holds nothing between calls; calls
+ * that share one must not overlap on the GPU. */
+sq_status sq_group_norm_workspace_size(int64_t B, int64_t S, int64_t C, int32_t groups, sq_dtype xt,
+                                       int32_t backward, size_t* bytes);
+
+/* y: [B, S, C] of type yt, strides ldy and ybs.  stats: device fp32
+ * [B, groups, 2], the mean and 1 / sqrt(var + eps) that the backward call takes, or
+ * NULL. */
+sq_status sq_group_norm_act(const void* x, sq_dtype xt, int64_t B, int64_t S, int64_t C,
+                            int64_t ldx, int64_t xbs, int32_t groups, const float* gamma,
+                            const float* beta, float eps, int32_t act, void* y, sq_dtype yt,
+                            int64_t ldy, int64_t ybs, float* stats, void* workspace,
+                            size_t workspace_bytes, sq_stream_t stream);
+
+/* The norm fused into the combined-code producer: c, int8 [B*S, C] with row
+ * stride ldc (a multiple of 16), holds the codes that
+ * sq_quantize_activations_combined writes for y = act(z) rounded to bf16 (bit for
+ * bit those of sq_group_norm_act's bf16 output), K segments of the C channels as
+ * there; C % 16 == 0.  y: bf16 [B*S, C], row stride ldy, written too, or NULL.
+ * The codes feed sq_linear_forward_combined. */
+sq_status sq_quantize_activations_combined_norm(const void* x, sq_dtype xt, int64_t B, int64_t S,
+                                                int64_t C, int64_t ldx, int64_t xbs,
+                                                int32_t groups, const float* gamma,
+                                                const float* beta, float eps, int32_t act,
+                                                const sq_segments* kseg, const float* s_pos,
+                                                const float* s_neg, int8_t* c, int64_t ldc,
+                                                void* y, int64_t ldy, void* workspace,
+                                                size_t workspace_bytes, sq_stream_t stream);
+
+/* Gradients: dy, x and dx [B, S, C] of type xt; stats as written by the forward
+ * call; with xhat = (x - mean) * rstd and dz = dy * act'(z):
+ * dgamma[c] = sum dz * xhat, dbeta[c] = sum dz over positions and images (fp32 [C],
+ * overwritten; either may be NULL), dx = rstd * (dz * gamma - m1 - xhat * m2) with
+ * m1, m2 the group's means of dz * gamma and dz * gamma * xhat.  Sums run in a fixed
+ * order. */
+sq_status sq_group_norm_act_backward(const void* dy, int64_t lddy, int64_t dybs, const void* x,
+                                     sq_dtype xt, int64_t B, int64_t S, int64_t C, int64_t ldx,
+                                     int64_t xbs, int32_t groups, const float* stats,
+                                     const float* gamma, const float* beta, int32_t act, void* dx,
+                                     int64_t lddx, int64_t dxbs, float* dgamma, float* dbeta,
+                                     void* workspace, size_t workspace_bytes, sq_stream_t stream);
+
+/* ---- Low-rank adapters of many requests beside a shared (quantized)
+ * projection.  The struct is host memory; a, b and scale are device buffers:
+ * a bf16 [L, R, K], b bf16 [L, N, R], contiguous, scale fp32 [L] (NULL: 1).
+ * Adapters of smaller rank are padded with zeros.  R % 8 == 0 and R <= 128 (a
+ * higher rank is the sum of two calls); K % 16 == 0, N % 16 == 0. */
+typedef struct {
+  int32_t L;
+  int32_t R;
+  int64_t K;
+  int64_t N;
+  const void* a;
+  const void* b;
+  const float* scale;
+} sq_adapters;
+
+/* Request q has the rows bounds[q] .. bounds[q+1] and the adapter index[q]
+ * (below 0: none); bounds: device int32 [requests + 1], not decreasing, within
+ * [0, M]; index: device int32 [requests].  An adapter may serve any number of
+ * requests.  A request with bounds outside the batch or an index >= L is left out
+ * and sets SQ_ERR_RANGE in the status word; falling bounds set it too, and which
+ * rows then receive their term is unspecified (no access leaves the tensors).
+ *   y[m, :] += scale_l * B_l (A_l x[m, :])   for the rows of requests with an adapter;
+ * all other rows of y are neither read nor written.  x: [M, K], y: [M, N]; products
+ * are exact, sums in fp32, one rounding to y's type.  hidden: fp32 [M, R] or NULL,
+ * receives A_l x (zeros in rows without an adapter) for the backward call.
+ * M = 0 is a no-op.  y must not overlap x. */
+sq_status sq_adapter_add(const void* x, sq_dtype xt, int64_t M, int64_t ldx,
+                         const sq_adapters* adapters, const int32_t* bounds, const int32_t* index,
+                         int32_t requests, void* y, sq_dtype yt, int64_t ldy, float* hidden,
+                         sq_stream_t stream);
+
+/* Host only: workspace bytes of sq_adapter_backward (rules as for
+ * sq_group_norm_workspace_size). */
+sq_status sq_adapter_backward_workspace_size(int64_t M, int32_t R, size_t* bytes);
+
+/* Gradients of the term that sq_adapter_add adds: dy [M, N], x and dx [M, K] (dx of
+ * x's type, written in every row, zeros in rows without an adapter), hidden as
+ * written by sq_adapter_add; da fp32 [L, R, K] and db fp32 [L, N, R], overwritten:
+ * sums over all rows of all requests of an adapter, in a fixed order, zeros for an
+ * adapter that no request uses. */
+sq_status sq_adapter_backward(const void* dy, sq_dtype dyt, int64_t M, int64_t lddy, const void* x,
+                              sq_dtype xt, int64_t ldx, const float* hidden,
+                              const sq_adapters* adapters, const int32_t* bounds,
+                              const int32_t* index, int32_t requests, void* dx, int64_t lddx,
+                              float* da, float* db, void* workspace, size_t workspace_bytes,
+                              sq_stream_t stream);
+
 /* Small-M forward from DualScale codes (1 <= M <= 128 tokens): the same result
  * as sq_linear_forward_codes, bit for bit (SegQuant DualScale, Spanish
  * technical summary 2.B; the two int8 products and the fused epilogue), with

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -28,7 +29,9 @@ __all__ = ["QuantizedWeight", "SegQuantError", "calibrate", "quantize_weights", 
            "splitk_workspace_size", "splitk_workspace", "linear_from_codes_splitk",
            "linear_accumulators", "stream_status", "qweight_sizes", "calibrate_hadamard",
            "quantize_activations_hadamard", "rotate_weights_hadamard",
-           "linear_from_codes_hadamard", "calibrate_act", "quantize_activations_combined_act"]
+           "linear_from_codes_hadamard", "calibrate_act", "quantize_activations_combined_act",
+           "group_norm_act", "group_norm_act_backward", "quantize_activations_combined_norm",
+           "Adapters", "adapter_add", "adapter_backward"]
 
 
 def _dtype_code(t: torch.dtype) -> int:
@@ -465,3 +468,262 @@ def linear_from_codes_hadamard(q_pos: torch.Tensor, q_neg: torch.Tensor, qw: Qua
         w_rot.stride(0), _ptr(s_pos), _ptr(s_neg), _ptr(bias), _ptr(out), _dtype_code(out.dtype),
         out.stride(0), _stream(stream)))
     return out
+
+
+# --------------------------------------------- group norm with an activation
+# The norm in front of the quantized layers of a U-Net or an image decoder,
+# channels last: maps are [B, S, C] with S = H*W (for an NCHW tensor in the
+# channels_last memory format, ``t.permute(0, 2, 3, 1).flatten(1, 2)``).
+
+def _norm_act_code(act: str) -> int:
+    return 0 if act == "none" else _act_code(act)
+
+
+def _check_map(x: torch.Tensor, name: str, like: Optional[torch.Tensor] = None):
+    if x.dim() != 3 or x.stride(2) != 1:
+        raise ValueError(f"{name} must be a 3-D [B, S, C] tensor with unit channel stride")
+    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if like is not None and x.shape != like.shape:
+        raise ValueError(f"{name} must have the shape {tuple(like.shape)}, not {tuple(x.shape)}")
+
+
+def _check_f32(t: Optional[torch.Tensor], shape, name: str):
+    """An optional contiguous fp32 CUDA tensor of the given shape: its pointer or None."""
+    if t is None:
+        return None
+    if (t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous()
+            or not t.is_cuda or t.get_device() != torch.cuda.current_device()):
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)} "
+                         "on the current device")
+    return t.data_ptr()
+
+
+def _row_stride(x: torch.Tensor) -> int:
+    """Element stride of positions (a single position or an empty map has none that matters)."""
+    return x.stride(1) if x.shape[1] > 1 else max(x.shape[2], 1)
+
+
+def _image_stride(x: torch.Tensor) -> int:
+    return x.stride(0) if x.shape[0] > 1 else 0
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_workspace_size(device: int, B: int, S: int, C: int, groups: int, xt: int, backward: int) -> int:
+    n = ctypes.c_size_t()
+    _lib.check("sq_group_norm_workspace_size", _lib.load().sq_group_norm_workspace_size(
+        B, S, C, groups, xt, backward, ctypes.byref(n)))
+    return n.value
+
+
+def _workspace(n: int, device, stream):
+    """A workspace of n bytes that lives until the call on ``stream`` has run."""
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def _norm_workspace(x: torch.Tensor, groups: int, backward: int, stream):
+    """(keep-alive tensor, pointer, bytes) of a norm call's workspace."""
+    B, S, C = x.shape
+    n = _norm_workspace_size(x.get_device(), B, S, C, groups, _dtype_code(x.dtype), backward)
+    if n == 0:
+        return None, None, 0
+    ws = _workspace(n, x.device, stream)
+    return ws, ws.data_ptr(), n
+
+
+def group_norm_act(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = None,
+                   beta: Optional[torch.Tensor] = None, eps: float = 1e-5, act: str = "none",
+                   out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                   return_stats: bool = False, stream=None):
+    """y = act(group_norm(x) * gamma + beta) of a channels-last map ``x`` [B, S, C];
+    act: 'none', 'silu' or 'gelu'.  ``out`` may be ``x`` itself.  With
+    ``return_stats`` also the fp32 [B, groups, 2] means and reciprocal deviations
+    that ``group_norm_act_backward`` takes."""
+    _check_map(x, "x")
+    B, S, C = x.shape
+    if out is None:
+        out = torch.empty((B, S, C), dtype=out_dtype or x.dtype, device=x.device)
+    _check_map(out, "out", x)
+    stats = torch.empty((B, groups, 2), dtype=torch.float32, device=x.device) if return_stats else None
+    ws, wp, wn = _norm_workspace(x, groups, 0, stream)
+    _lib.check("sq_group_norm_act", _lib.load().sq_group_norm_act(
+        x.data_ptr(), _dtype_code(x.dtype), B, S, C, _row_stride(x), _image_stride(x), groups,
+        _check_f32(gamma, (C,), "gamma"), _check_f32(beta, (C,), "beta"), eps, _norm_act_code(act),
+        out.data_ptr(), _dtype_code(out.dtype), _row_stride(out), _image_stride(out),
+        None if stats is None else stats.data_ptr(), wp, wn, _stream(stream)))
+    return (out, stats) if return_stats else out
+
+
+def quantize_activations_combined_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor],
+                                       beta: Optional[torch.Tensor], kseg: Sequence[int],
+                                       s_pos: torch.Tensor, s_neg: torch.Tensor, eps: float = 1e-5,
+                                       act: str = "none", out: Optional[torch.Tensor] = None,
+                                       return_y: bool = False, stream=None):
+    """Combined DualScale codes of y = act(group_norm(x)) rounded to bf16, int8
+    [B*S, C] with row stride a multiple of 16, in one pass over ``x`` [B, S, C]; the
+    codes feed ``linear_from_combined``.  With ``return_y`` also y, bf16 [B*S, C]
+    (the input of adapters beside the layer)."""
+    _check_map(x, "x")
+    B, S, C = x.shape
+    J = len(kseg) - 1
+    if out is None:
+        ldc = (C + 15) // 16 * 16
+        out = torch.empty((B * S, ldc), dtype=torch.int8, device=x.device)[:, :C]
+    _check_2d(out, "out")
+    if tuple(out.shape) != (B * S, C) or out.dtype != torch.int8:
+        raise ValueError(f"out must be int8 [{B * S}, {C}]")
+    y = torch.empty((B * S, C), dtype=torch.bfloat16, device=x.device) if return_y else None
+    seg, keep = _lib.segments(kseg)
+    ws, wp, wn = _norm_workspace(x, groups, 0, stream)
+    _lib.check("sq_quantize_activations_combined_norm",
+               _lib.load().sq_quantize_activations_combined_norm(
+                   x.data_ptr(), _dtype_code(x.dtype), B, S, C, _row_stride(x), _image_stride(x), groups,
+                   _check_f32(gamma, (C,), "gamma"), _check_f32(beta, (C,), "beta"), eps,
+                   _norm_act_code(act), ctypes.byref(seg), _check_f32(s_pos, (J,), "s_pos"),
+                   _check_f32(s_neg, (J,), "s_neg"), out.data_ptr(),
+                   out.stride(0) if B * S > 1 else (C + 15) // 16 * 16,
+                   None if y is None else y.data_ptr(), C, wp, wn, _stream(stream)))
+    return (out, y) if return_y else out
+
+
+def group_norm_act_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor,
+                            gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
+                            act: str = "none", dx: Optional[torch.Tensor] = None, stream=None):
+    """Gradients (dx, dgamma, dbeta) of ``group_norm_act``: dx of x's type, dgamma and
+    dbeta fp32 [C] (also where gamma or beta is None: those of ones and zeros).
+    ``stats`` as returned by the forward call; ``dx`` may be ``x`` or ``dy``."""
+    _check_map(x, "x")
+    _check_map(dy, "dy", x)
+    B, S, C = x.shape
+    if dy.dtype != x.dtype:
+        raise TypeError("dy must have x's dtype")
+    if stats.dim() != 3 or stats.shape[0] != B:
+        raise ValueError("stats must be the [B, groups, 2] tensor of the forward call")
+    groups = stats.shape[1]
+    if dx is None:
+        dx = torch.empty((B, S, C), dtype=x.dtype, device=x.device)
+    _check_map(dx, "dx", x)
+    if dx.dtype != x.dtype:
+        raise TypeError("dx must have x's dtype")
+    grads = torch.empty((2, C), dtype=torch.float32, device=x.device)
+    ws, wp, wn = _norm_workspace(x, groups, 1, stream)
+    g = grads.data_ptr()
+    _lib.check("sq_group_norm_act_backward", _lib.load().sq_group_norm_act_backward(
+        dy.data_ptr(), _row_stride(dy), _image_stride(dy), x.data_ptr(), _dtype_code(x.dtype), B, S, C,
+        _row_stride(x), _image_stride(x), groups, _check_f32(stats, (B, groups, 2), "stats"),
+        _check_f32(gamma, (C,), "gamma"), _check_f32(beta, (C,), "beta"), _norm_act_code(act),
+        dx.data_ptr(), _row_stride(dx), _image_stride(dx), g, g + 4 * C, wp, wn, _stream(stream)))
+    return dx, grads[0], grads[1]
+
+
+# ------------------------------------------------------- low-rank adapters
+@dataclasses.dataclass
+class Adapters:
+    """L low-rank adapters of a [N, K] projection: a bf16 [L, R, K], b bf16 [L, N, R],
+    scale fp32 [L] (None: 1).  Adapters of smaller rank are padded with zeros."""
+    a: torch.Tensor
+    b: torch.Tensor
+    scale: Optional[torch.Tensor] = None
+
+    def __post_init__(self):
+        a, b = self.a, self.b
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise ValueError("a must be [L, R, K] and b [L, N, R]")
+        for t, name in ((a, "a"), (b, "b")):
+            if t.dtype != torch.bfloat16 or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"{name} must be a contiguous bfloat16 CUDA tensor")
+        s = self.scale
+        if s is not None and (s.dtype != torch.float32 or s.shape != (a.shape[0],) or not s.is_cuda
+                              or not s.is_contiguous()):
+            raise ValueError("scale must be a contiguous float32 CUDA tensor of shape [L]")
+        if a.device != b.device or (s is not None and s.device != a.device):
+            raise ValueError("a, b and scale must be on the same device")
+
+    def c_struct(self):
+        """The C view (sq_adapters), rebuilt only when a tensor it is made of has moved."""
+        s = self.scale
+        key = (self.a.data_ptr(), self.b.data_ptr(), 0 if s is None else s.data_ptr())
+        cached = self.__dict__.get("_c_struct")
+        if cached is None or cached[0] != key:
+            L, R, K = self.a.shape
+            cached = (key, _lib.SqAdapters(L, R, K, self.b.shape[1], key[0], key[1], key[2] or None))
+            self.__dict__["_c_struct"] = cached
+        return cached[1]
+
+
+def _check_rows(t: torch.Tensor, rows: int, cols: int, name: str):
+    _check_2d(t, name)
+    if t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}], not {list(t.shape)}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current device")
+
+
+def _check_requests(bounds: torch.Tensor, index: torch.Tensor, adapters: Adapters) -> int:
+    n = index.shape[0] if index.dim() == 1 else -1
+    if (bounds.dtype != torch.int32 or index.dtype != torch.int32 or n < 0 or bounds.dim() != 1
+            or bounds.shape[0] != n + 1 or not bounds.is_contiguous() or not index.is_contiguous()):
+        raise ValueError("bounds must be int32 [requests + 1] and index int32 [requests]")
+    dev = torch.cuda.current_device()
+    if bounds.get_device() != dev or index.get_device() != dev or adapters.a.get_device() != dev:
+        raise ValueError("bounds, index and adapters must be on the current device")
+    return n
+
+
+def _ld(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def adapter_add(y: torch.Tensor, x: torch.Tensor, adapters: Adapters, bounds: torch.Tensor,
+                index: torch.Tensor, return_hidden: bool = False, stream=None):
+    """Adds the requests' low-rank terms to the shared projection's output ``y`` [M, N]
+    in place: rows bounds[q] .. bounds[q+1] of ``x`` [M, K] use adapter index[q]
+    (below 0: none), y += scale * (x a^T) b^T.  Rows of no request are left as they
+    are.  ``bounds`` int32 [Q + 1] and ``index`` int32 [Q] stay on the device.  For a
+    fused q | k | v projection with adapters of its own per part, call it on column
+    slices of ``y``.  With ``return_hidden`` returns (y, hidden), hidden = x a^T in fp32
+    [M, R] for ``adapter_backward``; otherwise y."""
+    n = _check_requests(bounds, index, adapters)
+    c = adapters.c_struct()
+    M = x.shape[0]
+    _check_rows(x, M, c.K, "x")
+    _check_rows(y, M, c.N, "y")
+    hidden = torch.empty((M, c.R), dtype=torch.float32, device=x.device) if return_hidden else None
+    _lib.check("sq_adapter_add", _lib.load().sq_adapter_add(
+        x.data_ptr(), _dtype_code(x.dtype), M, _ld(x), ctypes.byref(c), bounds.data_ptr(),
+        index.data_ptr(), n, y.data_ptr(), _dtype_code(y.dtype), _ld(y),
+        None if hidden is None else hidden.data_ptr(), _stream(stream)))
+    return (y, hidden) if return_hidden else y
+
+
+def adapter_backward(dy: torch.Tensor, x: torch.Tensor, hidden: torch.Tensor, adapters: Adapters,
+                     bounds: torch.Tensor, index: torch.Tensor, stream=None):
+    """Gradients (dx, da, db) of the term ``adapter_add`` adds: dx [M, K] of x's type
+    (zeros in rows without an adapter), da fp32 [L, R, K], db fp32 [L, N, R], each the sum
+    over all requests of its adapter.  ``hidden`` as returned by ``adapter_add``."""
+    n = _check_requests(bounds, index, adapters)
+    c = adapters.c_struct()
+    M, R = x.shape[0], c.R
+    _check_rows(x, M, c.K, "x")
+    _check_rows(dy, M, c.N, "dy")
+    dx = torch.empty((M, c.K), dtype=x.dtype, device=x.device)
+    da = torch.empty((c.L, R, c.K), dtype=torch.float32, device=x.device)
+    db = torch.empty((c.L, c.N, R), dtype=torch.float32, device=x.device)
+    wn = _adapter_workspace_size(M, R)
+    ws = _workspace(wn, x.device, stream)
+    _lib.check("sq_adapter_backward", _lib.load().sq_adapter_backward(
+        dy.data_ptr(), _dtype_code(dy.dtype), M, _ld(dy), x.data_ptr(), _dtype_code(x.dtype), _ld(x),
+        _check_f32(hidden, (M, R), "hidden"), ctypes.byref(c), bounds.data_ptr(), index.data_ptr(), n,
+        dx.data_ptr(), c.K, da.data_ptr(), db.data_ptr(), ws.data_ptr(), wn, _stream(stream)))
+    return dx, da, db
+
+
+@functools.lru_cache(maxsize=4096)
+def _adapter_workspace_size(M: int, R: int) -> int:
+    n = ctypes.c_size_t()
+    _lib.check("sq_adapter_backward_workspace_size",
+               _lib.load().sq_adapter_backward_workspace_size(M, R, ctypes.byref(n)))
+    return n.value

@@ -36,7 +36,14 @@ class SqQWeight(ctypes.Structure):
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+class SqAdapters(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int32), ("R", ctypes.c_int32), ("K", ctypes.c_int64),
+                ("N", ctypes.c_int64), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
+
+
 P_SEG = ctypes.POINTER(SqSegments)
+P_AD = ctypes.POINTER(SqAdapters)
 P_QW = ctypes.POINTER(SqQWeight)
 P_SIZE = ctypes.POINTER(c_size)
 
@@ -76,6 +83,22 @@ SIGNATURES = {
     "sq_linear_forward_codes_hadamard": (c_i32, [c_vp, c_vp, c_i64, c_i64, c_i64, P_QW, c_vp,
                                                  c_i64, c_vp, c_vp, c_vp, c_vp, c_i32, c_i64,
                                                  c_vp]),
+    "sq_group_norm_workspace_size": (c_i32, [c_i64, c_i64, c_i64, c_i32, c_i32, c_i32, P_SIZE]),
+    "sq_group_norm_act": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_i64, c_i64, c_i32, c_vp, c_vp,
+                                  ctypes.c_float, c_i32, c_vp, c_i32, c_i64, c_i64, c_vp, c_vp,
+                                  c_size, c_vp]),
+    "sq_quantize_activations_combined_norm": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_i64, c_i64,
+                                                      c_i32, c_vp, c_vp, ctypes.c_float, c_i32, P_SEG,
+                                                      c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp,
+                                                      c_size, c_vp]),
+    "sq_group_norm_act_backward": (c_i32, [c_vp, c_i64, c_i64, c_vp, c_i32, c_i64, c_i64, c_i64, c_i64,
+                                           c_i64, c_i32, c_vp, c_vp, c_vp, c_i32, c_vp, c_i64, c_i64,
+                                           c_vp, c_vp, c_vp, c_size, c_vp]),
+    "sq_adapter_add": (c_i32, [c_vp, c_i32, c_i64, c_i64, P_AD, c_vp, c_vp, c_i32, c_vp, c_i32, c_i64,
+                               c_vp, c_vp]),
+    "sq_adapter_backward_workspace_size": (c_i32, [c_i64, c_i32, P_SIZE]),
+    "sq_adapter_backward": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_vp, c_i32, c_i64, c_vp, P_AD, c_vp, c_vp,
+                                    c_i32, c_vp, c_i64, c_vp, c_vp, c_vp, c_size, c_vp]),
     "sq_stream_status": (c_i32, [c_vp]),
     "sq_status_string": (ctypes.c_char_p, [c_i32]),
     "sq_last_cuda_error": (ctypes.c_char_p, []),

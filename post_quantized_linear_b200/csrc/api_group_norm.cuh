@@ -1,0 +1,307 @@
+// Host side of the group norm entry points: argument checks, the choice of
+// tiles, and launches.  Included by segquant.cu behind its helpers.
+#pragma once
+
+namespace {
+
+// How a [B, S, C] map is cut.  cluster = true: a cluster of cs CTAs holds the
+// slab of an image and channel block in registers, nv vectors per thread.
+struct NormPlan {
+  sq::NormTile t;
+  int cs, nv, tiles;
+  bool cluster;
+  int threads_vn;
+};
+
+int gcd_i(int a, int b) { return b == 0 ? a : gcd_i(b, a % b); }
+
+// The largest block of channels a CTA's threads span, in 16-byte vectors.
+constexpr int kNormMaxVectors = sq::kNormThreads;
+
+// Chooses the tiles of `tensors` read (1 forward: x; 2 backward: x and dy).
+sq_status norm_plan(int64_t B, int64_t S, int64_t C, int32_t groups, int es, int tensors, NormPlan* out) {
+  const int vn = 16 / es;
+  const int cpg = (int)(C / groups);
+  const int unit = vn / gcd_i(vn, cpg);                 // groups in whole vectors
+  const int64_t unit_vec = (int64_t)unit * cpg / vn;
+  if (unit_vec > kNormMaxVectors) return SQ_ERR_UNSUPPORTED;
+  const int blocks_all = groups / unit;                 // C is a multiple of the vector
+  const int sms = num_sms();
+  NormPlan best = {};
+  double best_us = 1e30;
+  const int max_nv = tensors == 1 ? 16 : 8;
+  for (int m = 1; m <= blocks_all; ++m) {
+    if (blocks_all % m != 0) continue;
+    const int64_t vx = unit_vec * m;
+    if (vx > kNormMaxVectors / 2) break;
+    const int ty = (int)(sq::kNormThreads / vx);
+    for (int cs = 1; cs <= 8; cs *= 2) {
+      const int64_t rows = (S + cs - 1) / cs;
+      const int64_t need = (rows + ty - 1) / ty;
+      if (need > max_nv) continue;
+      if (cs > 1 && (int64_t)(cs - 1) * rows >= S) continue;   // a CTA without rows
+      int nv = 1;
+      while (nv < need) nv *= 2;
+      // Estimated time: waves of resident CTAs, each the latency of its loads,
+      // reductions and stores (2 us, measured at the smallest maps) and of the
+      // cluster barriers, plus its traffic at an SM's share of the copy rate
+      // (44 KB/us); narrow blocks waste part of the 32-byte sectors.
+      const int res = tensors == 1 && nv <= 4 ? 2 : 1;
+      const int64_t ctas = B * (blocks_all / m) * cs;
+      const int64_t waves = (ctas + (int64_t)sms * res - 1) / ((int64_t)sms * res);
+      const double on_sm = (double)std::min<int64_t>(res, (ctas + sms - 1) / sms);
+      const int chunk = (int)vx * 16;
+      const double waste = chunk % 32 == 0 || chunk >= C * es ? 1.0 : (double)((chunk + 31) / 32 * 32 + 16) / chunk;
+      const double kb = (double)rows * chunk * (tensors + 1) / 1024.0 * waste;
+      const double us = (double)waves * (2.0 + (cs > 1 ? 0.5 : 0.0) + on_sm * kb / 44.0);
+      if (us < best_us) {
+        best_us = us;
+        best.t = sq::NormTile{(int32_t)S, (int32_t)C, groups, cpg, unit * m, (int32_t)vx, ty, (int32_t)rows};
+        best.cs = cs;
+        best.nv = nv;
+        best.tiles = 1;
+        best.cluster = true;
+      }
+    }
+  }
+  // Two passes read the inputs twice, the second time mostly from L2, in two
+  // launches (measured: 3 us apart, 0.6 of the copy rate over all traffic).
+  const double total_kb = (double)B * S * C * es / 1024.0;
+  const double two_us = 8.0 + total_kb * (2 * tensors + 1) / (44.0 * sms);
+  if (best_us <= two_us) {
+    *out = best;
+    return SQ_OK;
+  }
+  NormPlan p = {};
+  int m = 1;
+  for (int k = 1; k <= blocks_all; ++k)
+    if (blocks_all % k == 0 && unit_vec * k <= kNormMaxVectors) m = k;
+  const int vx = (int)(unit_vec * m), ty = sq::kNormThreads / vx;
+  const int64_t cols = (int64_t)B * (blocks_all / m);
+  // about four CTAs per SM, each a whole number of thread rows
+  int64_t tiles = std::max<int64_t>(1, (4 * (int64_t)sms + cols - 1) / cols);
+  int64_t rows = (S + tiles - 1) / tiles;
+  rows = (rows + ty - 1) / ty * ty;
+  tiles = (S + rows - 1) / rows;
+  p.t = sq::NormTile{(int32_t)S, (int32_t)C, groups, cpg, unit * m, vx, ty, (int32_t)rows};
+  p.tiles = (int)tiles;
+  p.cs = 1;
+  p.cluster = false;
+  *out = p;
+  return SQ_OK;
+}
+
+sq_status norm_sizes(int64_t B, int64_t S, int64_t C, int32_t groups, sq_dtype xt) {
+  if (!dtype_ok(xt) || B < 0 || S < 0 || C <= 0 || groups <= 0 || C % groups != 0) return SQ_ERR_INVALID_ARG;
+  if (C % 8 != 0) return SQ_ERR_UNSUPPORTED;
+  if (C > SQ_MAX_K || B > 65535 || S > (1 << 30)) return SQ_ERR_RANGE;
+  return SQ_OK;
+}
+
+// A channels-last map: positions ld apart, images bs apart, 16-byte vectors.
+sq_status norm_map(const void* p, int es, int64_t B, int64_t S, int64_t C, int64_t ld, int64_t bs) {
+  if (p == nullptr || ld < C || (B > 1 && bs < 0)) return SQ_ERR_INVALID_ARG;
+  (void)S;
+  if (!aligned16(p) || (ld * es) % 16 != 0 || (B > 1 && (bs * es) % 16 != 0)) return SQ_ERR_ALIGNMENT;
+  return SQ_OK;
+}
+
+template <auto KERN, typename... Args>
+sq_status launch_grid(dim3 grid, int threads, int smem, int cluster, bool dependent, cudaStream_t stream,
+                      Args... args) {
+  if (smem > 48 * 1024) {
+    cudaError_t e = smem_limit<KERN>(200 * 1024);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (dependent) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cuda_status(cudaLaunchKernelEx(&cfg, KERN, args...));
+}
+
+template <typename XT>
+sq_status norm_forward(const NormPlan& pl, int64_t B, sq::NormArgs& a, cudaStream_t s) {
+  constexpr int vn = sq::Vec<XT>::n;
+  const int smem = 4 * sq::norm_smem_floats(pl.t.vx, vn, pl.t.nb);
+  const unsigned cblocks = (unsigned)(pl.t.G / pl.t.nb);
+  a.t = pl.t;
+  a.tiles = pl.tiles;
+  if (pl.cluster) {
+    const dim3 grid(cblocks * (unsigned)pl.cs, (unsigned)B);
+    switch (pl.nv) {
+      case 1: return launch_grid<sq::group_norm_cluster_kernel<XT, 1>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs);
+      case 2: return launch_grid<sq::group_norm_cluster_kernel<XT, 2>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs);
+      case 4: return launch_grid<sq::group_norm_cluster_kernel<XT, 4>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs);
+      case 8: return launch_grid<sq::group_norm_cluster_kernel<XT, 8>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs);
+      default: return launch_grid<sq::group_norm_cluster_kernel<XT, 16>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs);
+    }
+  }
+  const dim3 grid((unsigned)pl.tiles, cblocks, (unsigned)B);
+  sq_status st = launch_grid<sq::group_norm_stats_kernel<XT>>(grid, sq::kNormThreads, smem, 1, false, s, a);
+  if (st != SQ_OK) return st;
+  return launch_grid<sq::group_norm_apply_kernel<XT>>(grid, sq::kNormThreads, 8 * pl.t.nb, 1, false, s, a);
+}
+
+template <typename XT>
+sq_status norm_backward(const NormPlan& pl, int64_t B, sq::NormBwdArgs& a, float* dgamma, float* dbeta,
+                        cudaStream_t s) {
+  constexpr int vn = sq::Vec<XT>::n;
+  const int smem = 4 * sq::norm_smem_floats(pl.t.vx, vn, pl.t.nb);
+  const unsigned cblocks = (unsigned)(pl.t.G / pl.t.nb);
+  a.t = pl.t;
+  a.tiles = pl.tiles;
+  sq_status st;
+  if (pl.cluster) {
+    const dim3 grid(cblocks * (unsigned)pl.cs, (unsigned)B);
+    switch (pl.nv) {
+      case 1: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 1>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs); break;
+      case 2: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 2>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs); break;
+      case 4: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 4>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs); break;
+      default: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 8>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs); break;
+    }
+  } else {
+    const dim3 grid((unsigned)pl.tiles, cblocks, (unsigned)B);
+    st = launch_grid<sq::group_norm_bwd_sums_kernel<XT>>(grid, sq::kNormThreads, smem, 1, false, s, a);
+    if (st != SQ_OK) return st;
+    st = launch_grid<sq::group_norm_bwd_apply_kernel<XT>>(grid, sq::kNormThreads, 8 * (pl.t.vx * vn + pl.t.nb), 1, false, s, a);
+  }
+  if (st != SQ_OK || (dgamma == nullptr && dbeta == nullptr)) return st;
+  return launch_grid<sq::group_norm_bwd_params_kernel>(dim3((unsigned)((a.t.C + 127) / 128)), 128, 0, 1, false, s,
+                                                       (const float*)a.part, (int32_t)(B * pl.tiles), a.t.C, dgamma,
+                                                       dbeta);
+}
+
+sq_status group_norm_forward(const void* x, sq_dtype xt, int64_t B, int64_t S, int64_t C, int64_t ldx, int64_t xbs,
+                             int32_t groups, const float* gamma, const float* beta, float eps, int act, void* y,
+                             sq_dtype yt, int64_t ldy, int64_t ybs, const sq_segments* kseg, const float* s_pos,
+                             const float* s_neg, int8_t* codes, int64_t ldc, float* stats, void* workspace,
+                             size_t workspace_bytes, sq_stream_t stream) {
+  sq_status st = norm_sizes(B, S, C, groups, xt);
+  if (st != SQ_OK) return st;
+  if (act < 0 || act > 2 || !(eps >= 0.0f)) return SQ_ERR_INVALID_ARG;
+  sq::NormArgs a = {};
+  if (codes != nullptr) {
+    if (s_pos == nullptr || s_neg == nullptr || ldc < C) return SQ_ERR_INVALID_ARG;
+    st = check_segments(kseg, C, SQ_MAX_SEGMENTS, 128, &a.kseg);
+    if (st != SQ_OK) return st;
+    if (C % 16 != 0) return SQ_ERR_UNSUPPORTED;
+    if (!aligned16(codes) || ldc % 16 != 0) return SQ_ERR_ALIGNMENT;
+  }
+  if (y != nullptr && !dtype_ok(yt)) return SQ_ERR_INVALID_ARG;
+  NormPlan pl;
+  st = norm_plan(std::max<int64_t>(B, 1), std::max<int64_t>(S, 1), C, groups, elt_size(xt), 1, &pl);
+  if (st != SQ_OK) return st;
+  if (B == 0 || S == 0) return SQ_OK;
+  st = norm_map(x, elt_size(xt), B, S, C, ldx, xbs);
+  if (st != SQ_OK) return st;
+  if (y != nullptr) {
+    st = norm_map(y, elt_size(yt), B, S, C, ldy, ybs);
+    if (st != SQ_OK) return st;
+  }
+  if (!pl.cluster) {
+    if (workspace == nullptr || workspace_bytes < sizeof(float2) * (size_t)B * pl.tiles * groups)
+      return SQ_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return SQ_ERR_ALIGNMENT;
+  }
+  a.x = x; a.ldx = ldx; a.xbs = B > 1 ? xbs : 0;
+  a.y = y; a.ldy = ldy; a.ybs = B > 1 ? ybs : 0; a.y_bf16 = yt == SQ_BF16;
+  a.codes = codes; a.ldc = ldc; a.s_pos = s_pos; a.s_neg = s_neg;
+  a.gamma = gamma; a.beta = beta; a.eps = eps; a.act = act; a.stats = stats;
+  a.part = static_cast<float2*>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return xt == SQ_BF16 ? norm_forward<__nv_bfloat16>(pl, B, a, s) : norm_forward<float>(pl, B, a, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+sq_status sq_group_norm_workspace_size(int64_t B, int64_t S, int64_t C, int32_t groups, sq_dtype xt,
+                                       int32_t backward, size_t* bytes) {
+  if (bytes == nullptr) return SQ_ERR_INVALID_ARG;
+  *bytes = 0;
+  sq_status st = norm_sizes(B, S, C, groups, xt);
+  if (st != SQ_OK) return st;
+  NormPlan pl;
+  st = norm_plan(std::max<int64_t>(B, 1), std::max<int64_t>(S, 1), C, groups, elt_size(xt), backward ? 2 : 1, &pl);
+  if (st != SQ_OK || B == 0 || S == 0) return st;
+  if (backward) *bytes = sizeof(float) * 2 * (size_t)B * pl.tiles * (size_t)C;
+  else if (!pl.cluster) *bytes = sizeof(float2) * (size_t)B * pl.tiles * (size_t)groups;
+  return SQ_OK;
+}
+
+sq_status sq_group_norm_act(const void* x, sq_dtype xt, int64_t B, int64_t S, int64_t C, int64_t ldx, int64_t xbs,
+                            int32_t groups, const float* gamma, const float* beta, float eps, int32_t act, void* y,
+                            sq_dtype yt, int64_t ldy, int64_t ybs, float* stats, void* workspace,
+                            size_t workspace_bytes, sq_stream_t stream) {
+  if (y == nullptr && B > 0 && S > 0) return SQ_ERR_INVALID_ARG;
+  if (!dtype_ok(yt)) return SQ_ERR_INVALID_ARG;
+  return group_norm_forward(x, xt, B, S, C, ldx, xbs, groups, gamma, beta, eps, act, y, yt, ldy, ybs, nullptr,
+                            nullptr, nullptr, nullptr, 0, stats, workspace, workspace_bytes, stream);
+}
+
+sq_status sq_quantize_activations_combined_norm(const void* x, sq_dtype xt, int64_t B, int64_t S, int64_t C,
+                                                int64_t ldx, int64_t xbs, int32_t groups, const float* gamma,
+                                                const float* beta, float eps, int32_t act, const sq_segments* kseg,
+                                                const float* s_pos, const float* s_neg, int8_t* c, int64_t ldc,
+                                                void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                                                sq_stream_t stream) {
+  if (c == nullptr) return SQ_ERR_INVALID_ARG;
+  return group_norm_forward(x, xt, B, S, C, ldx, xbs, groups, gamma, beta, eps, act, y, SQ_BF16, ldy, S * ldy, kseg,
+                            s_pos, s_neg, c, ldc, nullptr, workspace, workspace_bytes, stream);
+}
+
+sq_status sq_group_norm_act_backward(const void* dy, int64_t lddy, int64_t dybs, const void* x, sq_dtype xt,
+                                     int64_t B, int64_t S, int64_t C, int64_t ldx, int64_t xbs, int32_t groups,
+                                     const float* stats, const float* gamma, const float* beta, int32_t act,
+                                     void* dx, int64_t lddx, int64_t dxbs, float* dgamma, float* dbeta,
+                                     void* workspace, size_t workspace_bytes, sq_stream_t stream) {
+  sq_status st = norm_sizes(B, S, C, groups, xt);
+  if (st != SQ_OK) return st;
+  if (act < 0 || act > 2) return SQ_ERR_INVALID_ARG;
+  NormPlan pl;
+  const int es = elt_size(xt);
+  st = norm_plan(std::max<int64_t>(B, 1), std::max<int64_t>(S, 1), C, groups, es, 2, &pl);
+  if (st != SQ_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (B == 0 || S == 0) {   // sums over nothing
+    if (dgamma != nullptr && (st = cuda_status(cudaMemsetAsync(dgamma, 0, sizeof(float) * (size_t)C, s))) != SQ_OK)
+      return st;
+    return dbeta == nullptr ? SQ_OK : cuda_status(cudaMemsetAsync(dbeta, 0, sizeof(float) * (size_t)C, s));
+  }
+  if (stats == nullptr) return SQ_ERR_INVALID_ARG;
+  if ((st = norm_map(x, es, B, S, C, ldx, xbs)) != SQ_OK) return st;
+  if ((st = norm_map(dy, es, B, S, C, lddy, dybs)) != SQ_OK) return st;
+  if ((st = norm_map(dx, es, B, S, C, lddx, dxbs)) != SQ_OK) return st;
+  if (workspace == nullptr || workspace_bytes < sizeof(float) * 2 * (size_t)B * pl.tiles * (size_t)C)
+    return SQ_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return SQ_ERR_ALIGNMENT;
+  sq::NormBwdArgs a = {};
+  a.x = x; a.ldx = ldx; a.xbs = B > 1 ? xbs : 0;
+  a.dy = dy; a.lddy = lddy; a.dybs = B > 1 ? dybs : 0;
+  a.dx = dx; a.lddx = lddx; a.dxbs = B > 1 ? dxbs : 0;
+  a.gamma = gamma; a.beta = beta; a.stats = stats; a.act = act;
+  a.part = static_cast<float*>(workspace);
+  return xt == SQ_BF16 ? norm_backward<__nv_bfloat16>(pl, B, a, dgamma, dbeta, s)
+                       : norm_backward<float>(pl, B, a, dgamma, dbeta, s);
+}
+
+}  // extern "C"

@@ -15,6 +15,7 @@
 
 #include "segquant.h"
 
+#include "adapters.cuh"
 #include "common.cuh"
 #include "gemm_dualscale.cuh"
 #include "gemm_dualscale_codes.cuh"
@@ -22,6 +23,7 @@
 #include "gemm_dualscale_splitk.cuh"
 #include "gemm_dualscale_inplace.cuh"
 #include "gemm_dualscale_pair.cuh"
+#include "group_norm.cuh"
 #include "ptx.cuh"
 #include "quant_kernels.cuh"
 
@@ -1673,3 +1675,6 @@ sq_status sq_stream_status(sq_stream_t stream) {
 }
 
 }  // extern "C"
+
+#include "api_group_norm.cuh"
+#include "api_adapters.cuh"

@@ -1,0 +1,277 @@
+"""Low-rank adapters of many requests beside a shared projection, and the run
+norm -> codes -> quantized linear -> adapters, against 64-bit definitions.
+
+Tolerances: products of bf16 values are exact in fp32; sums over K or N run in fp32
+(64 roundings of 2^-24 of the absolute terms cover chains whose roundings are
+independent).  Between the two products of a row, h (or u) is fp32; the tensor-core
+form multiplies it as a sum of bf16 parts, off by at most 2^-17 of itself for bf16
+outputs and 2^-24 for fp32 outputs.  The output's rounding: eps / 2 relative.
+"""
+import pytest
+import torch
+
+import post_quantized_linear_b200 as pq
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def half_step(t):
+    return torch.finfo(t).eps / 2
+
+
+def make(M, K, N, L, R, dtype=BF, ydtype=None, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x = rn(M, K).to(dtype)
+    y = rn(M, N).to(ydtype or dtype)
+    ad = pq.Adapters((rn(L, R, K) / K ** 0.5).to(BF), (rn(L, N, R) / R ** 0.5).to(BF),
+                     0.5 + torch.rand(L, generator=g, device="cuda"))
+    return x, y, ad, g
+
+
+def requests(lengths, index, first=0):
+    b = torch.tensor([first] + lengths, dtype=torch.int32).cumsum(0).to(torch.int32)
+    return b.cuda(), torch.tensor(index, dtype=torch.int32).cuda()
+
+
+def rows_of(bounds, index):
+    b = bounds.tolist()
+    return [(slice(b[q], b[q + 1]), l) for q, l in enumerate(index.tolist()) if l >= 0 and b[q + 1] > b[q]]
+
+
+def forward64(y, x, ad, bounds, index):
+    """(y, hidden) and bounds on the fp32 errors."""
+    out, e = y.double().clone(), torch.zeros_like(y, dtype=torch.float64)
+    R = ad.a.shape[1]
+    hid = torch.zeros(x.shape[0], R, dtype=torch.float64, device="cuda")
+    e_h = torch.zeros_like(hid)
+    part = 2.0 ** -17 if y.dtype == BF else U
+    for m, l in rows_of(bounds, index):
+        A, B, s = ad.a[l].double(), ad.b[l].double(), 1.0 if ad.scale is None else ad.scale[l].double()
+        hid[m] = x[m].double() @ A.t()
+        e_h[m] = 64 * U * (x[m].double().abs() @ A.abs().t())
+        out[m] += s * (hid[m] @ B.t())
+        e[m] = s * ((e_h[m] + (64 * U + part) * hid[m].abs()) @ B.abs().t()) + U * y[m].double().abs()
+    return (out, hid), (e, e_h)
+
+
+def backward64(dy, x, hidden, ad, bounds, index):
+    dx = torch.zeros_like(x, dtype=torch.float64)
+    da, db = torch.zeros_like(ad.a, dtype=torch.float64), torch.zeros_like(ad.b, dtype=torch.float64)
+    e_dx, e_da, e_db = torch.zeros_like(dx), torch.zeros_like(da), torch.zeros_like(db)
+    part = 2.0 ** -17 if x.dtype == BF else U
+    for m, l in rows_of(bounds, index):
+        A, B, s = ad.a[l].double(), ad.b[l].double(), 1.0 if ad.scale is None else ad.scale[l].double()
+        g, v, h = dy[m].double(), x[m].double(), hidden[m].double()
+        u = s * (g @ B)
+        e_u = 64 * U * s * (g.abs() @ B.abs())
+        dx[m] = u @ A
+        e_dx[m] = (e_u + (64 * U + part) * u.abs()) @ A.abs()
+        da[l] += u.t() @ v
+        e_da[l] += (e_u + 64 * U * u.abs()).t() @ v.abs()
+        db[l] += s * (g.t() @ h)
+        e_db[l] += 64 * U * s * (g.abs().t() @ h.abs())
+    return (dx, da, db), (e_dx, e_da, e_db)
+
+
+def check(got, ref, bound):
+    assert got.shape == ref.shape
+    tol = bound + half_step(got.dtype) * (ref.abs() + bound) + 1e-38
+    err = (got.double() - ref).abs()
+    assert torch.isfinite(got.float()).all()
+    assert (err <= tol).all(), f"worst {(err / tol).max().item():.2f} of the tolerance"
+
+
+# M, K, N, L, R, lengths, index, first row
+CASES = {
+    "one_row": (1, 128, 64, 1, 8, [1], [0], 0),
+    "single_rows": (37, 1152, 3456, 5, 16, [1] * 37, [(3 * i) % 5 for i in range(37)], 0),
+    "few_rows_each": (61, 768, 256, 4, 24, [3, 0, 9, 1, 17, 8, 16], [1, 2, -1, 3, 0, 0, 1], 5),
+    "one_request": (300, 512, 400, 1, 64, [300], [0], 0),
+    "ragged": (777, 1152, 2304, 3, 40, [128, 1, 0, 127, 129, 200, 31], [0, 2, 1, -1, 2, 0, 0], 100),
+    "largest_rank": (260, 272, 1040, 2, 128, [130, 130], [1, 0], 0),
+    "narrow": (200, 16, 16, 2, 8, [100, 99], [1, 1], 0),
+    "many_requests": (1500, 256, 128, 7, 32, [1, 2] * 500, [i % 8 - 1 for i in range(1000)], 0),
+    "long": (2500, 640, 1920, 2, 16, [2300, 7], [1, 0], 33),
+    "none": (40, 128, 64, 2, 8, [20, 20], [-1, -3], 0),
+}
+
+
+@pytest.mark.parametrize("dtype,ydtype", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)], ids=str)
+@pytest.mark.parametrize("case", CASES)
+def test_forward_matches_definition(case, dtype, ydtype):
+    M, K, N, L, R, lengths, index, first = CASES[case]
+    x, y, ad, _ = make(M, K, N, L, R, dtype, ydtype, seed=M)
+    bounds, idx = requests(lengths, index, first)
+    (ref, hid), (e, e_h) = forward64(y, x, ad, bounds, idx)
+    before = y.clone()
+    out, hidden = pq.adapter_add(y, x, ad, bounds, idx, return_hidden=True)
+    assert out is y
+    check(y, ref, e)
+    check(hidden, hid, e_h)
+    untouched = torch.ones(M, dtype=torch.bool, device="cuda")
+    for m, _ in rows_of(bounds, idx):
+        untouched[m] = False
+    assert torch.equal(y[untouched], before[untouched])
+    again = pq.adapter_add(before, x, ad, bounds, idx)
+    assert torch.equal(again, y)
+    assert pq.stream_status() == 0
+
+
+@pytest.mark.parametrize("dtype,dydtype", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)], ids=str)
+@pytest.mark.parametrize("case", CASES)
+def test_gradients_match_the_formula(case, dtype, dydtype):
+    M, K, N, L, R, lengths, index, first = CASES[case]
+    x, dy, ad, _ = make(M, K, N, L, R, dtype, dydtype, seed=M + 1)
+    bounds, idx = requests(lengths, index, first)
+    _, hidden = pq.adapter_add(torch.zeros_like(dy), x, ad, bounds, idx, return_hidden=True)
+    got = pq.adapter_backward(dy, x, hidden, ad, bounds, idx)
+    want, e = backward64(dy, x, hidden, ad, bounds, idx)
+    for a, b, c in zip(got, want, e):
+        check(a, b, c)
+    again = pq.adapter_backward(dy, x, hidden, ad, bounds, idx)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    assert pq.stream_status() == 0
+
+
+def test_gradients_match_differences():
+    """Central differences of the 64-bit term: exact but for roundings, the term is linear
+    in each argument; the kernel's fp32 sums are off by about 1e-6 of the terms."""
+    x, dy, ad, g = make(90, 128, 96, 2, 16, F32, F32, seed=4)
+    bounds, idx = requests([40, 30, 20], [1, 0, 1])
+    zero = torch.zeros_like(dy)
+    _, hidden = pq.adapter_add(zero.clone(), x, ad, bounds, idx, return_hidden=True)
+    grads = pq.adapter_backward(dy, x, hidden, ad, bounds, idx)
+
+    def f(x, a, b):
+        t = pq.Adapters(ad.a, ad.b, ad.scale)
+        t.a, t.b = a, b
+        return (forward64(zero, x, t, bounds, idx)[0][0] * dy.double()).sum()
+
+    at = [x.double(), ad.a.double(), ad.b.double()]
+    for i in range(3):
+        v = torch.randn(at[i].shape, generator=g, device="cuda", dtype=torch.float64)
+        lo, hi = list(at), list(at)
+        lo[i], hi[i] = at[i] - 0.5 * v, at[i] + 0.5 * v
+        want = (f(*hi) - f(*lo)).item()
+        terms = (grads[i].double() * v).abs().sum().item()
+        assert abs((grads[i].double() * v).sum().item() - want) <= 1e-5 * terms
+
+
+def test_column_slices_strides_and_no_scale():
+    """A fused q | k | v output with adapters of its own per part, in a padded buffer."""
+    x0, y0, ad, g = make(150, 272, 3 * 128 + 16, 2, 16, seed=8)
+    x, y = x0[:, 8:264], y0[:, 8:392]
+    bounds, idx = requests([70, 5, 70], [0, 1, 1], 2)
+    parts = [pq.Adapters(ad.a[:, :, i * 8:i * 8 + 256].contiguous(), ad.b[:, 128 * i:128 * i + 128].contiguous())
+             for i in range(2)]
+    want = y0.double().clone()
+    err = torch.zeros_like(want)
+    for i, p in enumerate(parts):
+        cols = slice(8 + 128 * i, 8 + 128 * i + 128)
+        (want[:, cols], _), (err[:, cols], _) = forward64(y0[:, cols], x, p, bounds, idx)
+    for i, p in enumerate(parts):
+        pq.adapter_add(y[:, 128 * i:128 * i + 128], x, p, bounds, idx)
+    check(y0, want, err)
+
+
+def test_non_finite_rows_of_other_requests():
+    """Infinities and NaN in rows of no request, or of another one, reach nothing else."""
+    for lengths in ([60, 100, 90], [1, 1, 1]):
+        M = sum(lengths) + 6
+        x, y, ad, g = make(M, 256, 192, 3, 16, seed=6)
+        dy = torch.randn(M, 192, generator=g, device="cuda").to(BF)
+        bounds, idx = requests(lengths, [0, 1, 2], 3)
+        b = bounds.tolist()
+        y2, want_h = pq.adapter_add(y.clone(), x, ad, bounds, idx, return_hidden=True)
+        want_g = pq.adapter_backward(dy, x, want_h, ad, bounds, idx)
+        bad = torch.zeros(M, dtype=torch.bool, device="cuda")
+        bad[:b[0]] = bad[b[3]:] = bad[b[1]:b[2]] = True
+        xb, dyb = x.clone(), dy.clone()
+        xb[bad], dyb[bad] = float("nan"), float("inf")
+        yb, hb = pq.adapter_add(y.clone(), xb, ad, bounds, idx, return_hidden=True)
+        assert torch.equal(yb[~bad], y2[~bad]) and torch.equal(hb[~bad], want_h[~bad])
+        assert torch.equal(yb[:b[0]], y[:b[0]]) and torch.equal(yb[b[3]:], y[b[3]:])
+        dx, da, db = pq.adapter_backward(dyb, xb, hb, ad, bounds, idx)
+        assert torch.equal(dx[~bad], want_g[0][~bad])
+        for l in (0, 2):
+            assert torch.equal(da[l], want_g[1][l]) and torch.equal(db[l], want_g[2][l])
+
+
+def test_bad_requests_are_left_out_and_reported():
+    """Bounds outside the batch and an unknown adapter: the kernels' own checks leave those
+    requests out and raise the range status; falling bounds raise it, and which rows of
+    the batch then receive their term is not specified."""
+    x, y, ad, _ = make(100, 128, 64, 2, 8, seed=2)
+    for b, i in (([0, 50, 300], [0, 1]), ([0, 50, 100], [0, 2]), ([0, 50, 20, 100], [0, 1, -1])):
+        bounds, idx = torch.tensor(b, dtype=torch.int32).cuda(), torch.tensor(i, dtype=torch.int32).cuda()
+        good = slice(0, 50)
+        (ref, _), (e, _) = forward64(y[good], x[good], ad, bounds[:2], idx[:1])
+        out = pq.adapter_add(y.clone(), x, ad, bounds, idx)
+        if b == sorted(b):
+            check(out[good], ref, e)
+            assert torch.equal(out[50:], y[50:])
+        assert pq.stream_status() == pq._lib.SQ_ERR_RANGE
+    assert pq.stream_status() == 0
+
+
+def test_empty_batches():
+    x, y, ad, _ = make(20, 128, 64, 2, 8)
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    start = torch.zeros(1, dtype=torch.int32, device="cuda")
+    before = y.clone()
+    _, h = pq.adapter_add(y, x, ad, start, none, return_hidden=True)
+    assert torch.equal(y, before) and (h == 0).all()
+    dx, da, db = pq.adapter_backward(y, x, h, ad, start, none)
+    assert (dx == 0).all() and (da == 0).all() and (db == 0).all()
+    pq.adapter_add(y[:0], x[:0], ad, start, none)
+    dx, da, db = pq.adapter_backward(y[:0], x[:0], h[:0], ad, start, none)
+    assert dx.shape == (0, 128) and (da == 0).all() and (db == 0).all()
+
+
+def test_graph_replays_with_new_requests():
+    x, y, ad, _ = make(400, 256, 320, 3, 16, seed=12)
+    plans = [requests([100, 300], [0, 2]), requests([399, 1], [1, 1]), requests([0, 0], [0, 0])]
+    bounds, idx = plans[0][0].clone(), plans[0][1].clone()
+    y1, ys = y.clone(), torch.empty_like(y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ys.copy_(y1)
+        _, h = pq.adapter_add(ys, x, ad, bounds, idx, return_hidden=True)
+        gr = pq.adapter_backward(y1, x, h, ad, bounds, idx)
+    for b, i in plans:
+        bounds.copy_(b)
+        idx.copy_(i)
+        graph.replay()
+        want, h2 = pq.adapter_add(y.clone(), x, ad, b, i, return_hidden=True)
+        assert torch.equal(ys, want) and torch.equal(h, h2)
+        assert all(torch.equal(a, c) for a, c in zip(gr, pq.adapter_backward(y, x, h2, ad, b, i)))
+
+
+@pytest.mark.parametrize("B,S,C,N,act", [(2, 256, 1152, 1152, "none"), (3, 33, 256, 400, "silu")])
+def test_norm_codes_linear_adapters_run(B, S, C, N, act):
+    """The run a block makes: norm to codes and bf16 rows, the quantized linear, adapters.
+    Each step equals the separate calls bit for bit; the whole is the 64-bit value of the
+    layer on the codes plus the term."""
+    g = torch.Generator(device="cuda").manual_seed(B)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, gamma, beta = (2 * rn(B, S, C) + 0.5).to(BF), 1 + 0.1 * rn(C), 0.1 * rn(C)
+    M, R = B * S, 16
+    qw = pq.quantize_weights(0.02 * rn(N, C), (0, C))
+    ad = pq.Adapters((rn(2, R, C) / C ** 0.5).to(BF), (rn(2, N, R) / R ** 0.5).to(BF))
+    bounds, idx = requests([S] * B, [i % 2 for i in range(B)])
+    y16 = pq.group_norm_act(x, 32, gamma, beta, act=act).view(M, C)
+    sp, sn = pq.calibrate(y16, (0, C))
+    codes, rows = pq.quantize_activations_combined_norm(x, 32, gamma, beta, (0, C), sp, sn, act=act, return_y=True)
+    base = pq.linear_from_combined(codes, qw, sp, sn)
+    assert torch.equal(base, pq.linear(y16, qw, sp, sn))
+    (want, _), (e, _) = forward64(base, rows, ad, bounds, idx)
+    check(pq.adapter_add(base, rows, ad, bounds, idx), want, e)
+    # base rounded, the sum rounded: two half steps of the layer's 64-bit value
+    q = codes.double()
+    full = torch.where(q >= 0, q * sp.double(), q * sn.double()) @ (qw.codes.double() * qw.scales[0].double()[:, None]).t()
+    (ref, _), (e2, _) = forward64(full, rows, ad, bounds, idx)
+    mag = q.abs() @ (qw.codes.double().abs() * qw.scales[0].double()[:, None]).t() * max(sp.item(), sn.item())
+    check(base, ref, e2 + e + half_step(BF) * full.abs() + 1e-6 * mag)
