@@ -1,0 +1,685 @@
+// Tensor-core forms of the adapter kernels (adapters.cuh has the formulas, the
+// pieces of requests and the forms for few rows): 128 rows of a request per
+// cluster of CTAs, bf16 operands, both products of the low-rank term in one
+// kernel, and the adapters' gradients.
+//
+// The terms are bound by memory: x is read once and y read and written once,
+// R/2 multiply-adds per byte.  So every byte moves by TMA through one ring that
+// runs from the first product's tiles into the second's without a break, and h
+// (or u) never leaves the chip between them.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "adapters.cuh"
+#include "common.cuh"
+#include "gemm_dualscale.cuh"
+#include "ptx.cuh"
+
+namespace sq {
+
+// Shared-memory matrix descriptor of an MN-major operand in the 128-byte
+// swizzle layout: atoms of 64 elements along M or N (128 bytes) by 8 along K,
+// 1024 bytes from one group of 8 along K to the next, `lbo` bytes from one
+// atom along M or N to the next.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;   // operand is MN-major
+
+__device__ __forceinline__ float4 dsmem_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+constexpr int kTileRows = 128;
+constexpr int kTileThreads = 320;          // TMA warp, MMA warp, eight epilogue warps
+constexpr int kTileEpiWarps = 8;
+constexpr int kTileX = kTileRows * 128;    // bytes of a 128-row, 128-byte-wide tile
+constexpr int kTileBars = 256;             // bytes of barriers and flags
+
+struct AdapterTileArgs {
+  AdapterArgs p;
+  int32_t cs;          // CTAs per cluster
+  int32_t stages;      // ring slots
+  int32_t slot_bytes;  // kTileX + the weight tile
+  int32_t parts;       // bf16 parts that h is multiplied as
+  long long wait_budget;
+  int32_t starve;
+};
+
+// Shared memory between the two products: this CTA's partial h in fp32 (rows
+// padded by 16 bytes), then h as `parts` bf16 operand tiles.
+__host__ __device__ inline int adapter_h_bytes(int rp, int parts, int cs) {
+  const int op = parts * kTileX * ((rp + 63) / 64);
+  const int ex = cs > 1 ? kTileRows * (rp + 4) * 4 : 0;
+  return ((op > ex ? op : ex) + 1023) / 1024 * 1024;
+}
+
+// Forward (BWD = false): h = x A^T over this CTA's share of K; the shares are
+// added over the cluster in rank order; y += scale h B^T over this CTA's share
+// of the columns, in tiles 128 bytes wide.  Backward: u = scale dy B, dx = u A, the
+// same steps with both weights MN-major.  RB: the largest rank (64 or 128).
+//
+// h is fp32 in TMEM; as an operand it is the sum of `parts` bf16 values (two for
+// bf16 outputs: off by 2^-17 of h, against the output's own 2^-8; three for fp32
+// outputs: exact to 2^-24), which costs R/2 more multiply-adds per output and no
+// bytes.
+template <int RB, typename YT, bool BWD>
+__global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
+    adapter_tile_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw1,
+                        const __grid_constant__ CUtensorMap tw2, const __grid_constant__ CUtensorMap ty,
+                        const __grid_constant__ AdapterTileArgs args) {
+  constexpr int ES = sizeof(YT);
+  constexpr int BN = 128 / ES;             // columns of an output tile
+  constexpr int D2 = 128;                  // TMEM column of the output accumulators
+  const AdapterArgs& p = args.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int cs = args.cs, NS = args.stages;
+  const int rank = blockIdx.x % cs;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0) check_requests(p, kTileThreads);
+  const AdapterItem it = adapter_item(p, blockIdx.x / cs, kTileRows);
+  const int D = BWD ? p.N : p.K, E = BWD ? p.K : p.N, R = p.R;
+  const int etiles = (E + BN - 1) / BN;
+  const int t0 = (int)((int64_t)rank * etiles / cs), t1 = (int)((int64_t)(rank + 1) * etiles / cs);
+  if (it.n == 0 || it.l < 0) {             // the same for every CTA of the cluster
+    if (BWD) {
+      const int c0 = t0 * BN, w = (min(E, t1 * BN) - c0) * ES / 16;
+      for (int m = warp; m < it.n; m += kTileThreads / 32) {
+        uint4* d = reinterpret_cast<uint4*>(static_cast<YT*>(p.y) + (int64_t)(it.row + m) * p.ldy + c0);
+        for (int i = lane; i < w; i += 32) d[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    } else if (p.h != nullptr && rank == 0) {
+      for (int i = threadIdx.x; i < it.n * R; i += kTileThreads) p.h[(int64_t)it.row * R + i] = 0.0f;
+    }
+    return;
+  }
+  const int RP = (R + 15) & ~15, rt = (RP + 63) / 64;
+  uint8_t* hbuf = smem + NS * args.slot_bytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(hbuf + adapter_h_bytes(RP, args.parts, cs));
+  uint64_t* full = bars;             // [4]
+  uint64_t* empty1 = full + 4;       // [4] slot free after a tile of the first product
+  uint64_t* empty3 = empty1 + 4;     // [4] slot free after a tile of the second
+  uint64_t* d_full = empty3 + 4;     // [2]
+  uint64_t* d_empty = d_full + 2;    // [2]
+  uint64_t* h_full = d_empty + 2;
+  uint64_t* h_ready = h_full + 1;
+  uint64_t* p_full = h_ready + 1;    // every CTA's partial h is written
+  uint64_t* p_free = p_full + 1;     // every CTA has read this one's
+  uint64_t* drain_bar = p_free + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const long long budget = args.wait_budget;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(smem_u32(full + i), 1);
+      mbar_init(smem_u32(empty1 + i), 1);
+      mbar_init(smem_u32(empty3 + i), kTileEpiWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(d_full + i), 1);
+      mbar_init(smem_u32(d_empty + i), kTileEpiWarps);
+    }
+    mbar_init(smem_u32(h_full), 1);
+    mbar_init(smem_u32(h_ready), kTileEpiWarps);
+    mbar_init(smem_u32(p_full), kTileEpiWarps * cs);
+    mbar_init(smem_u32(p_free), kTileEpiWarps * cs);
+    mbar_init(smem_u32(drain_bar), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (cs > 1) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int nkb = (D + 63) / 64;
+  const int kb0 = (int)((int64_t)rank * nkb / cs), kb1 = (int)((int64_t)(rank + 1) * nkb / cs);
+  const int nk = kb1 - kb0, nt = t1 - t0;
+  const int boxes = (it.n + 31) / 32;      // 32-row boxes that hold rows of the piece
+
+  if (warp == 0) {
+    // -------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tx);
+      tma_prefetch_desc(&tw1);
+      tma_prefetch_desc(&tw2);
+      if (!BWD) tma_prefetch_desc(&ty);
+      bool ok = args.starve == 0;
+      int i = 0;
+      for (; i < nk + nt && ok; ++i) {
+        const int s = i % NS, prev = i - NS;
+        if (prev >= 0) {
+          if (prev < nk) {
+            ok = wait1(smem_u32(empty1 + s), (prev / NS) & 1, abort_flag, budget);
+          } else {
+            const int first = nk + ((s - nk % NS) + NS) % NS;   // first tile of the second product in slot s
+            ok = wait1(smem_u32(empty3 + s), ((prev - first) / NS) & 1, abort_flag, budget);
+          }
+          if (!ok) break;
+        }
+        const uint32_t st = smem_u32(smem + s * args.slot_bytes), wt = st + kTileX, bar = smem_u32(full + s);
+        if (i < nk) {
+          const int k = (kb0 + i) * 64;
+          mbar_arrive_expect_tx(bar, boxes * 4096 + (BWD ? rt * 8192 : R * 128));
+          for (int b = 0; b < boxes; ++b) tma_load_2d(st + b * 4096, &tx, bar, k, it.row + 32 * b);
+          if (BWD) {
+            for (int t = 0; t < rt; ++t) tma_load_3d(wt + t * 8192, &tw1, bar, 64 * t, k, it.l);
+          } else {
+            tma_load_3d(wt, &tw1, bar, k, 0, it.l);
+          }
+        } else {
+          const int c = (t0 + i - nk) * BN;
+          mbar_arrive_expect_tx(bar, BWD ? RP * 128 : boxes * 4096 + rt * BN * 128);
+          if (BWD) {
+            tma_load_3d(wt, &tw2, bar, c, 0, it.l);
+          } else {
+            for (int t = 0; t < rt; ++t) tma_load_3d(wt + t * BN * 128, &tw2, bar, 64 * t, c, it.l);
+            for (int b = 0; b < boxes; ++b) tma_load_2d(st + b * 4096, &ty, bar, c, it.row + 32 * b);
+          }
+        }
+      }
+      drain_ring(full, NS, i, kDrainBudget);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      bool ok = true;
+      const uint32_t id1 = idesc_bf16(kTileRows, RP) | (BWD ? kIdescBMn : 0u);
+      for (int i = 0; i < nk; ++i) {
+        const int s = i % NS;
+        if (!(ok = wait1(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
+        const uint32_t st = smem_u32(smem + s * args.slot_bytes), wt = st + kTileX;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma_bf16(tmem, smem_desc_k_sw128(st + ks * 32),
+                    BWD ? smem_desc_mn_sw128(wt + ks * 2048, 8192) : smem_desc_k_sw128(wt + ks * 32), id1,
+                    (i > 0 || ks > 0) ? 1u : 0u);
+        umma_commit(smem_u32(empty1 + s));
+      }
+      if (ok) {
+        umma_commit(smem_u32(h_full));
+        ok = wait1(smem_u32(h_ready), 0, abort_flag, budget);
+        tc_fence_after();
+      }
+      const uint32_t id2 = idesc_bf16(kTileRows, BN) | (BWD ? kIdescBMn : 0u);
+      const uint32_t hb = smem_u32(hbuf);
+      for (int j = 0; j < nt && ok; ++j) {
+        const int i = nk + j, s = i % NS, b = j & 1;
+        if (j >= 2 && !(ok = wait1(smem_u32(d_empty + b), ((j >> 1) - 1) & 1, abort_flag, budget))) break;
+        if (!(ok = wait1(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
+        tc_fence_after();
+        const uint32_t wt = smem_u32(smem + s * args.slot_bytes) + kTileX;
+        uint32_t acc = 0;
+        for (int part = 0; part < args.parts; ++part)
+          for (int ks = 0; ks < RP / 16; ++ks) {
+            const uint32_t a = hb + (part * rt + (ks >> 2)) * kTileX + (ks & 3) * 32;
+            umma_bf16(tmem + D2 + b * BN, smem_desc_k_sw128(a),
+                      BWD ? smem_desc_mn_sw128(wt + ks * 2048, 8192)
+                          : smem_desc_k_sw128(wt + (ks >> 2) * BN * 128 + (ks & 3) * 32),
+                      id2, acc);
+            acc = 1;
+          }
+        umma_commit(smem_u32(d_full + b));
+      }
+      umma_commit(smem_u32(drain_bar));
+      wait_drain(smem_u32(drain_bar), 0, kDrainBudget);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const int row = quad * 32 + lane;
+    const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
+    const int hc = RP / 2, c0 = half * hc;    // this thread's columns of h
+    bool ok = wait_warp(smem_u32(h_full), 0, abort_flag, budget);
+    if (ok) {
+      tc_fence_after();
+      float v[RB / 2];
+#pragma unroll
+      for (int c = 0; c < RB / 2; c += 8) {
+        uint32_t u[8];
+        if (c < hc) tmem_ld8(t_lane + c0 + c, u);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[c + k] = c < hc ? __uint_as_float(u[k]) : 0.0f;
+      }
+      if (cs > 1) {
+        const int pr = RP + 4;                 // fp32 row pitch of the partial h: conflict-free 16-byte accesses
+        float* mine = reinterpret_cast<float*>(hbuf) + row * pr + c0;
+#pragma unroll
+        for (int c = 0; c < RB / 2; c += 4)
+          if (c < hc) *reinterpret_cast<float4*>(mine + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+        __syncwarp();
+        if (lane < cs) mbar_arrive_remote(mapa_shared(smem_u32(p_full), lane));
+        ok = wait_warp<true>(smem_u32(p_full), 0, abort_flag, budget);
+        if (ok) {
+#pragma unroll
+          for (int c = 0; c < RB / 2; ++c) v[c] = 0.0f;
+          for (int k = 0; k < cs; ++k) {
+            const uint32_t from = mapa_shared(smem_u32(mine), k);
+#pragma unroll
+            for (int c = 0; c < RB / 2; c += 4)
+              if (c < hc) {
+                const float4 o = dsmem_f32x4(from + 4 * c);
+                v[c] += o.x; v[c + 1] += o.y; v[c + 2] += o.z; v[c + 3] += o.w;
+              }
+          }
+          __syncwarp();
+          if (lane < cs) mbar_arrive_remote(mapa_shared(smem_u32(p_free), lane));
+          ok = wait_warp<true>(smem_u32(p_free), 0, abort_flag, budget);
+        }
+      }
+      if (ok) {
+        const float scale = p.scale != nullptr ? __ldg(p.scale + it.l) : 1.0f;
+        // each CTA of the cluster stores its share of the rows of h (u)
+        const bool keep = p.h != nullptr && row < it.n && row * cs / kTileRows == rank;
+        float* hg = p.h + (int64_t)(it.row + row) * R;
+#pragma unroll
+        for (int c = 0; c < RB / 2; c += 8) {
+          if (c < hc) {
+            const int col = c0 + c;
+            float o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float scaled = v[c + k] * scale;
+              o[k] = BWD ? scaled : v[c + k];
+              v[c + k] = col < R ? scaled : 0.0f;   // the padding of the rank is an operand, too
+            }
+            if (keep && col < R) store_vec<8>(hg, col, false, o);
+            uint8_t* d = hbuf + (col >> 6) * kTileX + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4);
+            for (int part = 0; part < args.parts; ++part) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                w[k] = pack_bf16(v[c + 2 * k], v[c + 2 * k + 1]);
+                v[c + 2 * k] -= __uint_as_float(w[k] << 16);
+                v[c + 2 * k + 1] -= __uint_as_float(w[k] & 0xFFFF0000u);
+              }
+              *reinterpret_cast<uint4*>(d + part * rt * kTileX) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        tc_fence_before();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(h_ready));
+      }
+    }
+    const int rows = min(32, it.n - quad * 32);     // rows of the piece in this quarter (may be < 1)
+    for (int j = 0; j < nt && ok; ++j) {
+      const int i = nk + j, s = i % NS, b = j & 1;
+      if (!(ok = wait_warp(smem_u32(d_full + b), (j >> 1) & 1, abort_flag, budget))) break;
+      if (!(ok = wait_warp(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
+      tc_fence_after();
+      if (rows > 0) {
+        uint8_t* tile = smem + s * args.slot_bytes + quad * 4096;
+        uint8_t* mine = tile + lane * 128;
+#pragma unroll
+        for (int g = 0; g < BN / 2; g += 16) {
+          uint32_t u[16];
+          tmem_ld16(t_lane + D2 + b * BN + half * (BN / 2) + g, u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 16 * ES / 16; ++q) {   // 16-byte chunks
+            uint4* at = reinterpret_cast<uint4*>(mine + (((half * 4 + g * ES / 16 + q) ^ (lane & 7)) << 4));
+            constexpr int PER = 16 / ES;
+            float o[PER];
+            if constexpr (!BWD) {
+              Vec<YT>::load_raw(*at, o);
+            } else {
+#pragma unroll
+              for (int k = 0; k < PER; ++k) o[k] = 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < PER; ++k) o[k] += __uint_as_float(u[q * PER + k]);
+            store_vec<PER>(at, 0, ES == 2, o);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(d_empty + b));
+        // out in rows of 64 bytes: four lanes per row
+        const int c = (t0 + j) * BN + half * (BN / 2) + (lane & 3) * (16 / ES);
+        if (c < E) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = k * 8 + (lane >> 2);
+            if (r < rows) {
+              const uint4 o = *reinterpret_cast<const uint4*>(tile + r * 128 + (((half * 4 + (lane & 3)) ^ (r & 7)) << 4));
+              *reinterpret_cast<uint4*>(static_cast<YT*>(p.y) + (int64_t)(it.row + quad * 32 + r) * p.ldy + c) = o;
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      } else if (lane == 0) {
+        mbar_arrive(smem_u32(d_empty + b));
+      }
+      if (lane == 0) mbar_arrive(smem_u32(empty3 + s));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (cs > 1) cluster_sync();      // no peer still reads this CTA's memory or signals its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// -------------------------------------------- gradients of the adapters, bf16
+// dA_l = sum u^T x and dB_l = scale sum dy^T h: 128 columns of the long axis by
+// the rank per cluster and adapter, contracted over the rows of all its requests
+// in pieces of 64, which the CTAs of the cluster take in turn; their sums are
+// added through distributed shared memory in rank order.
+// f (u or h, fp32) enters as three bf16 parts side by side along the rank axis
+// (exact to 2^-24, since the sums are fp32 results), g (x or dy) as it is.
+struct AdapterGradTileArgs {
+  const float* f[2];             // u, hidden: [M, R]
+  float* out[2];                 // da, db
+  const float* scale;            // of the second, or null
+  const int32_t* bounds;
+  const int32_t* index;
+  int32_t C[2];                  // K, N
+  int32_t tiles0;                // tiles of the first product (0: none)
+  int32_t M, R, L, Q;
+  int32_t cs, stages;
+  long long wait_budget;
+  int32_t starve;
+};
+constexpr int kGradPiece = 64;
+__host__ __device__ inline int adapter_grad_f_bytes(int rp) { return (3 * rp + 63) / 64 * 8192; }
+
+// The pieces of adapter l's requests, found by a warp together, 32 requests at a time.
+struct GradPieces {
+  int base = -32, pos = 0, end = 0, s = 0, e = 0;
+  unsigned mask = 0;
+  __device__ __forceinline__ bool next(const AdapterGradTileArgs& p, int l, int& m0, int& n) {
+    const int lane = threadIdx.x & 31;
+    while (pos >= end) {
+      while (mask == 0) {
+        base += 32;
+        if (base >= p.Q) return false;
+        const int q = base + lane;
+        bool hit = false;
+        if (q < p.Q && __ldg(p.index + q) == l) {
+          s = max(0, __ldg(p.bounds + q));
+          e = min(p.M, __ldg(p.bounds + q + 1));
+          hit = s < e;
+        }
+        mask = __ballot_sync(0xffffffffu, hit);
+      }
+      const int src = __ffs(mask) - 1;
+      mask &= mask - 1;
+      pos = __shfl_sync(0xffffffffu, s, src);
+      end = __shfl_sync(0xffffffffu, e, src);
+    }
+    m0 = pos;
+    n = min(kGradPiece, end - pos);
+    pos += kGradPiece;
+    return true;
+  }
+  // the next piece of this rank
+  int turn = 0;
+  __device__ __forceinline__ bool mine(const AdapterGradTileArgs& p, int l, int rank, int& m0, int& n) {
+    while (next(p, l, m0, n)) {
+      const bool is = turn == rank;
+      turn = turn + 1 == p.cs ? 0 : turn + 1;
+      if (is) return true;
+    }
+    return false;
+  }
+};
+
+template <int RB>
+__global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
+    adapter_grad_tile_kernel(const __grid_constant__ CUtensorMap tg0, const __grid_constant__ CUtensorMap tg1,
+                             const __grid_constant__ AdapterGradTileArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int TM = RB == 64 ? 256 : 512;
+  const int cs = p.cs, NS = p.stages, R = p.R, RP = (R + 15) & ~15;
+  const int rank = blockIdx.x % cs, l = blockIdx.y;
+  int tile = blockIdx.x / cs;
+  const int which = tile < p.tiles0 ? 0 : 1;
+  if (which) tile -= p.tiles0;
+  const int C = p.C[which], c0 = tile * 128;
+  const float* f = p.f[which];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slot_bytes = kTileX + adapter_grad_f_bytes(RP);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + max(NS * slot_bytes, cs > 1 ? 128 * (RP + 4) * 4 : 0));
+  uint64_t* full = bars;           // [4] g has landed
+  uint64_t* ready = full + 4;      // [4] f's parts are written (and g's rows behind the piece cleared)
+  uint64_t* empty = ready + 4;     // [4]
+  uint64_t* d_full = empty + 4;
+  uint64_t* p_full = d_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(p_full + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const long long budget = p.wait_budget;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(smem_u32(full + i), 1);
+      mbar_init(smem_u32(ready + i), kTileEpiWarps);
+      mbar_init(smem_u32(empty + i), 1);
+    }
+    mbar_init(smem_u32(d_full), 1);
+    mbar_init(smem_u32(p_full), kTileEpiWarps * cs);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), TM);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (cs > 1) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  GradPieces pieces;
+  int m0, n, i = 0;
+  bool ok = true;
+  if (warp == 0) {
+    // -------------------------------------------------------- TMA producer
+    const CUtensorMap* tg = which ? &tg1 : &tg0;
+    if (lane == 0) tma_prefetch_desc(tg);
+    ok = p.starve == 0;
+    while (ok && pieces.mine(p, l, rank, m0, n)) {
+      const int s = i % NS;
+      if (i >= NS && !(ok = wait_warp(smem_u32(empty + s), (i / NS - 1) & 1, abort_flag, budget))) break;
+      if (lane == 0) {
+        const uint32_t st = smem_u32(smem + s * slot_bytes), bar = smem_u32(full + s);
+        mbar_arrive_expect_tx(bar, kTileX);
+        tma_load_2d(st, tg, bar, c0, m0);
+        tma_load_2d(st + 8192, tg, bar, c0 + 64, m0);
+      }
+      ++i;
+    }
+    if (lane == 0) drain_ring(full, NS, i, kDrainBudget);
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    const int cols = 3 * RP, n1 = cols > 256 ? 192 : cols, n2 = cols - n1;
+    while (ok && pieces.mine(p, l, rank, m0, n)) {
+      const int s = i % NS;
+      if (!(ok = wait_warp(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
+      if (!(ok = wait_warp(smem_u32(ready + s), (i / NS) & 1, abort_flag, budget))) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t st = smem_u32(smem + s * slot_bytes), ft = st + kTileX;
+#pragma unroll
+        for (int ks = 0; ks < kGradPiece / 16; ++ks) {
+          const uint64_t a = smem_desc_mn_sw128(st + ks * 2048, 8192);
+          umma_bf16(tmem, a, smem_desc_mn_sw128(ft + ks * 2048, 8192), idesc_bf16(128, n1) | kIdescAMn | kIdescBMn,
+                    (i > 0 || ks > 0) ? 1u : 0u);
+          if (n2 > 0)
+            umma_bf16(tmem + n1, a, smem_desc_mn_sw128(ft + 3 * 8192 + ks * 2048, 8192),
+                      idesc_bf16(128, n2) | kIdescAMn | kIdescBMn, (i > 0 || ks > 0) ? 1u : 0u);
+        }
+        umma_commit(smem_u32(empty + s));
+      }
+      __syncwarp();
+      ++i;
+    }
+    if (lane == 0) {
+      umma_commit(smem_u32(d_full));
+      wait_drain(smem_u32(d_full), 0, kDrainBudget);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------- f's parts into shared memory, then the sums
+    const int tid = threadIdx.x - 64;
+    const int vecs = R / 8, units = kGradPiece * vecs;     // 8 ranks of one row each
+    constexpr int MAXU = kGradPiece * (RB / 8) / 256;      // units per thread
+    float v[MAXU][8];
+    auto fetch = [&](int m, int cnt) {
+#pragma unroll
+      for (int k = 0; k < MAXU; ++k) {
+        const int u = tid + 256 * k, r = u / vecs, c = u % vecs;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
+        if (u < units && r < cnt) {
+          const float4* src = reinterpret_cast<const float4*>(f + (int64_t)(m + r) * R + c * 8);
+          const float4 a = __ldg(src), b = __ldg(src + 1);
+          v[k][0] = a.x; v[k][1] = a.y; v[k][2] = a.z; v[k][3] = a.w;
+          v[k][4] = b.x; v[k][5] = b.y; v[k][6] = b.z; v[k][7] = b.w;
+        }
+      }
+    };
+    bool more = pieces.mine(p, l, rank, m0, n);
+    if (more) fetch(m0, n);
+    while (more) {
+      const int s = i % NS, cnt = n;
+      if (i >= NS && !(ok = wait_warp(smem_u32(empty + s), (i / NS - 1) & 1, abort_flag, budget))) break;
+      uint8_t* st = smem + s * slot_bytes;
+      uint8_t* ft = st + kTileX;
+#pragma unroll
+      for (int k = 0; k < MAXU; ++k) {
+        const int u = tid + 256 * k, r = u / vecs, c = u % vecs;
+        if (u < units) {
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              w[j] = pack_bf16(v[k][2 * j], v[k][2 * j + 1]);
+              v[k][2 * j] -= __uint_as_float(w[j] << 16);
+              v[k][2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+            const int col = part * RP + c * 8;
+            *reinterpret_cast<uint4*>(ft + (col >> 6) * 8192 + r * 128 + ((((col & 63) >> 3) ^ (r & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      more = pieces.mine(p, l, rank, m0, n);
+      if (more) fetch(m0, n);                              // in flight while this piece is handed over
+      if (cnt < kGradPiece) {
+        // rows behind the piece belong to other requests: cleared, whatever they hold
+        if (!(ok = wait_warp(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
+        for (int u = tid; u < (kGradPiece - cnt) * 16; u += 256)
+          *reinterpret_cast<uint4*>(st + (u >> 3 & 1) * 8192 + (cnt + (u >> 4)) * 128 + (u & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(ready + s));
+      ++i;
+    }
+    const int any = i;                                     // this CTA had pieces
+    if (ok) ok = wait_warp(smem_u32(d_full), 0, abort_flag, budget);
+    const int quad = warp & 3, half = (warp - 2) >> 2, row = quad * 32 + lane;
+    const int hc = RP / 2, r0 = half * hc;
+    const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
+    float t[RB / 2];
+    if (ok) {
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < RB / 2; c += 8) {
+        uint32_t a[8], b[8], d[8];
+        if (c < hc) {
+          tmem_ld8(t_lane + r0 + c, a);
+          tmem_ld8(t_lane + RP + r0 + c, b);
+          tmem_ld8(t_lane + 2 * RP + r0 + c, d);
+        }
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          t[c + k] = c < hc && any ? __uint_as_float(a[k]) + (__uint_as_float(b[k]) + __uint_as_float(d[k])) : 0.0f;
+      }
+      tc_fence_before();
+    }
+    const bool mine = cs == 1 || (quad * 2 + half) % cs == rank;
+    if (cs > 1) {
+      // the ring is idle: all copies have landed and all products are done
+      const int pr = RP + 4;
+      float* own = reinterpret_cast<float*>(smem) + row * pr + r0;
+      if (ok) {
+#pragma unroll
+        for (int c = 0; c < RB / 2; c += 4)
+          if (c < hc) *reinterpret_cast<float4*>(own + c) = make_float4(t[c], t[c + 1], t[c + 2], t[c + 3]);
+        __syncwarp();
+        if (lane < cs) mbar_arrive_remote(mapa_shared(smem_u32(p_full), lane));
+        ok = wait_warp<true>(smem_u32(p_full), 0, abort_flag, budget);
+      }
+      if (ok && mine) {
+#pragma unroll
+        for (int c = 0; c < RB / 2; ++c) t[c] = 0.0f;
+        for (int k = 0; k < cs; ++k) {
+          const uint32_t from = mapa_shared(smem_u32(own), k);
+#pragma unroll
+          for (int c = 0; c < RB / 2; c += 4)
+            if (c < hc) {
+              const float4 o = dsmem_f32x4(from + 4 * c);
+              t[c] += o.x; t[c + 1] += o.y; t[c + 2] += o.z; t[c + 3] += o.w;
+            }
+        }
+      }
+    }
+    if (ok && mine && c0 + row < C) {
+      const float scale = which && p.scale != nullptr ? __ldg(p.scale + l) : 1.0f;
+#pragma unroll
+      for (int c = 0; c < RB / 2; c += 8) {
+        if (c < hc && r0 + c < R) {
+          if (which) {
+            float o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = t[c + k] * scale;
+            store_vec<8>(p.out[1], ((int64_t)l * C + c0 + row) * R + r0 + c, false, o);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) p.out[0][((int64_t)l * R + r0 + c + k) * C + c0 + row] = t[c + k];
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (cs > 1) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TM);
+  }
+}
+
+}  // namespace sq

@@ -68,6 +68,155 @@ sq_status launch_adapter_grad(const sq::AdapterGradArgs& g, sq_dtype gt, cudaStr
   return launch_grid<sq::adapter_grad_kernel<float, TRANS>>(grid, sq::kGradThreads, 0, 1, false, s, g);
 }
 
+// A tiled map of rank 2 or 3, boxes with 128-byte swizzled rows; strides in bytes
+// for dimensions 1, 2.
+sq_status make_adapter_map(CUtensorMap* map, sq_dtype t, const void* base, int rank, uint64_t d0, uint64_t d1,
+                           uint64_t d2, uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return SQ_ERR_CUDA;
+  cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1, s2};
+  cuuint32_t box[3] = {b0, b1, 1}, estr[3] = {1, 1, 1};
+  CUresult r = fn(map, t == SQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                  (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SQ_OK : SQ_ERR_CUDA;
+}
+
+constexpr int kSmemPerSm = 227 * 1024;
+
+template <int RB, typename YT, bool BWD>
+sq_status launch_tile_rb(const sq::AdapterArgs& a, const CUtensorMap& tx, const CUtensorMap& tw1,
+                         const CUtensorMap& tw2, const CUtensorMap& ty, cudaStream_t s) {
+  constexpr auto kern = sq::adapter_tile_kernel<RB, YT, BWD>;
+  const int D = BWD ? a.N : a.K, E = BWD ? a.K : a.N;
+  const int rp = (a.R + 15) / 16 * 16;
+  sq::AdapterTileArgs t = {};
+  t.p = a;
+  t.parts = sizeof(YT) == 2 ? 2 : 3;
+  t.slot_bytes = sq::kTileX + (RB == 64 ? 8192 : 16384);
+  t.wait_budget = g_wait_budget;
+  t.starve = g_debug_starve;
+  // Pieces expected: the batch cut into 128 rows, or one per request.  The
+  // cluster grows until two CTAs per SM (one at ranks above 64) have work.
+  const int64_t pieces = std::max<int64_t>((a.M + sq::kTileRows - 1) / sq::kTileRows, std::min<int64_t>(a.Q, a.M));
+  const int64_t want = (int64_t)num_sms() * (RB == 64 ? 2 : 1);
+  const int most = std::min({8, (D + 63) / 64, (E + 128 / (int)sizeof(YT) - 1) / (128 / (int)sizeof(YT))});
+  int cs = 1;
+  while (cs * 2 <= most && pieces * cs * 2 <= want) cs *= 2;
+  t.cs = cs;
+  const int rest = sq::adapter_h_bytes(rp, t.parts, cs) + sq::kTileBars + 1024;
+  const bool two = RB == 64 && 3 * t.slot_bytes + rest <= kSmemPerSm / 2 - 1024;
+  t.stages = two ? 3 : 4 * t.slot_bytes + rest <= kSmemPerSm ? 4 : 3;
+  const int smem = t.stages * t.slot_bytes + rest;
+  cudaError_t e = smem_limit<kern>(kSmemPerSm);
+  if (e != cudaSuccess) return cuda_status(e);
+  const int64_t slots = (int64_t)a.M / sq::kTileRows + a.Q + 3;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(slots * cs));
+  cfg.blockDim = dim3(sq::kTileThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, tx, tw1, tw2, ty, t));
+}
+
+template <bool BWD>
+sq_status launch_tile(const sq::AdapterArgs& a, sq_dtype yt, cudaStream_t s) {
+  const uint64_t K = a.K, N = a.N, R = a.R, L = a.L, M = a.M;
+  const uint32_t rp = (uint32_t)((R + 15) / 16 * 16), bn = yt == SQ_BF16 ? 64 : 32;
+  CUtensorMap tx, tw1, tw2, ty;
+  sq_status st = make_adapter_map(&tx, SQ_BF16, a.x, 2, BWD ? N : K, M, 1, a.ldx * 2, 0, 64, 32);
+  if (st != SQ_OK) return st;
+  if (BWD) {
+    if ((st = make_adapter_map(&tw1, SQ_BF16, a.b, 3, R, N, L, R * 2, N * R * 2, 64, 64)) != SQ_OK) return st;
+    if ((st = make_adapter_map(&tw2, SQ_BF16, a.a, 3, K, R, L, K * 2, K * R * 2, 64, rp)) != SQ_OK) return st;
+    ty = tx;
+  } else {
+    if ((st = make_adapter_map(&tw1, SQ_BF16, a.a, 3, K, R, L, K * 2, K * R * 2, 64, (uint32_t)R)) != SQ_OK) return st;
+    if ((st = make_adapter_map(&tw2, SQ_BF16, a.b, 3, R, N, L, R * 2, N * R * 2, 64, bn)) != SQ_OK) return st;
+    if ((st = make_adapter_map(&ty, yt, a.y, 2, N, M, 1, a.ldy * elt_size(yt), 0, bn, 32)) != SQ_OK) return st;
+  }
+  if (R <= 64)
+    return yt == SQ_BF16 ? launch_tile_rb<64, __nv_bfloat16, BWD>(a, tx, tw1, tw2, ty, s)
+                         : launch_tile_rb<64, float, BWD>(a, tx, tw1, tw2, ty, s);
+  return yt == SQ_BF16 ? launch_tile_rb<128, __nv_bfloat16, BWD>(a, tx, tw1, tw2, ty, s)
+                       : launch_tile_rb<128, float, BWD>(a, tx, tw1, tw2, ty, s);
+}
+
+// The first product in bf16 tiles of 128 rows pays where requests have rows to fill
+// them; with a few rows each, and for fp32 rows, the few-rows form is taken.
+bool use_tiles(const sq::AdapterArgs& a, sq_dtype xt) {
+  return xt == SQ_BF16 && (int64_t)a.M > (int64_t)sq::kFewRows * std::max(a.Q, 1);
+}
+
+template <int RB>
+sq_status launch_grad_tile_rb(sq::AdapterGradTileArgs g, const CUtensorMap& t0, const CUtensorMap& t1, int tiles,
+                              cudaStream_t s) {
+  constexpr auto kern = sq::adapter_grad_tile_kernel<RB>;
+  const int rp = (g.R + 15) / 16 * 16;
+  const int slot = sq::kTileX + sq::adapter_grad_f_bytes(rp);
+  const int room = (RB == 64 ? kSmemPerSm / 2 - 1024 : kSmemPerSm) - sq::kTileBars - 1024;
+  g.stages = std::min(4, room / slot);
+  // the cluster shares an adapter's pieces: as many CTAs as fill the SMs twice
+  const int64_t per = std::max<int64_t>(1, (int64_t)g.M / sq::kGradPiece / std::max(1, std::min(g.L, g.Q)));
+  const int64_t ctas = (int64_t)tiles * std::min(g.L, std::max(g.Q, 1));
+  int cs = 1;
+  while (cs < 8 && cs * 2 <= per && ctas * cs * 2 <= (int64_t)num_sms() * (RB == 64 ? 4 : 2)) cs *= 2;
+  g.cs = cs;
+  // At least the share of shared memory that the CTA has of TMEM (half, or all): a CTA
+  // that is resident never waits for TMEM of another cluster's.
+  const int smem = std::max(std::max(g.stages * slot, cs > 1 ? 128 * (rp + 4) * 4 : 0) + sq::kTileBars + 1024,
+                            (RB == 64 ? kSmemPerSm / 2 : kSmemPerSm) - 4096);
+  cudaError_t e = smem_limit<kern>(kSmemPerSm);
+  if (e != cudaSuccess) return cuda_status(e);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * cs), (unsigned)g.L);
+  cfg.blockDim = dim3(sq::kTileThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, t0, t1, g));
+}
+
+// Both gradients (or the bf16 one of them) on the tensor cores.
+sq_status launch_grad_tiles(const sq::AdapterArgs& a, const float* u, const float* hidden, const void* x,
+                            int64_t ldx, const void* dy, int64_t lddy, float* da, float* db, cudaStream_t s) {
+  CUtensorMap t0, t1;
+  sq_status st;
+  if (da != nullptr &&
+      (st = make_adapter_map(&t0, SQ_BF16, x, 2, a.K, a.M, 1, ldx * 2, 0, 64, sq::kGradPiece)) != SQ_OK)
+    return st;
+  if (db != nullptr &&
+      (st = make_adapter_map(&t1, SQ_BF16, dy, 2, a.N, a.M, 1, lddy * 2, 0, 64, sq::kGradPiece)) != SQ_OK)
+    return st;
+  if (da == nullptr) t0 = t1;
+  if (db == nullptr) t1 = t0;
+  sq::AdapterGradTileArgs g = {};
+  g.f[0] = u; g.f[1] = hidden;
+  g.out[0] = da; g.out[1] = db;
+  g.scale = a.scale; g.bounds = a.bounds; g.index = a.index;
+  g.C[0] = a.K; g.C[1] = a.N;
+  g.tiles0 = da != nullptr ? (a.K + 127) / 128 : 0;
+  g.M = a.M; g.R = a.R; g.L = a.L; g.Q = a.Q;
+  g.wait_budget = g_wait_budget;
+  g.starve = g_debug_starve;
+  const int tiles = g.tiles0 + (db != nullptr ? (a.N + 127) / 128 : 0);
+  return a.R <= 64 ? launch_grad_tile_rb<64>(g, t0, t1, tiles, s) : launch_grad_tile_rb<128>(g, t0, t1, tiles, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -84,7 +233,8 @@ sq_status sq_adapter_add(const void* x, sq_dtype xt, int64_t M, int64_t ldx, con
   if (hidden != nullptr && !aligned16(hidden)) return SQ_ERR_ALIGNMENT;
   sq::AdapterArgs a = adapter_args(adapters, bounds, index, requests, M);
   a.x = x; a.ldx = ldx; a.y = y; a.ldy = ldy; a.h = hidden;
-  return launch_few_rows<false>(a, xt, yt, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return use_tiles(a, xt) ? launch_tile<false>(a, yt, s) : launch_few_rows<false>(a, xt, yt, s);
 }
 
 sq_status sq_adapter_backward_workspace_size(int64_t M, int32_t R, size_t* bytes) {
@@ -102,6 +252,8 @@ sq_status sq_adapter_backward(const void* dy, sq_dtype dyt, int64_t M, int64_t l
   if (!dtype_ok(xt) || !dtype_ok(dyt) || da == nullptr || db == nullptr) return SQ_ERR_INVALID_ARG;
   if (!aligned16(da) || !aligned16(db)) return SQ_ERR_ALIGNMENT;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  sq::AdapterArgs a = adapter_args(adapters, bounds, index, requests, M);
+  float* u = static_cast<float*>(workspace);
   if (M > 0) {
     if ((st = check_matrix(dy, dyt, adapters->N, lddy)) != SQ_OK) return st;
     if ((st = check_matrix(x, xt, adapters->K, ldx)) != SQ_OK) return st;
@@ -109,17 +261,28 @@ sq_status sq_adapter_backward(const void* dy, sq_dtype dyt, int64_t M, int64_t l
     if (hidden == nullptr || workspace == nullptr || workspace_bytes < sizeof(float) * (size_t)M * adapters->R)
       return SQ_ERR_INVALID_ARG;
     if (!aligned16(hidden) || !aligned16(workspace)) return SQ_ERR_ALIGNMENT;
-    sq::AdapterArgs a = adapter_args(adapters, bounds, index, requests, M);
-    a.x = dy; a.ldx = lddy; a.y = dx; a.ldy = lddx; a.h = static_cast<float*>(workspace);
-    if ((st = launch_few_rows<true>(a, dyt, xt, s)) != SQ_OK) return st;
+    a.x = dy; a.ldx = lddy; a.y = dx; a.ldy = lddx; a.h = u;
+    st = use_tiles(a, dyt) ? launch_tile<true>(a, xt, s) : launch_few_rows<true>(a, dyt, xt, s);
+    if (st != SQ_OK) return st;
+  }
+  // bf16 rows by tensor cores (three exact parts of u and h), fp32 rows by the fp32 lanes
+  const bool ta = M > 0 && xt == SQ_BF16, tb = M > 0 && dyt == SQ_BF16;
+  if (ta || tb) {
+    st = launch_grad_tiles(a, u, hidden, x, ldx, dy, lddy, ta ? da : nullptr, tb ? db : nullptr, s);
+    if (st != SQ_OK) return st;
   }
   sq::AdapterGradArgs g = {};
   g.bounds = bounds; g.index = index; g.M = (int32_t)M; g.R = adapters->R; g.L = adapters->L;
   g.Q = M > 0 ? requests : 0;
-  g.f = static_cast<const float*>(workspace); g.g = x; g.ldg = ldx; g.C = (int32_t)adapters->K; g.out = da;
-  if ((st = launch_adapter_grad<false>(g, xt, s)) != SQ_OK) return st;
-  g.f = hidden; g.g = dy; g.ldg = lddy; g.C = (int32_t)adapters->N; g.out = db; g.scale = adapters->scale;
-  return launch_adapter_grad<true>(g, dyt, s);
+  if (!ta) {
+    g.f = u; g.g = x; g.ldg = ldx; g.C = (int32_t)adapters->K; g.out = da;
+    if ((st = launch_adapter_grad<false>(g, xt, s)) != SQ_OK) return st;
+  }
+  if (!tb) {
+    g.f = hidden; g.g = dy; g.ldg = lddy; g.C = (int32_t)adapters->N; g.out = db; g.scale = adapters->scale;
+    return launch_adapter_grad<true>(g, dyt, s);
+  }
+  return SQ_OK;
 }
 
 }  // extern "C"

@@ -16,6 +16,7 @@
 #include "segquant.h"
 
 #include "adapters.cuh"
+#include "adapters_tile.cuh"
 #include "common.cuh"
 #include "gemm_dualscale.cuh"
 #include "gemm_dualscale_codes.cuh"
