@@ -340,20 +340,19 @@ sq_status sq_group_norm_act(const void* x, sq_dtype xt, int64_t B, int64_t S, in
                             int64_t ldy, int64_t ybs, float* stats, void* workspace,
                             size_t workspace_bytes, sq_stream_t stream);
 
-/* The norm fused into the combined-code producer: c, int8 [B*S, C] with row
- * stride ldc (a multiple of 16), holds the codes that
- * sq_quantize_activations_combined writes for y = act(z) rounded to bf16 (bit for
- * bit those of sq_group_norm_act's bf16 output), K segments of the C channels as
- * there; C % 16 == 0.  y: bf16 [B*S, C], row stride ldy, written too, or NULL.
- * The codes feed sq_linear_forward_combined. */
-sq_status sq_quantize_activations_combined_norm(const void* x, sq_dtype xt, int64_t B, int64_t S,
-                                                int64_t C, int64_t ldx, int64_t xbs,
-                                                int32_t groups, const float* gamma,
-                                                const float* beta, float eps, int32_t act,
-                                                const sq_segments* kseg, const float* s_pos,
-                                                const float* s_neg, int8_t* c, int64_t ldc,
-                                                void* y, int64_t ldy, void* workspace,
-                                                size_t workspace_bytes, sq_stream_t stream);
+/* The norm fused into the producer of the DualScale codes: q_pos and q_neg, int8
+ * [B*S, C] with row stride ldq (a multiple of 16), hold the codes that
+ * sq_quantize_activations writes for y = act(z) rounded to bf16 (bit for bit those of
+ * sq_group_norm_act's bf16 output), K segments of the C channels as there;
+ * C % 16 == 0.  y: bf16 [B*S, C], row stride ldy, written too, or NULL.  The codes feed
+ * sq_linear_forward_codes (SegQuant DualScale, Spanish technical summary 2.B). */
+sq_status sq_quantize_activations_norm(const void* x, sq_dtype xt, int64_t B, int64_t S, int64_t C,
+                                       int64_t ldx, int64_t xbs, int32_t groups,
+                                       const float* gamma, const float* beta, float eps,
+                                       int32_t act, const sq_segments* kseg, const float* s_pos,
+                                       const float* s_neg, int8_t* q_pos, int8_t* q_neg,
+                                       int64_t ldq, void* y, int64_t ldy, void* workspace,
+                                       size_t workspace_bytes, sq_stream_t stream);
 
 /* Gradients: dy, x and dx [B, S, C] of type xt; stats as written by the forward
  * call; with xhat = (x - mean) * rstd and dz = dy * act'(z):

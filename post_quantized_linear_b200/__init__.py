@@ -30,7 +30,7 @@ __all__ = ["QuantizedWeight", "SegQuantError", "calibrate", "quantize_weights", 
            "linear_accumulators", "stream_status", "qweight_sizes", "calibrate_hadamard",
            "quantize_activations_hadamard", "rotate_weights_hadamard",
            "linear_from_codes_hadamard", "calibrate_act", "quantize_activations_combined_act",
-           "group_norm_act", "group_norm_act_backward", "quantize_activations_combined_norm",
+           "group_norm_act", "group_norm_act_backward", "quantize_activations_norm",
            "Adapters", "adapter_add", "adapter_backward"]
 
 
@@ -557,36 +557,38 @@ def group_norm_act(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] =
     return (out, stats) if return_stats else out
 
 
-def quantize_activations_combined_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor],
-                                       beta: Optional[torch.Tensor], kseg: Sequence[int],
-                                       s_pos: torch.Tensor, s_neg: torch.Tensor, eps: float = 1e-5,
-                                       act: str = "none", out: Optional[torch.Tensor] = None,
-                                       return_y: bool = False, stream=None):
-    """Combined DualScale codes of y = act(group_norm(x)) rounded to bf16, int8
-    [B*S, C] with row stride a multiple of 16, in one pass over ``x`` [B, S, C]; the
-    codes feed ``linear_from_combined``.  With ``return_y`` also y, bf16 [B*S, C]
-    (the input of adapters beside the layer)."""
+def quantize_activations_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor],
+                              beta: Optional[torch.Tensor], kseg: Sequence[int], s_pos: torch.Tensor,
+                              s_neg: torch.Tensor, eps: float = 1e-5, act: str = "none", out=None,
+                              return_y: bool = False, stream=None):
+    """DualScale codes (q+, q-) of y = act(group_norm(x)) rounded to bf16, int8
+    [B*S, C] each (row stride a multiple of 16), in one pass over ``x`` [B, S, C]; they
+    feed ``linear_from_codes``.  With ``return_y`` (q+, q-, y), y bf16 [B*S, C] (the
+    input of adapters beside the layer)."""
     _check_map(x, "x")
     B, S, C = x.shape
     J = len(kseg) - 1
     if out is None:
-        ldc = (C + 15) // 16 * 16
-        out = torch.empty((B * S, ldc), dtype=torch.int8, device=x.device)[:, :C]
-    _check_2d(out, "out")
-    if tuple(out.shape) != (B * S, C) or out.dtype != torch.int8:
-        raise ValueError(f"out must be int8 [{B * S}, {C}]")
+        ldq = (C + 15) // 16 * 16
+        qp, qn = (t[:, :C] for t in torch.empty((2, B * S, ldq), dtype=torch.int8, device=x.device).unbind())
+    else:
+        qp, qn = out
+        for t, name in ((qp, "q_pos"), (qn, "q_neg")):
+            _check_rows(t, B * S, C, name)
+            if t.dtype != torch.int8:
+                raise ValueError(f"{name} must be int8")
+        if qp.stride(0) != qn.stride(0):
+            raise ValueError("q_pos and q_neg must share a row stride")
     y = torch.empty((B * S, C), dtype=torch.bfloat16, device=x.device) if return_y else None
     seg, keep = _lib.segments(kseg)
     ws, wp, wn = _norm_workspace(x, groups, 0, stream)
-    _lib.check("sq_quantize_activations_combined_norm",
-               _lib.load().sq_quantize_activations_combined_norm(
-                   x.data_ptr(), _dtype_code(x.dtype), B, S, C, _row_stride(x), _image_stride(x), groups,
-                   _check_f32(gamma, (C,), "gamma"), _check_f32(beta, (C,), "beta"), eps,
-                   _norm_act_code(act), ctypes.byref(seg), _check_f32(s_pos, (J,), "s_pos"),
-                   _check_f32(s_neg, (J,), "s_neg"), out.data_ptr(),
-                   out.stride(0) if B * S > 1 else (C + 15) // 16 * 16,
-                   None if y is None else y.data_ptr(), C, wp, wn, _stream(stream)))
-    return (out, y) if return_y else out
+    _lib.check("sq_quantize_activations_norm", _lib.load().sq_quantize_activations_norm(
+        x.data_ptr(), _dtype_code(x.dtype), B, S, C, _row_stride(x), _image_stride(x), groups,
+        _check_f32(gamma, (C,), "gamma"), _check_f32(beta, (C,), "beta"), eps, _norm_act_code(act),
+        ctypes.byref(seg), _check_f32(s_pos, (J,), "s_pos"), _check_f32(s_neg, (J,), "s_neg"),
+        qp.data_ptr(), qn.data_ptr(), qp.stride(0) if B * S > 1 else (C + 15) // 16 * 16,
+        None if y is None else y.data_ptr(), C, wp, wn, _stream(stream)))
+    return (qp, qn, y) if return_y else (qp, qn)
 
 
 def group_norm_act_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tensor,

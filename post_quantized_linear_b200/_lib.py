@@ -87,10 +87,9 @@ SIGNATURES = {
     "sq_group_norm_act": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_i64, c_i64, c_i32, c_vp, c_vp,
                                   ctypes.c_float, c_i32, c_vp, c_i32, c_i64, c_i64, c_vp, c_vp,
                                   c_size, c_vp]),
-    "sq_quantize_activations_combined_norm": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_i64, c_i64,
-                                                      c_i32, c_vp, c_vp, ctypes.c_float, c_i32, P_SEG,
-                                                      c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp,
-                                                      c_size, c_vp]),
+    "sq_quantize_activations_norm": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_i64, c_i64, c_i32, c_vp,
+                                             c_vp, ctypes.c_float, c_i32, P_SEG, c_vp, c_vp, c_vp, c_vp,
+                                             c_i64, c_vp, c_i64, c_vp, c_size, c_vp]),
     "sq_group_norm_act_backward": (c_i32, [c_vp, c_i64, c_i64, c_vp, c_i32, c_i64, c_i64, c_i64, c_i64,
                                            c_i64, c_i32, c_vp, c_vp, c_vp, c_i32, c_vp, c_i64, c_i64,
                                            c_vp, c_vp, c_vp, c_size, c_vp]),

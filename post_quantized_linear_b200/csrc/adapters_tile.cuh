@@ -59,11 +59,14 @@ struct AdapterTileArgs {
   int32_t starve;
 };
 
-// Shared memory between the two products: this CTA's partial h in fp32 (rows
-// padded by 16 bytes), then h as `parts` bf16 operand tiles.
+// Shared memory between the two products: this CTA's partial h in fp32, four columns
+// of a row together and rows next to one another (a warp reads 512 contiguous bytes
+// of a peer; with rows of R values it read 32 pieces of 16 bytes, and the first
+// product's sums over the cluster took most of the kernel: 100 us instead of TBD at
+// 8192 x 4608 x 1152, rank 64), then h as `parts` bf16 operand tiles.
 __host__ __device__ inline int adapter_h_bytes(int rp, int parts, int cs) {
   const int op = parts * kTileX * ((rp + 63) / 64);
-  const int ex = cs > 1 ? kTileRows * (rp + 4) * 4 : 0;
+  const int ex = cs > 1 ? kTileRows * rp * 4 : 0;
   return ((op > ex ? op : ex) + 1023) / 1024 * 1024;
 }
 
@@ -262,11 +265,10 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
         for (int k = 0; k < 8; ++k) v[c + k] = c < hc ? __uint_as_float(u[k]) : 0.0f;
       }
       if (cs > 1) {
-        const int pr = RP + 4;                 // fp32 row pitch of the partial h: conflict-free 16-byte accesses
-        float* mine = reinterpret_cast<float*>(hbuf) + row * pr + c0;
+        float4* mine = reinterpret_cast<float4*>(hbuf) + (c0 / 4) * kTileRows + row;
 #pragma unroll
         for (int c = 0; c < RB / 2; c += 4)
-          if (c < hc) *reinterpret_cast<float4*>(mine + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+          if (c < hc) mine[(c / 4) * kTileRows] = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
         __syncwarp();
         if (lane < cs) mbar_arrive_remote(mapa_shared(smem_u32(p_full), lane));
         ok = wait_warp<true>(smem_u32(p_full), 0, abort_flag, budget);
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
 #pragma unroll
             for (int c = 0; c < RB / 2; c += 4)
               if (c < hc) {
-                const float4 o = dsmem_f32x4(from + 4 * c);
+                const float4 o = dsmem_f32x4(from + (c / 4) * kTileRows * 16);
                 v[c] += o.x; v[c + 1] += o.y; v[c + 2] += o.z; v[c + 3] += o.w;
               }
           }
@@ -465,7 +467,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
   const float* f = p.f[which];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slot_bytes = kTileX + adapter_grad_f_bytes(RP);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + max(NS * slot_bytes, cs > 1 ? 128 * (RP + 4) * 4 : 0));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + max(NS * slot_bytes, cs > 1 ? 128 * RP * 4 : 0));
   uint64_t* full = bars;           // [4] g has landed
   uint64_t* ready = full + 4;      // [4] f's parts are written (and g's rows behind the piece cleared)
   uint64_t* empty = ready + 4;     // [4]
@@ -631,12 +633,11 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
     const bool mine = cs == 1 || (quad * 2 + half) % cs == rank;
     if (cs > 1) {
       // the ring is idle: all copies have landed and all products are done
-      const int pr = RP + 4;
-      float* own = reinterpret_cast<float*>(smem) + row * pr + r0;
+      float4* own = reinterpret_cast<float4*>(smem) + (r0 / 4) * 128 + row;
       if (ok) {
 #pragma unroll
         for (int c = 0; c < RB / 2; c += 4)
-          if (c < hc) *reinterpret_cast<float4*>(own + c) = make_float4(t[c], t[c + 1], t[c + 2], t[c + 3]);
+          if (c < hc) own[(c / 4) * 128] = make_float4(t[c], t[c + 1], t[c + 2], t[c + 3]);
         __syncwarp();
         if (lane < cs) mbar_arrive_remote(mapa_shared(smem_u32(p_full), lane));
         ok = wait_warp<true>(smem_u32(p_full), 0, abort_flag, budget);
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
 #pragma unroll
           for (int c = 0; c < RB / 2; c += 4)
             if (c < hc) {
-              const float4 o = dsmem_f32x4(from + 4 * c);
+              const float4 o = dsmem_f32x4(from + (c / 4) * 128 * 16);
               t[c] += o.x; t[c + 1] += o.y; t[c + 2] += o.z; t[c + 3] += o.w;
             }
         }

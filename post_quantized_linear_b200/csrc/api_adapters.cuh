@@ -172,7 +172,7 @@ sq_status launch_grad_tile_rb(sq::AdapterGradTileArgs g, const CUtensorMap& t0, 
   g.cs = cs;
   // At least the share of shared memory that the CTA has of TMEM (half, or all): a CTA
   // that is resident never waits for TMEM of another cluster's.
-  const int smem = std::max(std::max(g.stages * slot, cs > 1 ? 128 * (rp + 4) * 4 : 0) + sq::kTileBars + 1024,
+  const int smem = std::max(std::max(g.stages * slot, cs > 1 ? 128 * rp * 4 : 0) + sq::kTileBars + 1024,
                             (RB == 64 ? kSmemPerSm / 2 : kSmemPerSm) - 4096);
   cudaError_t e = smem_limit<kern>(kSmemPerSm);
   if (e != cudaSuccess) return cuda_status(e);

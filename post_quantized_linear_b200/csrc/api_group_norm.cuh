@@ -9,8 +9,8 @@ namespace {
 struct NormPlan {
   sq::NormTile t;
   int cs, nv, tiles;
+  int threads;        // of the two-pass form
   bool cluster;
-  int threads_vn;
 };
 
 int gcd_i(int a, int b) { return b == 0 ? a : gcd_i(b, a % b); }
@@ -65,7 +65,7 @@ sq_status norm_plan(int64_t B, int64_t S, int64_t C, int32_t groups, int es, int
     }
   }
   // Two passes read the inputs twice, the second time mostly from L2, in two
-  // launches (measured: 3 us apart, 0.6 of the copy rate over all traffic).
+  // launches.
   const double total_kb = (double)B * S * C * es / 1024.0;
   const double two_us = 8.0 + total_kb * (2 * tensors + 1) / (44.0 * sms);
   if (best_us <= two_us) {
@@ -73,13 +73,15 @@ sq_status norm_plan(int64_t B, int64_t S, int64_t C, int32_t groups, int es, int
     return SQ_OK;
   }
   NormPlan p = {};
+  p.threads = unit_vec <= sq::kNormThreads2 ? sq::kNormThreads2 : sq::kNormThreads;
   int m = 1;
   for (int k = 1; k <= blocks_all; ++k)
-    if (blocks_all % k == 0 && unit_vec * k <= kNormMaxVectors) m = k;
-  const int vx = (int)(unit_vec * m), ty = sq::kNormThreads / vx;
+    if (blocks_all % k == 0 && unit_vec * k <= p.threads) m = k;
+  const int vx = (int)(unit_vec * m), ty = p.threads / vx;
   const int64_t cols = (int64_t)B * (blocks_all / m);
-  // about four CTAs per SM, each a whole number of thread rows
-  int64_t tiles = std::max<int64_t>(1, (4 * (int64_t)sms + cols - 1) / cols);
+  // one wave of resident CTAs, each a whole number of thread rows
+  const int64_t resident = (int64_t)sms * (p.threads == sq::kNormThreads ? 1 : tensors == 1 ? 3 : 2);
+  int64_t tiles = std::max<int64_t>(1, resident / cols);
   int64_t rows = (S + tiles - 1) / tiles;
   rows = (rows + ty - 1) / ty * ty;
   tiles = (S + rows - 1) / rows;
@@ -137,73 +139,93 @@ sq_status launch_grid(dim3 grid, int threads, int smem, int cluster, bool depend
   return cuda_status(cudaLaunchKernelEx(&cfg, KERN, args...));
 }
 
+template <typename XT, int NT>
+sq_status norm_forward_two(const NormPlan& pl, int64_t B, const sq::NormArgs& a, cudaStream_t s) {
+  const int smem = 4 * sq::norm_smem_floats(NT, pl.t.vx, sq::Vec<XT>::n, pl.t.nb);
+  const dim3 grid((unsigned)pl.tiles, (unsigned)(pl.t.G / pl.t.nb), (unsigned)B);
+  sq_status st = launch_grid<sq::group_norm_stats_kernel<XT, NT>>(grid, NT, smem, 1, false, s, a);
+  if (st != SQ_OK) return st;
+  return launch_grid<sq::group_norm_apply_kernel<XT, NT>>(grid, NT, 8 * pl.t.nb, 1, true, s, a);
+}
+
 template <typename XT>
 sq_status norm_forward(const NormPlan& pl, int64_t B, sq::NormArgs& a, cudaStream_t s) {
-  constexpr int vn = sq::Vec<XT>::n;
-  const int smem = 4 * sq::norm_smem_floats(pl.t.vx, vn, pl.t.nb);
-  const unsigned cblocks = (unsigned)(pl.t.G / pl.t.nb);
   a.t = pl.t;
   a.tiles = pl.tiles;
-  if (pl.cluster) {
-    const dim3 grid(cblocks * (unsigned)pl.cs, (unsigned)B);
-    switch (pl.nv) {
-      case 1: return launch_grid<sq::group_norm_cluster_kernel<XT, 1>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs);
-      case 2: return launch_grid<sq::group_norm_cluster_kernel<XT, 2>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs);
-      case 4: return launch_grid<sq::group_norm_cluster_kernel<XT, 4>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs);
-      case 8: return launch_grid<sq::group_norm_cluster_kernel<XT, 8>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs);
-      default: return launch_grid<sq::group_norm_cluster_kernel<XT, 16>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs);
-    }
+  if (!pl.cluster)
+    return pl.threads == sq::kNormThreads2 ? norm_forward_two<XT, sq::kNormThreads2>(pl, B, a, s)
+                                           : norm_forward_two<XT, sq::kNormThreads>(pl, B, a, s);
+  constexpr int nt = sq::kNormThreads;
+  const int smem = 4 * sq::norm_smem_floats(nt, pl.t.vx, sq::Vec<XT>::n, pl.t.nb), cs = pl.cs;
+  const dim3 grid((unsigned)(pl.t.G / pl.t.nb * cs), (unsigned)B);
+  switch (pl.nv) {
+    case 1: return launch_grid<sq::group_norm_cluster_kernel<XT, 1>>(grid, nt, smem, cs, false, s, a, cs);
+    case 2: return launch_grid<sq::group_norm_cluster_kernel<XT, 2>>(grid, nt, smem, cs, false, s, a, cs);
+    case 4: return launch_grid<sq::group_norm_cluster_kernel<XT, 4>>(grid, nt, smem, cs, false, s, a, cs);
+    case 8: return launch_grid<sq::group_norm_cluster_kernel<XT, 8>>(grid, nt, smem, cs, false, s, a, cs);
+    default: return launch_grid<sq::group_norm_cluster_kernel<XT, 16>>(grid, nt, smem, cs, false, s, a, cs);
   }
-  const dim3 grid((unsigned)pl.tiles, cblocks, (unsigned)B);
-  sq_status st = launch_grid<sq::group_norm_stats_kernel<XT>>(grid, sq::kNormThreads, smem, 1, false, s, a);
-  if (st != SQ_OK) return st;
-  return launch_grid<sq::group_norm_apply_kernel<XT>>(grid, sq::kNormThreads, 8 * pl.t.nb, 1, false, s, a);
+}
+
+sq_status norm_params(const sq::NormBwdArgs& a, int64_t B, float* dgamma, float* dbeta, cudaStream_t s) {
+  return launch_grid<sq::group_norm_bwd_params_kernel>(dim3((unsigned)((a.t.C + 31) / 32)), 32 * sq::kParamWarps, 0, 1,
+                                                       true, s, a, (int32_t)B, dgamma, dbeta);
+}
+
+template <typename XT, int NT>
+sq_status norm_backward_two(const NormPlan& pl, int64_t B, const sq::NormBwdArgs& a, float* dgamma, float* dbeta,
+                            cudaStream_t s) {
+  constexpr int vn = sq::Vec<XT>::n;
+  const dim3 grid((unsigned)pl.tiles, (unsigned)(pl.t.G / pl.t.nb), (unsigned)B);
+  const int smem = 4 * sq::norm_smem_floats(NT, pl.t.vx, vn, pl.t.nb);
+  sq_status st = launch_grid<sq::group_norm_bwd_sums_kernel<XT, NT>>(grid, NT, smem, 1, false, s, a);
+  if (st != SQ_OK || (st = norm_params(a, B, dgamma, dbeta, s)) != SQ_OK) return st;
+  return launch_grid<sq::group_norm_bwd_apply_kernel<XT, NT>>(grid, NT, 8 * (pl.t.vx * vn + pl.t.nb), 1, true, s, a);
 }
 
 template <typename XT>
 sq_status norm_backward(const NormPlan& pl, int64_t B, sq::NormBwdArgs& a, float* dgamma, float* dbeta,
                         cudaStream_t s) {
-  constexpr int vn = sq::Vec<XT>::n;
-  const int smem = 4 * sq::norm_smem_floats(pl.t.vx, vn, pl.t.nb);
-  const unsigned cblocks = (unsigned)(pl.t.G / pl.t.nb);
   a.t = pl.t;
-  a.tiles = pl.tiles;
+  a.tiles = pl.cluster ? 0 : pl.tiles;
+  if (!pl.cluster)
+    return pl.threads == sq::kNormThreads2 ? norm_backward_two<XT, sq::kNormThreads2>(pl, B, a, dgamma, dbeta, s)
+                                           : norm_backward_two<XT, sq::kNormThreads>(pl, B, a, dgamma, dbeta, s);
+  constexpr int nt = sq::kNormThreads;
+  const int smem = 4 * sq::norm_smem_floats(nt, pl.t.vx, sq::Vec<XT>::n, pl.t.nb), cs = pl.cs;
+  const dim3 grid((unsigned)(pl.t.G / pl.t.nb * cs), (unsigned)B);
   sq_status st;
-  if (pl.cluster) {
-    const dim3 grid(cblocks * (unsigned)pl.cs, (unsigned)B);
-    switch (pl.nv) {
-      case 1: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 1>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs); break;
-      case 2: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 2>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs); break;
-      case 4: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 4>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs); break;
-      default: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 8>>(grid, sq::kNormThreads, smem, pl.cs, false, s, a, pl.cs); break;
-    }
-  } else {
-    const dim3 grid((unsigned)pl.tiles, cblocks, (unsigned)B);
-    st = launch_grid<sq::group_norm_bwd_sums_kernel<XT>>(grid, sq::kNormThreads, smem, 1, false, s, a);
-    if (st != SQ_OK) return st;
-    st = launch_grid<sq::group_norm_bwd_apply_kernel<XT>>(grid, sq::kNormThreads, 8 * (pl.t.vx * vn + pl.t.nb), 1, false, s, a);
+  switch (pl.nv) {
+    case 1: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 1>>(grid, nt, smem, cs, false, s, a, cs); break;
+    case 2: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 2>>(grid, nt, smem, cs, false, s, a, cs); break;
+    case 4: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 4>>(grid, nt, smem, cs, false, s, a, cs); break;
+    default: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 8>>(grid, nt, smem, cs, false, s, a, cs); break;
   }
   if (st != SQ_OK || (dgamma == nullptr && dbeta == nullptr)) return st;
-  return launch_grid<sq::group_norm_bwd_params_kernel>(dim3((unsigned)((a.t.C + 127) / 128)), 128, 0, 1, false, s,
-                                                       (const float*)a.part, (int32_t)(B * pl.tiles), a.t.C, dgamma,
-                                                       dbeta);
+  return norm_params(a, B, dgamma, dbeta, s);
+}
+
+// Bytes of a backward call's workspace: the images' sums, then the tiles' (none when
+// an image is one tile).
+size_t norm_bwd_bytes(const NormPlan& pl, int64_t B, int64_t C) {
+  return sizeof(float) * 2 * (size_t)B * (size_t)C * (pl.cluster ? 1 : 1 + (size_t)pl.tiles);
 }
 
 sq_status group_norm_forward(const void* x, sq_dtype xt, int64_t B, int64_t S, int64_t C, int64_t ldx, int64_t xbs,
                              int32_t groups, const float* gamma, const float* beta, float eps, int act, void* y,
                              sq_dtype yt, int64_t ldy, int64_t ybs, const sq_segments* kseg, const float* s_pos,
-                             const float* s_neg, int8_t* codes, int64_t ldc, float* stats, void* workspace,
+                             const float* s_neg, int8_t* q_pos, int8_t* q_neg, int64_t ldq, float* stats, void* workspace,
                              size_t workspace_bytes, sq_stream_t stream) {
   sq_status st = norm_sizes(B, S, C, groups, xt);
   if (st != SQ_OK) return st;
   if (act < 0 || act > 2 || !(eps >= 0.0f)) return SQ_ERR_INVALID_ARG;
   sq::NormArgs a = {};
-  if (codes != nullptr) {
-    if (s_pos == nullptr || s_neg == nullptr || ldc < C) return SQ_ERR_INVALID_ARG;
+  if (q_pos != nullptr) {
+    if (s_pos == nullptr || s_neg == nullptr || ldq < C) return SQ_ERR_INVALID_ARG;
     st = check_segments(kseg, C, SQ_MAX_SEGMENTS, 128, &a.kseg);
     if (st != SQ_OK) return st;
     if (C % 16 != 0) return SQ_ERR_UNSUPPORTED;
-    if (!aligned16(codes) || ldc % 16 != 0) return SQ_ERR_ALIGNMENT;
+    if (!aligned16(q_pos) || !aligned16(q_neg) || ldq % 16 != 0) return SQ_ERR_ALIGNMENT;
   }
   if (y != nullptr && !dtype_ok(yt)) return SQ_ERR_INVALID_ARG;
   NormPlan pl;
@@ -223,7 +245,7 @@ sq_status group_norm_forward(const void* x, sq_dtype xt, int64_t B, int64_t S, i
   }
   a.x = x; a.ldx = ldx; a.xbs = B > 1 ? xbs : 0;
   a.y = y; a.ldy = ldy; a.ybs = B > 1 ? ybs : 0; a.y_bf16 = yt == SQ_BF16;
-  a.codes = codes; a.ldc = ldc; a.s_pos = s_pos; a.s_neg = s_neg;
+  a.q_pos = q_pos; a.q_neg = q_neg; a.ldq = ldq; a.s_pos = s_pos; a.s_neg = s_neg;
   a.gamma = gamma; a.beta = beta; a.eps = eps; a.act = act; a.stats = stats;
   a.part = static_cast<float2*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -243,7 +265,7 @@ sq_status sq_group_norm_workspace_size(int64_t B, int64_t S, int64_t C, int32_t 
   NormPlan pl;
   st = norm_plan(std::max<int64_t>(B, 1), std::max<int64_t>(S, 1), C, groups, elt_size(xt), backward ? 2 : 1, &pl);
   if (st != SQ_OK || B == 0 || S == 0) return st;
-  if (backward) *bytes = sizeof(float) * 2 * (size_t)B * pl.tiles * (size_t)C;
+  if (backward) *bytes = norm_bwd_bytes(pl, B, C);
   else if (!pl.cluster) *bytes = sizeof(float2) * (size_t)B * pl.tiles * (size_t)groups;
   return SQ_OK;
 }
@@ -255,18 +277,19 @@ sq_status sq_group_norm_act(const void* x, sq_dtype xt, int64_t B, int64_t S, in
   if (y == nullptr && B > 0 && S > 0) return SQ_ERR_INVALID_ARG;
   if (!dtype_ok(yt)) return SQ_ERR_INVALID_ARG;
   return group_norm_forward(x, xt, B, S, C, ldx, xbs, groups, gamma, beta, eps, act, y, yt, ldy, ybs, nullptr,
-                            nullptr, nullptr, nullptr, 0, stats, workspace, workspace_bytes, stream);
+                            nullptr, nullptr, nullptr, nullptr, 0, stats, workspace, workspace_bytes, stream);
 }
 
-sq_status sq_quantize_activations_combined_norm(const void* x, sq_dtype xt, int64_t B, int64_t S, int64_t C,
+sq_status sq_quantize_activations_norm(const void* x, sq_dtype xt, int64_t B, int64_t S, int64_t C,
                                                 int64_t ldx, int64_t xbs, int32_t groups, const float* gamma,
                                                 const float* beta, float eps, int32_t act, const sq_segments* kseg,
-                                                const float* s_pos, const float* s_neg, int8_t* c, int64_t ldc,
+                                                const float* s_pos, const float* s_neg, int8_t* q_pos, int8_t* q_neg,
+                                                int64_t ldq,
                                                 void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
                                                 sq_stream_t stream) {
-  if (c == nullptr) return SQ_ERR_INVALID_ARG;
+  if (q_pos == nullptr || q_neg == nullptr) return SQ_ERR_INVALID_ARG;
   return group_norm_forward(x, xt, B, S, C, ldx, xbs, groups, gamma, beta, eps, act, y, SQ_BF16, ldy, S * ldy, kseg,
-                            s_pos, s_neg, c, ldc, nullptr, workspace, workspace_bytes, stream);
+                            s_pos, s_neg, q_pos, q_neg, ldq, nullptr, workspace, workspace_bytes, stream);
 }
 
 sq_status sq_group_norm_act_backward(const void* dy, int64_t lddy, int64_t dybs, const void* x, sq_dtype xt,
@@ -291,7 +314,7 @@ sq_status sq_group_norm_act_backward(const void* dy, int64_t lddy, int64_t dybs,
   if ((st = norm_map(x, es, B, S, C, ldx, xbs)) != SQ_OK) return st;
   if ((st = norm_map(dy, es, B, S, C, lddy, dybs)) != SQ_OK) return st;
   if ((st = norm_map(dx, es, B, S, C, lddx, dxbs)) != SQ_OK) return st;
-  if (workspace == nullptr || workspace_bytes < sizeof(float) * 2 * (size_t)B * pl.tiles * (size_t)C)
+  if (workspace == nullptr || workspace_bytes < norm_bwd_bytes(pl, B, C))
     return SQ_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return SQ_ERR_ALIGNMENT;
   sq::NormBwdArgs a = {};
@@ -299,7 +322,8 @@ sq_status sq_group_norm_act_backward(const void* dy, int64_t lddy, int64_t dybs,
   a.dy = dy; a.lddy = lddy; a.dybs = B > 1 ? dybs : 0;
   a.dx = dx; a.lddx = lddx; a.dxbs = B > 1 ? dxbs : 0;
   a.gamma = gamma; a.beta = beta; a.stats = stats; a.act = act;
-  a.part = static_cast<float*>(workspace);
+  a.total = static_cast<float*>(workspace);
+  a.part = a.total + 2 * (size_t)B * (size_t)C;
   return xt == SQ_BF16 ? norm_backward<__nv_bfloat16>(pl, B, a, dgamma, dbeta, s)
                        : norm_backward<float>(pl, B, a, dgamma, dbeta, s);
 }

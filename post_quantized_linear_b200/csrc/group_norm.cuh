@@ -18,6 +18,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -26,8 +27,8 @@
 
 namespace sq {
 
-constexpr int kNormThreads = 512;
-constexpr int kNormWarps = kNormThreads / 32;
+constexpr int kNormThreads = 512;    // of the cluster form
+constexpr int kNormThreads2 = 256;   // of the two-pass form (512 for groups wider than 256 vectors)
 constexpr int ACT_NONE = 0;
 
 // One block of channels (whole groups, a multiple of 16 bytes wide) and how a
@@ -35,7 +36,7 @@ constexpr int ACT_NONE = 0;
 struct NormTile {
   int32_t S, C, G, cpg;   // positions, channels, groups, channels per group
   int32_t nb;             // groups per channel block
-  int32_t vx, ty;         // vx * ty <= kNormThreads
+  int32_t vx, ty;         // vx * ty <= threads of the CTA
   int32_t rows;           // positions per CTA
 };
 
@@ -44,8 +45,9 @@ struct NormArgs {
   int64_t ldx, xbs;              // element strides of positions and images
   void* y;                       // fp32 or bf16, may be null when codes are written
   int64_t ldy, ybs;
-  int8_t* codes;                 // combined DualScale codes [B*S, C], or null
-  int64_t ldc;
+  int8_t* q_pos;                 // DualScale codes [B*S, C], or null
+  int8_t* q_neg;
+  int64_t ldq;
   const float* gamma;            // [C] or null (1)
   const float* beta;             // [C] or null (0)
   const float* s_pos;
@@ -70,9 +72,10 @@ struct NormBwdArgs {
   const float* gamma;
   const float* beta;
   const float* stats;            // [B][G][2] mean, rstd of the forward pass
-  float* part;                   // [B][tiles][2][C]: sums of dz and of dz * xhat
+  float* part;                   // [B][tiles][2][C]: sums of dz and of dz * (x - mean)
+  float* total;                  // [B][2][C]: the same over all positions of an image
   NormTile t;
-  int32_t tiles;
+  int32_t tiles;                 // per image; 0: total is written by the clusters
   int32_t act;
 };
 
@@ -109,26 +112,36 @@ __device__ __forceinline__ void store_vec(void* y, int64_t at, bool bf16, const 
 // -------------------------------------------------------------- activations
 // exp and the quotient by CUDA's fast forms (relative error about 2^-21): the
 // result is stored in bf16, or in fp32 within 1e-6 of its scale.
-__device__ __forceinline__ float norm_act(float z, int act) {
-  if (act == ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
-  if (act == ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-  return z;
+template <int ACT>
+__device__ __forceinline__ float norm_act(float z) {
+  if constexpr (ACT == ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
+  else if constexpr (ACT == ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+  else return z;
 }
-__device__ __forceinline__ float norm_act_slope(float z, int act) {
-  if (act == ACT_SILU) {
+template <int ACT>
+__device__ __forceinline__ float norm_act_slope(float z) {
+  if constexpr (ACT == ACT_SILU) {
     const float p = __fdividef(1.0f, 1.0f + __expf(-z));
     return p * fmaf(z, 1.0f - p, 1.0f);
+  } else if constexpr (ACT == ACT_GELU) {
+    return fmaf(z * 0.39894228f, __expf(-0.5f * z * z), fmaf(0.5f, erff(z * 0.70710678f), 0.5f));
+  } else {
+    return 1.0f;
   }
-  if (act == ACT_GELU)
-    return fmaf(z * 0.39894228f, __expf(-0.5f * z * z), 0.5f * (1.0f + erff(z * 0.70710678f)));
-  return 1.0f;
+}
+// The activation is a launch argument: one uniform branch outside the loops.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  if (act == ACT_SILU) f(std::integral_constant<int, ACT_SILU>{});
+  else if (act == ACT_GELU) f(std::integral_constant<int, ACT_GELU>{});
+  else f(std::integral_constant<int, ACT_NONE>{});
 }
 
 // --------------------------------------------------------------- reductions
 // Per-thread, per-channel values v[VN] of all rows of threads -> per-channel
-// totals ch[0 .. vx*VN) in shared memory.  `scratch` holds kNormThreads * VN
+// totals ch[0 .. vx*VN) in shared memory.  `scratch` holds NT * VN
 // floats.  Begins and ends with every thread past a barrier.
-template <int VN>
+template <int NT, int VN>
 __device__ __forceinline__ void reduce_channels(const float (&v)[VN], bool active, int tx, int r,
                                                 const NormTile& t, float* scratch, float* ch) {
   const int W = t.vx * VN;
@@ -140,9 +153,9 @@ __device__ __forceinline__ void reduce_channels(const float (&v)[VN], bool activ
           make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
   }
   __syncthreads();
-  const int nseg = W < kNormThreads ? kNormThreads / W : 1;
+  const int nseg = W < NT ? NT / W : 1;
   if (nseg == 1) {
-    for (int c = threadIdx.x; c < W; c += kNormThreads) {
+    for (int c = threadIdx.x; c < W; c += NT) {
       float s = 0.0f;
       for (int k = 0; k < t.ty; ++k) s += scratch[k * W + c];
       ch[c] = s;
@@ -172,7 +185,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Group totals grp[0 .. nb) of the per-thread, per-channel values.
-template <int VN>
+template <int NT, int VN>
 __device__ __forceinline__ void reduce_groups(const float (&v)[VN], bool active, int tx, int r,
                                               const NormTile& t, float* scratch, float* ch,
                                               float* grp) {
@@ -187,7 +200,7 @@ __device__ __forceinline__ void reduce_groups(const float (&v)[VN], bool active,
       __syncthreads();
       if (lane == 0) scratch[warp] = s;
       __syncthreads();
-      s = warp_sum(lane < kNormWarps ? scratch[lane] : 0.0f);
+      s = warp_sum(lane < (NT / 32) ? scratch[lane] : 0.0f);
       if (threadIdx.x == 0) grp[0] = s;
       __syncthreads();
       return;
@@ -197,7 +210,7 @@ __device__ __forceinline__ void reduce_groups(const float (&v)[VN], bool active,
     const int per = vg * t.ty;
     if (active) scratch[(tx / vg) * per + r * vg + tx % vg] = s;
     __syncthreads();
-    for (int g = warp; g < t.nb; g += kNormWarps) {
+    for (int g = warp; g < t.nb; g += (NT / 32)) {
       float a = 0.0f;
       for (int k = lane; k < per; k += 32) a += scratch[g * per + k];
       a = warp_sum(a);
@@ -206,8 +219,8 @@ __device__ __forceinline__ void reduce_groups(const float (&v)[VN], bool active,
     __syncthreads();
     return;
   }
-  reduce_channels<VN>(v, active, tx, r, t, scratch, ch);
-  for (int g = warp; g < t.nb; g += kNormWarps) {
+  reduce_channels<NT, VN>(v, active, tx, r, t, scratch, ch);
+  for (int g = warp; g < t.nb; g += (NT / 32)) {
     float a = 0.0f;
     for (int k = lane; k < t.cpg; k += 32) a += ch[g * t.cpg + k];
     a = warp_sum(a);
@@ -240,45 +253,51 @@ __device__ __forceinline__ void cluster_wait() {
 }
 
 // --------------------------------------------------------- per-thread apply
-// The channel constants of one thread's vector and what it writes.
+// The channel constants of one thread's vector and what it writes: z = x a + b
+// with b = beta - mean a, off by 2^-24 of |mean a| like the mean itself.
 template <int VN>
 struct NormOut {
-  float mean[VN], a[VN], b[VN], rp, rn;
+  float a[VN], b[VN], rp, rn;
   __device__ __forceinline__ void init(const NormArgs& p, int c0, int lc, const float* mean_g,
                                        const float* rstd_g) {
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
       const int g = (lc + i) / p.t.cpg, c = c0 + lc + i;
-      mean[i] = mean_g[g];
-      a[i] = rstd_g[g] * (p.gamma ? p.gamma[c] : 1.0f);
-      b[i] = p.beta ? p.beta[c] : 0.0f;
+      a[i] = rstd_g[g] * (p.gamma ? __ldg(p.gamma + c) : 1.0f);
+      b[i] = fmaf(-mean_g[g], a[i], p.beta ? __ldg(p.beta + c) : 0.0f);
     }
     rp = rn = 0.0f;
-    if (p.codes != nullptr) {
+    if (p.q_pos != nullptr) {
       const int j = p.kseg.segment_of(c0 + lc);   // bounds are multiples of 128
       const float sp = p.s_pos[j], sn = p.s_neg[j];
       rp = sp > 0.0f ? __frcp_rn(sp) : 0.0f;
       rn = sn > 0.0f ? __frcp_rn(sn) : 0.0f;
     }
   }
+  template <int ACT>
   __device__ __forceinline__ void put(const NormArgs& p, int img, int row, int c, const float (&x)[VN]) {
     float v[VN];
 #pragma unroll
-    for (int i = 0; i < VN; ++i) v[i] = norm_act(fmaf(x[i] - mean[i], a[i], b[i]), p.act);
-    if (p.codes != nullptr) {
+    for (int i = 0; i < VN; ++i) v[i] = norm_act<ACT>(fmaf(x[i], a[i], b[i]));
+    if (p.q_pos != nullptr) {
       // the codes are those of the bf16 values that y holds
-      uint32_t q[VN];
+      uint32_t q[VN], n[VN];
 #pragma unroll
       for (int i = 0; i < VN; ++i) {
         v[i] = __bfloat162float(__float2bfloat16_rn(v[i]));
-        q[i] = code_pos(v[i], rp) + code_neg(v[i], rn);
+        q[i] = code_pos(v[i], rp);
+        n[i] = code_neg(v[i], rn);
       }
-      int8_t* d = p.codes + ((int64_t)img * p.t.S + row) * p.ldc + c;
-      if constexpr (VN == 8)
-        *reinterpret_cast<uint2*>(d) =
+      const int64_t at = ((int64_t)img * p.t.S + row) * p.ldq + c;
+      if constexpr (VN == 8) {
+        *reinterpret_cast<uint2*>(p.q_pos + at) =
             make_uint2(pack4_low(q[0], q[1], q[2], q[3]), pack4_low(q[4], q[5], q[6], q[7]));
-      else
-        *reinterpret_cast<uint32_t*>(d) = pack4_low(q[0], q[1], q[2], q[3]);
+        *reinterpret_cast<uint2*>(p.q_neg + at) =
+            make_uint2(pack4_low(n[0], n[1], n[2], n[3]), pack4_low(n[4], n[5], n[6], n[7]));
+      } else {
+        *reinterpret_cast<uint32_t*>(p.q_pos + at) = pack4_low(q[0], q[1], q[2], q[3]);
+        *reinterpret_cast<uint32_t*>(p.q_neg + at) = pack4_low(n[0], n[1], n[2], n[3]);
+      }
     }
     if (p.y != nullptr)
       store_vec<VN>(p.y, (int64_t)img * p.ybs + (int64_t)row * p.ldy + c, p.y_bf16 != 0, v);
@@ -287,9 +306,9 @@ struct NormOut {
 
 // Shared memory of the norm kernels, in floats: scratch (reductions, then the
 // cluster's totals), two totals per channel and four values per group.
-__host__ __device__ inline int norm_smem_floats(int vx, int vn, int nb) {
+__host__ __device__ inline int norm_smem_floats(int threads, int vx, int vn, int nb) {
   const int w2 = 2 * vx * vn;
-  return (kNormThreads * vn > w2 ? kNormThreads * vn : w2) + w2 + 4 * nb;
+  return (threads * vn > w2 ? threads * vn : w2) + w2 + 4 * nb;
 }
 
 // ------------------------------------------------- forward, slab in registers
@@ -334,7 +353,7 @@ __global__ void __launch_bounds__(kNormThreads, NV <= 4 ? 2 : 1)
 #pragma unroll
     for (int k = 0; k < VN; ++k) s[k] += v[k];   // absent rows are zeros
   }
-  reduce_groups<VN>(s, active, tx, r, t, scratch, ch, pub_mean);
+  reduce_groups<kNormThreads, VN>(s, active, tx, r, t, scratch, ch, pub_mean);
   const float n_loc = (float)n_rows * (float)t.cpg;
   for (int g = threadIdx.x; g < t.nb; g += kNormThreads)
     pub_mean[g] = n_loc > 0.0f ? pub_mean[g] / n_loc : 0.0f;
@@ -351,7 +370,7 @@ __global__ void __launch_bounds__(kNormThreads, NV <= 4 ? 2 : 1)
       for (int k = 0; k < VN; ++k) { const float d = v[k] - m[k]; s[k] = fmaf(d, d, s[k]); }
     }
   }
-  reduce_groups<VN>(s, active, tx, r, t, scratch, ch, pub_m2);
+  reduce_groups<kNormThreads, VN>(s, active, tx, r, t, scratch, ch, pub_m2);
   if (cs > 1) { cluster_arrive(); cluster_wait(); }
   for (int g = threadIdx.x; g < t.nb; g += kNormThreads) {
     float n = 0.0f, mean = 0.0f, m2 = 0.0f;
@@ -377,13 +396,15 @@ __global__ void __launch_bounds__(kNormThreads, NV <= 4 ? 2 : 1)
   if (active) {
     NormOut<VN> o;
     o.init(p, c0, lc, fin_mean, fin_rstd);
+    with_act(p.act, [&](auto act) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int row = r0 + r + i * t.ty;
-      float v[VN];
-      Vec<XT>::load_raw(raw[i], v);
-      if (row < r1) o.put(p, img, row, c0 + lc, v);
-    }
+      for (int i = 0; i < NV; ++i) {
+        const int row = r0 + r + i * t.ty;
+        float v[VN];
+        Vec<XT>::load_raw(raw[i], v);
+        if (row < r1) o.template put<decltype(act)::value>(p, img, row, c0 + lc, v);
+      }
+    });
   }
   __syncwarp();
   if (cs > 1) cluster_wait();     // the peers have read this CTA's
@@ -391,18 +412,19 @@ __global__ void __launch_bounds__(kNormThreads, NV <= 4 ? 2 : 1)
 
 // ------------------------------------------------------- forward, two passes
 // Pass 1: one CTA per (tile of positions, channel block, image) writes mean and
-// M2 of each of its groups.  A thread takes eight rows at a time: their mean
+// M2 of each of its groups.  A thread takes a few rows at a time: their mean
 // and squared deviations per channel, merged into its running ones.
-template <typename XT>
-__global__ void __launch_bounds__(kNormThreads, 2) group_norm_stats_kernel(const NormArgs p) {
-  constexpr int VN = Vec<XT>::n, U = 8;
+template <typename XT, int NT>
+__global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_stats_kernel(const NormArgs p) {
+  constexpr int VN = Vec<XT>::n, U = 32 / VN;
   extern __shared__ __align__(16) float sm[];
   const NormTile& t = p.t;
   const int W = t.vx * VN;
   float* scratch = sm;
-  float* ch = scratch + max(kNormThreads * VN, 2 * W);
+  float* ch = scratch + max(NT * VN, 2 * W);
   float* g_mean = ch + 2 * W;
   float* g_m2 = g_mean + t.nb;
+  grid_dep_launch();
   const int tile = blockIdx.x, cb = blockIdx.y, img = blockIdx.z;
   const int tx = threadIdx.x % t.vx, r = threadIdx.x / t.vx;
   const bool active = r < t.ty;
@@ -413,17 +435,21 @@ __global__ void __launch_bounds__(kNormThreads, 2) group_norm_stats_kernel(const
 #pragma unroll
   for (int k = 0; k < VN; ++k) mean[k] = m2[k] = 0.0f;
   if (active) {
-    for (int row = r0 + r; row < r1; row += U * t.ty) {
-      uint4 raw[U];
-      int cnt = 0;
+    uint4 raw[U], ahead[U];
+    auto fetch = [&](uint4 (&to)[U], int row) {
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (row + i * t.ty < r1) {
-          raw[i] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)(row + i * t.ty) * p.ldx));
-          ++cnt;
-        }
+        to[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row + i * t.ty < r1)
+          to[i] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)(row + i * t.ty) * p.ldx));
       }
+    };
+    fetch(ahead, r0 + r);
+    for (int row = r0 + r; row < r1; row += U * t.ty) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) raw[i] = ahead[i];
+      fetch(ahead, row + U * t.ty);      // in flight while this chunk is summed
+      const int cnt = min(U, (r1 - row + t.ty - 1) / t.ty);
       float s[VN];
 #pragma unroll
       for (int k = 0; k < VN; ++k) s[k] = 0.0f;
@@ -459,24 +485,24 @@ __global__ void __launch_bounds__(kNormThreads, 2) group_norm_stats_kernel(const
   float s[VN];
 #pragma unroll
   for (int k = 0; k < VN; ++k) s[k] = n * mean[k];
-  reduce_groups<VN>(s, active, tx, r, t, scratch, ch, g_mean);
+  reduce_groups<NT, VN>(s, active, tx, r, t, scratch, ch, g_mean);
   const float n_tile = (float)(r1 - r0) * (float)t.cpg;
-  for (int g = threadIdx.x; g < t.nb; g += kNormThreads) g_mean[g] /= n_tile;
+  for (int g = threadIdx.x; g < t.nb; g += NT) g_mean[g] /= n_tile;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < VN; ++k) {
     const float d = active ? mean[k] - g_mean[(lc + k) / t.cpg] : 0.0f;
     s[k] = fmaf(n * d, d, m2[k]);
   }
-  reduce_groups<VN>(s, active, tx, r, t, scratch, ch, g_m2);
-  for (int g = threadIdx.x; g < t.nb; g += kNormThreads)
+  reduce_groups<NT, VN>(s, active, tx, r, t, scratch, ch, g_m2);
+  for (int g = threadIdx.x; g < t.nb; g += NT)
     p.part[((int64_t)img * p.tiles + tile) * t.G + cb * t.nb + g] = make_float2(g_mean[g], g_m2[g]);
 }
 
 // Pass 2: the same tiles in the opposite order (the last ones read are the
 // likeliest in L2); each CTA merges its groups' tiles first, a warp per group.
-template <typename XT>
-__global__ void __launch_bounds__(kNormThreads, 2) group_norm_apply_kernel(const NormArgs p) {
+template <typename XT, int NT>
+__global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_apply_kernel(const NormArgs p) {
   constexpr int VN = Vec<XT>::n, U = 4;
   extern __shared__ __align__(16) float sm[];
   const NormTile& t = p.t;
@@ -486,7 +512,8 @@ __global__ void __launch_bounds__(kNormThreads, 2) group_norm_apply_kernel(const
             img = gridDim.z - 1 - blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = cb * t.nb * t.cpg;
-  for (int g = warp; g < t.nb; g += kNormWarps) {
+  grid_dep_wait();
+  for (int g = warp; g < t.nb; g += (NT / 32)) {
     float n = 0.0f, mean = 0.0f, m2 = 0.0f;
     for (int k = lane; k < p.tiles; k += 32) {
       const float2 v = p.part[((int64_t)img * p.tiles + k) * t.G + cb * t.nb + g];
@@ -518,96 +545,116 @@ __global__ void __launch_bounds__(kNormThreads, 2) group_norm_apply_kernel(const
   const XT* base = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + c0 + lc;
   NormOut<VN> o;
   o.init(p, c0, lc, fin_mean, fin_rstd);
-  for (int row = r0 + r; row < r1; row += U * t.ty) {
-    uint4 raw[U];
+  with_act(p.act, [&](auto act) {
+    uint4 raw[U], ahead[U];
+    auto fetch = [&](int row) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (row + i * t.ty < r1) raw[i] = load_stream(base + (int64_t)(row + i * t.ty) * p.ldx);
-    }
+      for (int i = 0; i < U; ++i)
+        if (row + i * t.ty < r1) ahead[i] = load_stream(base + (int64_t)(row + i * t.ty) * p.ldx);
+    };
+    fetch(r0 + r);
+    for (int row = r0 + r; row < r1; row += U * t.ty) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      float v[VN];
-      Vec<XT>::load_raw(raw[i], v);
-      if (row + i * t.ty < r1) o.put(p, img, row + i * t.ty, c0 + lc, v);
+      for (int i = 0; i < U; ++i) raw[i] = ahead[i];
+      fetch(row + U * t.ty);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        float v[VN];
+        Vec<XT>::load_raw(raw[i], v);
+        if (row + i * t.ty < r1) o.template put<decltype(act)::value>(p, img, row + i * t.ty, c0 + lc, v);
+      }
     }
-  }
+  });
 }
 
 // ------------------------------------------------------------------ gradients
-// One thread's channel constants in the backward pass.
+// The sums run over d = x - mean: dz = dy act'(d a + beta), a = rstd gamma,
+// s1 = sum dz, s2 = sum dz d = (sum dz xhat) / rstd.  With the group's m1, m2
+//   dx = a dz + d p + q,  p = -rstd^2 m2,  q = -rstd m1,
+// and with the constants of x itself (b = beta - mean a, q' = q - mean p), as the
+// forward has them, dx = a dz + (x p + q').
 template <int VN>
 struct NormGrad {
-  float mean[VN], rstd[VN], ga[VN], be[VN];
+  float mean[VN], a[VN], be[VN];
   __device__ __forceinline__ void init(const NormBwdArgs& p, int img, int c0, int lc) {
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
       const int c = c0 + lc + i;
-      const float* st = p.stats + ((int64_t)img * p.t.G + c / p.t.cpg) * 2;
-      mean[i] = st[0];
-      rstd[i] = st[1];
-      ga[i] = p.gamma ? p.gamma[c] : 1.0f;
-      be[i] = p.beta ? p.beta[c] : 0.0f;
+      const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (int64_t)img * p.t.G + c / p.t.cpg);
+      mean[i] = st.x;
+      a[i] = st.y * (p.gamma ? __ldg(p.gamma + c) : 1.0f);
+      be[i] = p.beta ? __ldg(p.beta + c) : 0.0f;
     }
   }
-  __device__ __forceinline__ float hat(int i, float x) const { return (x - mean[i]) * rstd[i]; }
-  __device__ __forceinline__ float dz(const NormBwdArgs& p, int i, float xh, float dy) const {
-    return dy * norm_act_slope(fmaf(xh, ga[i], be[i]), p.act);
+  template <int ACT, typename XT>
+  __device__ __forceinline__ void sums(const uint4& xr, const uint4& gr, float (&s1)[VN], float (&s2)[VN]) const {
+    float x[VN], g[VN];
+    Vec<XT>::load_raw(xr, x);
+    Vec<XT>::load_raw(gr, g);
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+      const float d = x[i] - mean[i], dz = g[i] * norm_act_slope<ACT>(fmaf(d, a[i], be[i]));
+      s1[i] += dz;
+      s2[i] = fmaf(dz, d, s2[i]);
+    }
   }
 };
 
-template <typename XT, int VN>
-__device__ __forceinline__ void grad_sums(const NormGrad<VN>& k, const NormBwdArgs& p, const uint4& xr,
-                                          const uint4& gr, float (&s1)[VN], float (&s2)[VN]) {
-  float x[VN], g[VN];
-  Vec<XT>::load_raw(xr, x);
-  Vec<XT>::load_raw(gr, g);
+template <int VN>
+struct NormGradOut {
+  float a[VN], b[VN], pp[VN], q[VN];
+  // g1, g2: m1 and m2 of the block's groups
+  __device__ __forceinline__ void init(const NormBwdArgs& p, int img, int c0, int lc, const float* g1,
+                                       const float* g2) {
 #pragma unroll
-  for (int i = 0; i < VN; ++i) {
-    const float xh = k.hat(i, x[i]), d = k.dz(p, i, xh, g[i]);
-    s1[i] += d;
-    s2[i] = fmaf(d, xh, s2[i]);
+    for (int i = 0; i < VN; ++i) {
+      const int c = c0 + lc + i, g = (lc + i) / p.t.cpg;
+      const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (int64_t)img * p.t.G + c / p.t.cpg);
+      a[i] = st.y * (p.gamma ? __ldg(p.gamma + c) : 1.0f);
+      b[i] = fmaf(-st.x, a[i], p.beta ? __ldg(p.beta + c) : 0.0f);
+      pp[i] = -st.y * st.y * g2[g];
+      q[i] = -fmaf(st.x, pp[i], st.y * g1[g]);
+    }
   }
-}
-
-// m1, m2: the group's means of dz gamma and dz gamma xhat, per channel of the vector.
-template <typename XT, int VN>
-__device__ __forceinline__ void grad_put(const NormGrad<VN>& k, const NormBwdArgs& p, int64_t at,
-                                         const uint4& xr, const uint4& gr, const float (&m1)[VN],
-                                         const float (&m2)[VN]) {
-  float x[VN], g[VN], o[VN];
-  Vec<XT>::load_raw(xr, x);
-  Vec<XT>::load_raw(gr, g);
+  template <int ACT, typename XT>
+  __device__ __forceinline__ void put(void* dx, int64_t at, const uint4& xr, const uint4& gr) const {
+    float x[VN], g[VN], o[VN];
+    Vec<XT>::load_raw(xr, x);
+    Vec<XT>::load_raw(gr, g);
 #pragma unroll
-  for (int i = 0; i < VN; ++i) {
-    const float xh = k.hat(i, x[i]), d = k.dz(p, i, xh, g[i]);
-    o[i] = k.rstd[i] * (fmaf(d, k.ga[i], -m1[i]) - xh * m2[i]);
+    for (int i = 0; i < VN; ++i)
+      o[i] = fmaf(g[i] * norm_act_slope<ACT>(fmaf(x[i], a[i], b[i])), a[i], fmaf(x[i], pp[i], q[i]));
+    store_vec<VN>(dx, at, VN == 8, o);
   }
-  store_vec<VN>(p.dx, at, VN == 8, o);
-}
+};
 
-// Group means from the per-channel totals tot[2][W] (sums of dz, of dz*xhat).
-__device__ __forceinline__ void grad_group_means(const NormBwdArgs& p, int c0, int W, const float* tot,
+// m1 and m2 of the block's groups from its channels' sums tot[2][W].
+template <int NT>
+__device__ __forceinline__ void grad_group_means(const NormBwdArgs& p, int img, int c0, int W, const float* tot,
                                                  float* g1, float* g2) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float inv = 1.0f / ((float)p.t.S * (float)p.t.cpg);
-  for (int g = warp; g < p.t.nb; g += kNormWarps) {
+  for (int g = warp; g < p.t.nb; g += NT / 32) {
     float a = 0.0f, b = 0.0f;
     for (int k = lane; k < p.t.cpg; k += 32) {
       const int c = g * p.t.cpg + k;
-      const float ga = p.gamma ? p.gamma[c0 + c] : 1.0f;
+      const float ga = p.gamma ? __ldg(p.gamma + c0 + c) : 1.0f;
       a = fmaf(ga, tot[c], a);
       b = fmaf(ga, tot[W + c], b);
     }
     a = warp_sum(a);
     b = warp_sum(b);
-    if (lane == 0) { g1[g] = a * inv; g2[g] = b * inv; }
+    // rstd turns the sum over d into the one over xhat
+    if (lane == 0) {
+      g1[g] = a * inv;
+      g2[g] = b * inv * p.stats[((int64_t)img * p.t.G + c0 / p.t.cpg + g) * 2 + 1];
+    }
   }
   __syncthreads();
 }
 
-// Slab of x and dy in the registers of a cluster; part[img][0][2][C] receives
-// the image's sums for dgamma and dbeta.
+// Slab of x and dy in the registers of a cluster; total[img] receives the
+// image's sums for dgamma and dbeta.
 template <typename XT, int NV>
 __global__ void __launch_bounds__(kNormThreads, 1)
     group_norm_bwd_cluster_kernel(const NormBwdArgs p, int cs) {
@@ -616,7 +663,7 @@ __global__ void __launch_bounds__(kNormThreads, 1)
   const NormTile& t = p.t;
   const int W = t.vx * VN;
   float* scratch = sm;                           // later the cluster's totals [2][W]
-  float* ch = scratch + max(kNormThreads * VN, 2 * W);       // this CTA's totals [2][W]
+  float* ch = scratch + max(kNormThreads * VN, 2 * W);   // this CTA's totals [2][W]
   float* g1 = ch + 2 * W;
   float* g2 = g1 + t.nb;
   const int rank = blockIdx.x % cs, cb = blockIdx.x / cs, img = blockIdx.y;
@@ -626,6 +673,7 @@ __global__ void __launch_bounds__(kNormThreads, 1)
   const int r0 = rank * t.rows, r1 = min(t.S, r0 + t.rows);
   const XT* xb = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + c0 + lc;
   const XT* gb = static_cast<const XT*>(p.dy) + (int64_t)img * p.dybs + c0 + lc;
+  grid_dep_launch();
   uint4 xr[NV], gr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -636,18 +684,20 @@ __global__ void __launch_bounds__(kNormThreads, 1)
       gr[i] = load_stream(gb + (int64_t)row * p.lddy);
     }
   }
-  NormGrad<VN> k;
   float s1[VN], s2[VN];
 #pragma unroll
   for (int i = 0; i < VN; ++i) s1[i] = s2[i] = 0.0f;
   if (active) {
+    NormGrad<VN> k;
     k.init(p, img, c0, lc);
+    with_act(p.act, [&](auto act) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (r0 + r + i * t.ty < r1) grad_sums<XT, VN>(k, p, xr[i], gr[i], s1, s2);
+      for (int i = 0; i < NV; ++i)
+        if (r0 + r + i * t.ty < r1) k.template sums<decltype(act)::value, XT>(xr[i], gr[i], s1, s2);
+    });
   }
-  reduce_channels<VN>(s1, active, tx, r, t, scratch, ch);
-  reduce_channels<VN>(s2, active, tx, r, t, scratch, ch + W);
+  reduce_channels<kNormThreads, VN>(s1, active, tx, r, t, scratch, ch);
+  reduce_channels<kNormThreads, VN>(s2, active, tx, r, t, scratch, ch + W);
   if (cs > 1) { cluster_arrive(); cluster_wait(); }
   for (int c = threadIdx.x; c < 2 * W; c += kNormThreads) {
     float a = 0.0f;
@@ -658,35 +708,39 @@ __global__ void __launch_bounds__(kNormThreads, 1)
     }
     scratch[c] = a;
     if (rank == 0)
-      p.part[(int64_t)img * 2 * t.C + (c < W ? c0 + c : t.C + c0 + c - W)] = a;
+      p.total[(int64_t)img * 2 * t.C + (c < W ? c0 + c : t.C + c0 + c - W)] = a;
   }
   __syncthreads();
   if (cs > 1) cluster_arrive();
-  grad_group_means(p, c0, W, scratch, g1, g2);
+  grad_group_means<kNormThreads>(p, img, c0, W, scratch, g1, g2);
   if (active) {
-    float m1[VN], m2[VN];
+    NormGradOut<VN> o;
+    o.init(p, img, c0, lc, g1, g2);
+    with_act(p.act, [&](auto act) {
 #pragma unroll
-    for (int i = 0; i < VN; ++i) { m1[i] = g1[(lc + i) / t.cpg]; m2[i] = g2[(lc + i) / t.cpg]; }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int row = r0 + r + i * t.ty;
-      if (row < r1)
-        grad_put<XT, VN>(k, p, (int64_t)img * p.dxbs + (int64_t)row * p.lddx + c0 + lc, xr[i], gr[i], m1, m2);
-    }
+      for (int i = 0; i < NV; ++i) {
+        const int row = r0 + r + i * t.ty;
+        if (row < r1)
+          o.template put<decltype(act)::value, XT>(
+              p.dx, (int64_t)img * p.dxbs + (int64_t)row * p.lddx + c0 + lc, xr[i], gr[i]);
+      }
+    });
   }
   __syncwarp();
   if (cs > 1) cluster_wait();
 }
 
-// Two passes: the tiles' per-channel sums, then dx.
-template <typename XT>
-__global__ void __launch_bounds__(kNormThreads, 1) group_norm_bwd_sums_kernel(const NormBwdArgs p) {
+// Two passes: the tiles' per-channel sums, the images' (group_norm_bwd_params_kernel),
+// then dx.
+template <typename XT, int NT>
+__global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_sums_kernel(const NormBwdArgs p) {
   constexpr int VN = Vec<XT>::n, U = 4;
   extern __shared__ __align__(16) float sm[];
   const NormTile& t = p.t;
   const int W = t.vx * VN;
   float* scratch = sm;
-  float* ch = scratch + max(kNormThreads * VN, 2 * W);
+  float* ch = scratch + max(NT * VN, 2 * W);
+  grid_dep_launch();
   const int tile = blockIdx.x, cb = blockIdx.y, img = blockIdx.z;
   const int tx = threadIdx.x % t.vx, r = threadIdx.x / t.vx;
   const bool active = r < t.ty;
@@ -698,33 +752,41 @@ __global__ void __launch_bounds__(kNormThreads, 1) group_norm_bwd_sums_kernel(co
 #pragma unroll
   for (int i = 0; i < VN; ++i) s1[i] = s2[i] = 0.0f;
   if (active) {
-    NormGrad<VN> k;
-    k.init(p, img, c0, lc);
-    for (int row = r0 + r; row < r1; row += U * t.ty) {
-      uint4 xr[U], gr[U];
+    uint4 xr[U], gr[U], xa[U], ga[U];
+    auto fetch = [&](int row) {
 #pragma unroll
       for (int i = 0; i < U; ++i)
         if (row + i * t.ty < r1) {
-          xr[i] = __ldg(reinterpret_cast<const uint4*>(xb + (int64_t)(row + i * t.ty) * p.ldx));
-          gr[i] = __ldg(reinterpret_cast<const uint4*>(gb + (int64_t)(row + i * t.ty) * p.lddy));
+          xa[i] = __ldg(reinterpret_cast<const uint4*>(xb + (int64_t)(row + i * t.ty) * p.ldx));
+          ga[i] = __ldg(reinterpret_cast<const uint4*>(gb + (int64_t)(row + i * t.ty) * p.lddy));
         }
+    };
+    fetch(r0 + r);
+    NormGrad<VN> k;
+    k.init(p, img, c0, lc);
+    with_act(p.act, [&](auto act) {
+      for (int row = r0 + r; row < r1; row += U * t.ty) {
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (row + i * t.ty < r1) grad_sums<XT, VN>(k, p, xr[i], gr[i], s1, s2);
-    }
+        for (int i = 0; i < U; ++i) { xr[i] = xa[i]; gr[i] = ga[i]; }
+        fetch(row + U * t.ty);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (row + i * t.ty < r1) k.template sums<decltype(act)::value, XT>(xr[i], gr[i], s1, s2);
+      }
+    });
   }
-  reduce_channels<VN>(s1, active, tx, r, t, scratch, ch);
-  reduce_channels<VN>(s2, active, tx, r, t, scratch, ch + W);
+  reduce_channels<NT, VN>(s1, active, tx, r, t, scratch, ch);
+  reduce_channels<NT, VN>(s2, active, tx, r, t, scratch, ch + W);
   float* d = p.part + ((int64_t)img * p.tiles + tile) * 2 * t.C + c0;
-  for (int c = threadIdx.x; c < W; c += kNormThreads) {
+  for (int c = threadIdx.x; c < W; c += NT) {
     d[c] = ch[c];
     d[t.C + c] = ch[W + c];
   }
 }
 
-template <typename XT>
-__global__ void __launch_bounds__(kNormThreads, 1) group_norm_bwd_apply_kernel(const NormBwdArgs p) {
-  constexpr int VN = Vec<XT>::n, U = 4;
+template <typename XT, int NT>
+__global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_apply_kernel(const NormBwdArgs p) {
+  constexpr int VN = Vec<XT>::n, U = 2;
   extern __shared__ __align__(16) float sm[];
   const NormTile& t = p.t;
   const int W = t.vx * VN;
@@ -734,55 +796,106 @@ __global__ void __launch_bounds__(kNormThreads, 1) group_norm_bwd_apply_kernel(c
   const int tile = gridDim.x - 1 - blockIdx.x, cb = gridDim.y - 1 - blockIdx.y,
             img = gridDim.z - 1 - blockIdx.z;
   const int c0 = cb * t.nb * t.cpg;
-  for (int c = threadIdx.x; c < 2 * W; c += kNormThreads) {
-    const float* d = p.part + (int64_t)img * p.tiles * 2 * t.C + (c < W ? c0 + c : t.C + c0 + c - W);
-    float a = 0.0f;
-    for (int k = 0; k < p.tiles; ++k) a += d[(int64_t)k * 2 * t.C];
-    tot[c] = a;
-  }
-  __syncthreads();
-  grad_group_means(p, c0, W, tot, g1, g2);
   const int tx = threadIdx.x % t.vx, r = threadIdx.x / t.vx;
-  if (r >= t.ty) return;
+  const bool active = r < t.ty;
   const int lc = tx * VN;
   const int r0 = tile * t.rows, r1 = min(t.S, r0 + t.rows);
   const XT* xb = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + c0 + lc;
   const XT* gb = static_cast<const XT*>(p.dy) + (int64_t)img * p.dybs + c0 + lc;
-  NormGrad<VN> k;
-  k.init(p, img, c0, lc);
-  float m1[VN], m2[VN];
-#pragma unroll
-  for (int i = 0; i < VN; ++i) { m1[i] = g1[(lc + i) / t.cpg]; m2[i] = g2[(lc + i) / t.cpg]; }
-  for (int row = r0 + r; row < r1; row += U * t.ty) {
-    uint4 xr[U], gr[U];
+  grid_dep_wait();
+  uint4 xr[U], gr[U], xa[U], ga[U];
+  auto fetch = [&](int row) {
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (row + i * t.ty < r1) {
-        xr[i] = load_stream(xb + (int64_t)(row + i * t.ty) * p.ldx);
-        gr[i] = load_stream(gb + (int64_t)(row + i * t.ty) * p.lddy);
+      if (active && row + i * t.ty < r1) {
+        xa[i] = load_stream(xb + (int64_t)(row + i * t.ty) * p.ldx);
+        ga[i] = load_stream(gb + (int64_t)(row + i * t.ty) * p.lddy);
       }
+  };
+  fetch(r0 + r);
+  for (int c = threadIdx.x; c < 2 * W; c += NT)
+    tot[c] = p.total[(int64_t)img * 2 * t.C + (c < W ? c0 + c : t.C + c0 + c - W)];
+  __syncthreads();
+  grad_group_means<NT>(p, img, c0, W, tot, g1, g2);
+  if (!active) return;
+  NormGradOut<VN> o;
+  o.init(p, img, c0, lc, g1, g2);
+  with_act(p.act, [&](auto act) {
+    for (int row = r0 + r; row < r1; row += U * t.ty) {
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (row + i * t.ty < r1)
-        grad_put<XT, VN>(k, p, (int64_t)img * p.dxbs + (int64_t)(row + i * t.ty) * p.lddx + c0 + lc, xr[i],
-                         gr[i], m1, m2);
-  }
+      for (int i = 0; i < U; ++i) { xr[i] = xa[i]; gr[i] = ga[i]; }
+      fetch(row + U * t.ty);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (row + i * t.ty < r1)
+          o.template put<decltype(act)::value, XT>(
+              p.dx, (int64_t)img * p.dxbs + (int64_t)(row + i * t.ty) * p.lddx + c0 + lc, xr[i], gr[i]);
+    }
+  });
 }
 
-// dbeta and dgamma: the sums of all images and tiles, in order; a thread per channel.
-__global__ void __launch_bounds__(128) group_norm_bwd_params_kernel(const float* __restrict__ part,
-                                                                    int32_t count, int32_t C,
-                                                                    float* __restrict__ dgamma,
-                                                                    float* __restrict__ dbeta) {
-  const int c = blockIdx.x * 128 + threadIdx.x;
-  if (c >= C) return;
-  float a = 0.0f, b = 0.0f;
-  for (int k = 0; k < count; ++k) {
-    a += part[(int64_t)k * 2 * C + c];
-    b += part[(int64_t)k * 2 * C + C + c];
+// dbeta and dgamma, and (two passes) each image's sums over its tiles.  A block
+// has 32 channels; its warps share the tiles of an image and their sums are added in
+// order, so every result repeats bit for bit.
+constexpr int kParamWarps = 16;
+__global__ void __launch_bounds__(32 * kParamWarps) group_norm_bwd_params_kernel(const NormBwdArgs p, int32_t B,
+                                                                                 float* __restrict__ dgamma,
+                                                                                 float* __restrict__ dbeta) {
+  __shared__ float sh[2][kParamWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int C = p.t.C, c = blockIdx.x * 32 + lane;
+  grid_dep_launch();
+  grid_dep_wait();
+  float sum1 = 0.0f, sum2 = 0.0f;                // this warp's images
+  const float* stat = p.stats + (int64_t)(min(c, C - 1) / p.t.cpg) * 2 + 1;
+  if (p.tiles > 0) {
+    for (int b = 0; b < B; ++b) {
+      float a1 = 0.0f, a2 = 0.0f;
+      if (c < C) {
+        const float* d = p.part + (int64_t)b * p.tiles * 2 * C + c;
+#pragma unroll 4
+        for (int k = warp; k < p.tiles; k += kParamWarps) {
+          a1 += d[(int64_t)k * 2 * C];
+          a2 += d[(int64_t)k * 2 * C + C];
+        }
+      }
+      sh[0][warp][lane] = a1;
+      sh[1][warp][lane] = a2;
+      __syncthreads();
+      if (warp < 2 && c < C) {
+        float a = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kParamWarps; ++k) a += sh[warp][k][lane];
+        p.total[((int64_t)b * 2 + warp) * C + c] = a;
+        sum1 += warp == 0 ? a : a * stat[(int64_t)b * p.t.G * 2];
+      }
+      __syncthreads();
+    }
+    if (warp < 2) sh[warp][0][lane] = sum1;
+    __syncthreads();
+    if (warp == 0 && c < C) {
+      if (dbeta != nullptr) dbeta[c] = sh[0][0][lane];
+      if (dgamma != nullptr) dgamma[c] = sh[1][0][lane];
+    }
+    return;
   }
-  if (dbeta != nullptr) dbeta[c] = a;
-  if (dgamma != nullptr) dgamma[c] = b;
+  if (c < C) {
+#pragma unroll 2
+    for (int b = warp; b < B; b += kParamWarps) {
+      sum1 += p.total[(int64_t)b * 2 * C + c];
+      sum2 = fmaf(p.total[((int64_t)b * 2 + 1) * C + c], stat[(int64_t)b * p.t.G * 2], sum2);
+    }
+  }
+  sh[0][warp][lane] = sum1;
+  sh[1][warp][lane] = sum2;
+  __syncthreads();
+  if (warp < 2 && c < C) {
+    float a = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kParamWarps; ++k) a += sh[warp][k][lane];
+    float* out = warp == 0 ? dbeta : dgamma;
+    if (out != nullptr) out[c] = a;
+  }
 }
 
 }  // namespace sq

@@ -264,13 +264,13 @@ def test_norm_codes_linear_adapters_run(B, S, C, N, act):
     bounds, idx = requests([S] * B, [i % 2 for i in range(B)])
     y16 = pq.group_norm_act(x, 32, gamma, beta, act=act).view(M, C)
     sp, sn = pq.calibrate(y16, (0, C))
-    codes, rows = pq.quantize_activations_combined_norm(x, 32, gamma, beta, (0, C), sp, sn, act=act, return_y=True)
-    base = pq.linear_from_combined(codes, qw, sp, sn)
+    qp, qn, rows = pq.quantize_activations_norm(x, 32, gamma, beta, (0, C), sp, sn, act=act, return_y=True)
+    base = pq.linear_from_codes(qp, qn, qw, sp, sn)
     assert torch.equal(base, pq.linear(y16, qw, sp, sn))
     (want, _), (e, _) = forward64(base, rows, ad, bounds, idx)
     check(pq.adapter_add(base, rows, ad, bounds, idx), want, e)
     # base rounded, the sum rounded: two half steps of the layer's 64-bit value
-    q = codes.double()
+    q = qp.double() + qn.double()
     full = torch.where(q >= 0, q * sp.double(), q * sn.double()) @ (qw.codes.double() * qw.scales[0].double()[:, None]).t()
     (ref, _), (e2, _) = forward64(full, rows, ad, bounds, idx)
     mag = q.abs() @ (qw.codes.double().abs() * qw.scales[0].double()[:, None]).t() * max(sp.item(), sn.item())

@@ -159,12 +159,13 @@ def test_codes_equal_the_quantizer_of_the_norm(shape, dtype, act):
     kseg = (0, C) if C < 256 else (0, 256, C)
     y16 = pq.group_norm_act(x, G, gamma, beta, act=act, out_dtype=BF).view(B * S, C)
     sp, sn = pq.calibrate(y16, kseg)
-    want = pq.quantize_activations_combined(y16, kseg, sp, sn)
-    codes, y = pq.quantize_activations_combined_norm(x, G, gamma, beta, kseg, sp, sn, act=act, return_y=True)
-    assert torch.equal(codes, want) and torch.equal(y, y16)
-    wide = torch.full((B * S, C + 32), 99, dtype=torch.int8, device="cuda")
-    pq.quantize_activations_combined_norm(x, G, gamma, beta, kseg, sp, sn, act=act, out=wide[:, :C])
-    assert torch.equal(wide[:, :C], want) and (wide[:, C:] == 99).all()
+    want = pq.quantize_activations(y16, kseg, sp, sn)
+    qp, qn, y = pq.quantize_activations_norm(x, G, gamma, beta, kseg, sp, sn, act=act, return_y=True)
+    assert torch.equal(qp, want[0]) and torch.equal(qn, want[1]) and torch.equal(y, y16)
+    wide = torch.full((2, B * S, C + 32), 99, dtype=torch.int8, device="cuda")
+    pq.quantize_activations_norm(x, G, gamma, beta, kseg, sp, sn, act=act, out=(wide[0, :, :C], wide[1, :, :C]))
+    for w, t in zip(wide, want):
+        assert torch.equal(w[:, :C], t) and (w[:, C:] == 99).all()
     assert pq.stream_status() == 0
 
 

@@ -63,15 +63,17 @@ def test_norm_workspace_size():
     assert L.load().sq_group_norm_workspace_size(2, 64, 1280, 32, 0, 0, None) == L.SQ_ERR_INVALID_ARG
 
 
-def codes(kb=(0, 64), C=64, c=FAKE, ldc=64, sp=FAKE, sn=FAKE, y=None, ldy=64, groups=8, ldx=64):
+def codes(kb=(0, 64), C=64, c=FAKE, n=FAKE, ldc=64, sp=FAKE, sn=FAKE, y=None, ldy=64, groups=8, ldx=64):
     s, keep = _seg(kb)
-    return L.load().sq_quantize_activations_combined_norm(FAKE, L.SQ_BF16, 2, 9, C, ldx, 9 * ldx, groups, None, None,
-                                                          1e-5, 0, ctypes.byref(s), sp, sn, c, ldc, y, ldy, None, 0,
+    return L.load().sq_quantize_activations_norm(FAKE, L.SQ_BF16, 2, 9, C, ldx, 9 * ldx, groups, None, None,
+                                                          1e-5, 0, ctypes.byref(s), sp, sn, c, n, ldc, y, ldy, None, 0,
                                                           None)
 
 
 def test_norm_codes_refusals():
     assert codes(c=None) == L.SQ_ERR_INVALID_ARG
+    assert codes(n=None) == L.SQ_ERR_INVALID_ARG
+    assert codes(n=FAKE + 8) == L.SQ_ERR_ALIGNMENT
     assert codes(sp=None) == L.SQ_ERR_INVALID_ARG
     assert codes(ldc=48) == L.SQ_ERR_INVALID_ARG
     assert codes(ldc=72) == L.SQ_ERR_ALIGNMENT
