@@ -269,10 +269,10 @@ def run(state):
             return pq.adapter_add(s["y"], s["x"], adapters, s["bounds"], s["index"])
         if op == "adapter_bwd":
             return pq.adapter_backward(s["dy"], s["x"], s["hidden"], adapters, s["bounds"], s["index"])
-        codes, x16 = pq.quantize_activations_combined_norm(
+        q_pos, q_neg, x16 = pq.quantize_activations_norm(
             s["x"], c["G"], s["gamma"], s["beta"], (0, c["C"]), s["s_pos"], s["s_neg"], eps=EPS,
             act=c["act"], return_y=True)
-        y = pq.linear_from_combined(codes, qw, s["s_pos"], s["s_neg"])
+        y = pq.linear_from_codes(q_pos, q_neg, qw, s["s_pos"], s["s_neg"])
         return pq.adapter_add(y, x16, adapters, s["bounds"], s["index"]), x16
     if op == "norm":
         return _norm(s).to(s["x"].dtype)
