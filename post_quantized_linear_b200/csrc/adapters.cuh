@@ -41,30 +41,61 @@ struct AdapterItem {
 
 // Item `slot` when requests are cut into pieces of T rows.  The rows before the
 // first request and behind the last count as two more requests, without an
-// adapter.  Request r's pieces begin at slot floor(start_r / T) + r: a request
-// of any length fits before the next one's, so the slot of every piece follows
-// from its own request's bounds alone and M / T + Q + 3 slots cover the batch.  A warp
-// finds the request by a 32-way search.  Pieces of a request with bounds outside
-// the batch or an index beyond the adapters are left out, so no read or write
-// leaves the tensors; check_requests raises the range status for them.
+// adapter.  Up to 62 requests: a warp counts the pieces of all of them and sums the
+// counts, so the items come without gaps.  More: request r's pieces begin at slot
+// floor(start_r / T) + r, which leaves room for a request of any length before the
+// next one's, so its own bounds alone place them and a 32-way search finds the
+// request of a slot.  M / T + Q + 3 slots hold every piece in both.
+// Pieces of a request with bounds outside the batch or an index beyond the adapters
+// are left out, so no read or write leaves the tensors; check_requests raises the
+// range status for them.
 __device__ __forceinline__ AdapterItem adapter_item(const AdapterArgs& p, int slot, int T) {
   const int lane = threadIdx.x & 31;
   const int count = p.Q + 2;
   auto start = [&](int r) { return r == 0 ? 0 : r <= p.Q + 1 ? __ldg(p.bounds + r - 1) : p.M; };
-  int lo = 0, span = count;
-  while (span > 1) {
-    const int step = (span + 31) >> 5;
-    const int r = lo + lane * step;
-    const bool le = lane * step < span && start(r) / T + r <= slot;
-    const unsigned m = __ballot_sync(0xffffffffu, le) | 1u;
-    const int k = 31 - __clz(m);
-    span = min(step, span - k * step);
-    lo += k * step;
-  }
-  const int s = start(lo), e = start(lo + 1);
   AdapterItem it;
-  it.l = (lo == 0 || lo == p.Q + 1) ? -1 : __ldg(p.index + lo - 1);
-  const int piece = slot - (s / T + lo);
+  int s, e, piece, lo;
+  if (count <= 64) {
+    // lane: requests 2 lane and 2 lane + 1
+    const int r = 2 * lane;
+    const int b0 = r < count ? start(r) : p.M, b1 = r < count ? start(r + 1) : p.M,
+              b2 = r + 1 < count ? start(r + 2) : p.M;
+    const int l0 = r >= 1 && r <= p.Q ? __ldg(p.index + r - 1) : -1, l1 = r + 1 <= p.Q ? __ldg(p.index + r) : -1;
+    const int n0 = max(0, b1 - b0 + T - 1) / T, n1 = max(0, b2 - b1 + T - 1) / T;
+    int sum = n0 + n1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, sum > slot);
+    it.row = it.n = 0;
+    it.l = -1;
+    if (m == 0) return it;
+    const int src = __ffs(m) - 1;
+    const int first = slot - (sum - n0 - n1);              // within the lane's two requests
+    const bool second = first >= n0;
+    s = __shfl_sync(0xffffffffu, second ? b1 : b0, src);
+    e = __shfl_sync(0xffffffffu, second ? b2 : b1, src);
+    it.l = __shfl_sync(0xffffffffu, second ? l1 : l0, src);
+    piece = __shfl_sync(0xffffffffu, second ? first - n0 : first, src);
+  } else {
+    lo = 0;
+    int span = count;
+    while (span > 1) {
+      const int step = (span + 31) >> 5;
+      const int r = lo + lane * step;
+      const bool le = lane * step < span && start(r) / T + r <= slot;
+      const unsigned m = __ballot_sync(0xffffffffu, le) | 1u;
+      const int k = 31 - __clz(m);
+      span = min(step, span - k * step);
+      lo += k * step;
+    }
+    s = start(lo);
+    e = start(lo + 1);
+    it.l = (lo == 0 || lo == p.Q + 1) ? -1 : __ldg(p.index + lo - 1);
+    piece = slot - (s / T + lo);
+  }
   it.row = s + piece * T;
   it.n = min(T, e - it.row);
   if (s < 0 || e > p.M || it.l >= p.L || piece < 0 || it.n < 0) it.n = 0;

@@ -43,6 +43,15 @@ __device__ __forceinline__ float4 dsmem_f32x4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void dsmem_store_u32x4(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3])
+               : "memory");
+}
+// Orders this thread's generic-proxy accesses, to any CTA of the cluster, with the
+// async proxy's.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
 constexpr int kTileRows = 128;
 constexpr int kTileThreads = 320;          // TMA warp, MMA warp, eight epilogue warps
 constexpr int kTileEpiWarps = 8;
@@ -59,14 +68,11 @@ struct AdapterTileArgs {
   int32_t starve;
 };
 
-// Shared memory between the two products: this CTA's partial h in fp32, four columns
-// of a row together and rows next to one another (a warp reads 512 contiguous bytes
-// of a peer; with rows of R values it read 32 pieces of 16 bytes, and the first
-// product's sums over the cluster took most of the kernel: 100 us instead of TBD at
-// 8192 x 4608 x 1152, rank 64), then h as `parts` bf16 operand tiles.
-__host__ __device__ inline int adapter_h_bytes(int rp, int parts, int cs) {
+// Shared memory between the two products: this CTA's partial h in fp32 (rows padded
+// by 16 bytes against bank conflicts), then h as `parts` bf16 operand tiles.
+__host__ __device__ inline int adapter_h_bytes(int rp, int parts) {
   const int op = parts * kTileX * ((rp + 63) / 64);
-  const int ex = cs > 1 ? kTileRows * rp * 4 : 0;
+  const int ex = kTileRows * (rp + 4) * 4;
   return ((op > ex ? op : ex) + 1023) / 1024 * 1024;
 }
 
@@ -112,7 +118,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
   }
   const int RP = (R + 15) & ~15, rt = (RP + 63) / 64;
   uint8_t* hbuf = smem + NS * args.slot_bytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(hbuf + adapter_h_bytes(RP, args.parts, cs));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(hbuf + adapter_h_bytes(RP, args.parts));
   uint64_t* full = bars;             // [4]
   uint64_t* empty1 = full + 4;       // [4] slot free after a tile of the first product
   uint64_t* empty3 = empty1 + 4;     // [4] slot free after a tile of the second
@@ -137,7 +143,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
       mbar_init(smem_u32(d_empty + i), kTileEpiWarps);
     }
     mbar_init(smem_u32(h_full), 1);
-    mbar_init(smem_u32(h_ready), kTileEpiWarps);
+    mbar_init(smem_u32(h_ready), kTileEpiWarps * cs);
     mbar_init(smem_u32(p_full), kTileEpiWarps * cs);
     mbar_init(smem_u32(p_free), kTileEpiWarps * cs);
     mbar_init(smem_u32(drain_bar), 1);
@@ -220,7 +226,8 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
       }
       if (ok) {
         umma_commit(smem_u32(h_full));
-        ok = wait1(smem_u32(h_ready), 0, abort_flag, budget);
+        ok = wait1s<true>(smem_u32(h_ready), 0, abort_flag, budget);
+        fence_proxy_async_all();
         tc_fence_after();
       }
       const uint32_t id2 = idesc_bf16(kTileRows, BN) | (BWD ? kIdescBMn : 0u);
@@ -251,78 +258,88 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
     const int quad = warp & 3, half = (warp - 2) >> 2;
     const int row = quad * 32 + lane;
     const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-    const int hc = RP / 2, c0 = half * hc;    // this thread's columns of h
+    const int hc = RP / 2, c0 = half * hc;    // this thread's columns of the partial h
     bool ok = wait_warp(smem_u32(h_full), 0, abort_flag, budget);
     if (ok) {
       tc_fence_after();
-      float v[RB / 2];
+      // 1. this CTA's share of h, into its own shared memory
+      const int pitch = RP + 4;
+      float* mine = reinterpret_cast<float*>(hbuf) + row * pitch + c0;
 #pragma unroll
       for (int c = 0; c < RB / 2; c += 8) {
-        uint32_t u[8];
-        if (c < hc) tmem_ld8(t_lane + c0 + c, u);
-        tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[c + k] = c < hc ? __uint_as_float(u[k]) : 0.0f;
-      }
-      if (cs > 1) {
-        float4* mine = reinterpret_cast<float4*>(hbuf) + (c0 / 4) * kTileRows + row;
-#pragma unroll
-        for (int c = 0; c < RB / 2; c += 4)
-          if (c < hc) mine[(c / 4) * kTileRows] = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
-        __syncwarp();
-        if (lane < cs) mbar_arrive_remote(mapa_shared(smem_u32(p_full), lane));
-        ok = wait_warp<true>(smem_u32(p_full), 0, abort_flag, budget);
-        if (ok) {
-#pragma unroll
-          for (int c = 0; c < RB / 2; ++c) v[c] = 0.0f;
-          for (int k = 0; k < cs; ++k) {
-            const uint32_t from = mapa_shared(smem_u32(mine), k);
-#pragma unroll
-            for (int c = 0; c < RB / 2; c += 4)
-              if (c < hc) {
-                const float4 o = dsmem_f32x4(from + (c / 4) * kTileRows * 16);
-                v[c] += o.x; v[c + 1] += o.y; v[c + 2] += o.z; v[c + 3] += o.w;
-              }
-          }
-          __syncwarp();
-          if (lane < cs) mbar_arrive_remote(mapa_shared(smem_u32(p_free), lane));
-          ok = wait_warp<true>(smem_u32(p_free), 0, abort_flag, budget);
+        if (c < hc) {
+          uint32_t u[8];
+          tmem_ld8(t_lane + c0 + c, u);
+          tmem_wait_ld();
+          *reinterpret_cast<uint4*>(mine + c) = make_uint4(u[0], u[1], u[2], u[3]);
+          *reinterpret_cast<uint4*>(mine + c + 4) = make_uint4(u[4], u[5], u[6], u[7]);
         }
       }
-      if (ok) {
-        const float scale = p.scale != nullptr ? __ldg(p.scale + it.l) : 1.0f;
-        // each CTA of the cluster stores its share of the rows of h (u)
-        const bool keep = p.h != nullptr && row < it.n && row * cs / kTileRows == rank;
-        float* hg = p.h + (int64_t)(it.row + row) * R;
+      tc_fence_before();
+      __syncwarp();
+      if (lane < cs) mbar_arrive_remote(mapa_shared(smem_u32(p_full), lane));
+      ok = wait_warp<true>(smem_u32(p_full), 0, abort_flag, budget);
+    }
+    if (ok) {
+      // 2. each CTA adds its share of the rows over the cluster, in rank order: units of
+      // eight columns of a row, whole rows side by side, so that a warp reads long runs
+      // of a peer's memory
+      const int et = threadIdx.x - 64, octs = RP / 8;
+      const int units = it.n * octs;
+      const int u0 = (int)((int64_t)rank * units / cs), u1 = (int)((int64_t)(rank + 1) * units / cs);
+      constexpr int MAXU = kTileRows * (RB / 8) / 256;
+      float v[MAXU][8];
 #pragma unroll
-        for (int c = 0; c < RB / 2; c += 8) {
-          if (c < hc) {
-            const int col = c0 + c;
+      for (int k = 0; k < MAXU; ++k) {
+        const int u = u0 + et + 256 * k;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
+        if (u < u1) {
+          const uint32_t at = smem_u32(hbuf) + ((u / octs) * (RP + 4) + (u % octs) * 8) * 4;
+          for (int q = 0; q < cs; ++q) {
+            const uint32_t from = mapa_shared(at, q);
+            const float4 a = dsmem_f32x4(from), b = dsmem_f32x4(from + 16);
+            v[k][0] += a.x; v[k][1] += a.y; v[k][2] += a.z; v[k][3] += a.w;
+            v[k][4] += b.x; v[k][5] += b.y; v[k][6] += b.z; v[k][7] += b.w;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane < cs) mbar_arrive_remote(mapa_shared(smem_u32(p_free), lane));
+      const float scale = p.scale != nullptr ? __ldg(p.scale + it.l) : 1.0f;
+      ok = wait_warp<true>(smem_u32(p_free), 0, abort_flag, budget);
+      if (ok) {
+        // 3. the sums, scaled and cut into bf16 parts, into every CTA's operand
+#pragma unroll
+        for (int k = 0; k < MAXU; ++k) {
+          const int u = u0 + et + 256 * k;
+          if (u < u1) {
+            const int hr = u / octs, col = (u % octs) * 8;
             float o[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float scaled = v[c + k] * scale;
-              o[k] = BWD ? scaled : v[c + k];
-              v[c + k] = col < R ? scaled : 0.0f;   // the padding of the rank is an operand, too
+            for (int j = 0; j < 8; ++j) {
+              const float scaled = v[k][j] * scale;
+              o[j] = BWD ? scaled : v[k][j];
+              v[k][j] = col < R ? scaled : 0.0f;   // the padding of the rank is an operand, too
             }
-            if (keep && col < R) store_vec<8>(hg, col, false, o);
-            uint8_t* d = hbuf + (col >> 6) * kTileX + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4);
+            if (p.h != nullptr && col < R)
+              store_vec<8>(p.h, (int64_t)(it.row + hr) * R + col, false, o);
+            const uint32_t d = smem_u32(hbuf) + (col >> 6) * kTileX + hr * 128 + ((((col & 63) >> 3) ^ (hr & 7)) << 4);
             for (int part = 0; part < args.parts; ++part) {
               uint32_t w[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                w[k] = pack_bf16(v[c + 2 * k], v[c + 2 * k + 1]);
-                v[c + 2 * k] -= __uint_as_float(w[k] << 16);
-                v[c + 2 * k + 1] -= __uint_as_float(w[k] & 0xFFFF0000u);
+              for (int j = 0; j < 4; ++j) {
+                w[j] = pack_bf16(v[k][2 * j], v[k][2 * j + 1]);
+                v[k][2 * j] -= __uint_as_float(w[j] << 16);
+                v[k][2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
               }
-              *reinterpret_cast<uint4*>(d + part * rt * kTileX) = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int q = 0; q < cs; ++q) dsmem_store_u32x4(mapa_shared(d + part * rt * kTileX, q), w);
             }
           }
         }
-        tc_fence_before();
-        fence_proxy_async_smem();
+        fence_proxy_async_all();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(h_ready));
+        if (lane < cs) mbar_arrive_remote(mapa_shared(smem_u32(h_ready), lane));
       }
     }
     const int rows = min(32, it.n - quad * 32);     // rows of the piece in this quarter (may be < 1)

@@ -85,6 +85,40 @@ sq_status make_adapter_map(CUtensorMap* map, sq_dtype t, const void* base, int r
 
 constexpr int kSmemPerSm = 227 * 1024;
 
+// How many clusters of cs CTAs of a kernel the device holds at once with one CTA on an
+// SM (which is what the query counts for clusters), asked once per device and size of
+// shared memory (per kernel, the last one asked for).
+template <auto KERN>
+int resident_clusters(int cs, int threads, int smem) {
+  static std::atomic<uint64_t> known[kMaxDevices][9] = {};   // smem << 32 | clusters + 1
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || cs > 8) return 0;
+  const uint64_t v = known[dev][cs].load(std::memory_order_relaxed);
+  if (v != 0 && (int)(v >> 32) == smem) return (int)(v & 0xFFFFFFFFu) - 1;
+  if (smem_limit<KERN>(kSmemPerSm) != cudaSuccess) return 0;
+  // the answer, and what the device really holds, go by the kernel's carve-out
+  if (cudaFuncSetAttribute(KERN, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
+    (void)cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(cs * 1024));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, KERN, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    n = num_sms() / cs;
+  }
+  known[dev][cs].store((uint64_t)smem << 32 | (uint64_t)(n + 1), std::memory_order_relaxed);
+  return n;
+}
+
 template <int RB, typename YT, bool BWD>
 sq_status launch_tile_rb(const sq::AdapterArgs& a, const CUtensorMap& tx, const CUtensorMap& tw1,
                          const CUtensorMap& tw2, const CUtensorMap& ty, cudaStream_t s) {
@@ -97,18 +131,18 @@ sq_status launch_tile_rb(const sq::AdapterArgs& a, const CUtensorMap& tx, const 
   t.slot_bytes = sq::kTileX + (RB == 64 ? 8192 : 16384);
   t.wait_budget = g_wait_budget;
   t.starve = g_debug_starve;
-  // Pieces expected: the batch cut into 128 rows, or one per request.  The
-  // cluster grows until two CTAs per SM (one at ranks above 64) have work.
-  const int64_t pieces = std::max<int64_t>((a.M + sq::kTileRows - 1) / sq::kTileRows, std::min<int64_t>(a.Q, a.M));
-  const int64_t want = (int64_t)num_sms() * (RB == 64 ? 2 : 1);
-  const int most = std::min({8, (D + 63) / 64, (E + 128 / (int)sizeof(YT) - 1) / (128 / (int)sizeof(YT))});
-  int cs = 1;
-  while (cs * 2 <= most && pieces * cs * 2 <= want) cs *= 2;
-  t.cs = cs;
-  const int rest = sq::adapter_h_bytes(rp, t.parts, cs) + sq::kTileBars + 1024;
+  const int rest = sq::adapter_h_bytes(rp, t.parts) + sq::kTileBars + 1024;
   const bool two = RB == 64 && 3 * t.slot_bytes + rest <= kSmemPerSm / 2 - 1024;
   t.stages = two ? 3 : 4 * t.slot_bytes + rest <= kSmemPerSm ? 4 : 3;
   const int smem = t.stages * t.slot_bytes + rest;
+  // Pieces expected: the batch cut into 128 rows, or one per request.  The largest
+  // cluster whose pieces are all resident at once: a second wave of a few clusters
+  // costs a whole pass.
+  const int64_t pieces = std::max<int64_t>((a.M + sq::kTileRows - 1) / sq::kTileRows, std::min<int64_t>(a.Q, a.M));
+  const int most = std::min({8, (D + 63) / 64, (E + 128 / (int)sizeof(YT) - 1) / (128 / (int)sizeof(YT))});
+  int cs = std::max(1, most);
+  while (cs > 1 && pieces > (two ? 2 : 1) * resident_clusters<kern>(cs, sq::kTileThreads, smem)) --cs;
+  t.cs = cs;
   cudaError_t e = smem_limit<kern>(kSmemPerSm);
   if (e != cudaSuccess) return cuda_status(e);
   const int64_t slots = (int64_t)a.M / sq::kTileRows + a.Q + 3;

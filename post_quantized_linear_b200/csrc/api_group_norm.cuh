@@ -4,8 +4,10 @@
 
 namespace {
 
+constexpr int kNormSmem = 227 * 1024;
+
 // How a [B, S, C] map is cut.  cluster = true: a cluster of cs CTAs holds the
-// slab of an image and channel block in registers, nv vectors per thread.
+// slab of an image and channel block in shared memory, nv vectors per thread.
 struct NormPlan {
   sq::NormTile t;
   int cs, nv, tiles;
@@ -15,8 +17,11 @@ struct NormPlan {
 
 int gcd_i(int a, int b) { return b == 0 ? a : gcd_i(b, a % b); }
 
-// The largest block of channels a CTA's threads span, in 16-byte vectors.
-constexpr int kNormMaxVectors = sq::kNormThreads;
+// Shared memory of a cluster CTA: `tensors` slabs of nv vectors per thread, and the
+// reductions.
+int norm_cluster_smem(const sq::NormTile& t, int nv, int vn, int tensors) {
+  return nv * sq::kNormThreads * 16 * tensors + 4 * sq::norm_smem_floats(sq::kNormThreads, t.vx, vn, t.nb);
+}
 
 // Chooses the tiles of `tensors` read (1 forward: x; 2 backward: x and dy).
 sq_status norm_plan(int64_t B, int64_t S, int64_t C, int32_t groups, int es, int tensors, NormPlan* out) {
@@ -24,41 +29,41 @@ sq_status norm_plan(int64_t B, int64_t S, int64_t C, int32_t groups, int es, int
   const int cpg = (int)(C / groups);
   const int unit = vn / gcd_i(vn, cpg);                 // groups in whole vectors
   const int64_t unit_vec = (int64_t)unit * cpg / vn;
-  if (unit_vec > kNormMaxVectors) return SQ_ERR_UNSUPPORTED;
+  if (unit_vec > sq::kNormThreadsMax) return SQ_ERR_UNSUPPORTED;
   const int blocks_all = groups / unit;                 // C is a multiple of the vector
   const int sms = num_sms();
   NormPlan best = {};
   double best_us = 1e30;
-  const int max_nv = tensors == 1 ? 16 : 8;
   for (int m = 1; m <= blocks_all; ++m) {
     if (blocks_all % m != 0) continue;
     const int64_t vx = unit_vec * m;
-    if (vx > kNormMaxVectors / 2) break;
+    if (vx > sq::kNormThreads) break;
     const int ty = (int)(sq::kNormThreads / vx);
     for (int cs = 1; cs <= 8; cs *= 2) {
       const int64_t rows = (S + cs - 1) / cs;
-      const int64_t need = (rows + ty - 1) / ty;
-      if (need > max_nv) continue;
+      const int64_t nv = (rows + ty - 1) / ty;
       if (cs > 1 && (int64_t)(cs - 1) * rows >= S) continue;   // a CTA without rows
-      int nv = 1;
-      while (nv < need) nv *= 2;
+      if (nv > 64) continue;
+      const sq::NormTile t{(int32_t)S, (int32_t)C, groups, cpg, unit * m, (int32_t)vx, ty, (int32_t)rows};
+      const int smem = norm_cluster_smem(t, (int)nv, vn, tensors) + 1024;
+      if (smem > kNormSmem) continue;
       // Estimated time: waves of resident CTAs, each the latency of its loads,
-      // reductions and stores (2 us, measured at the smallest maps) and of the
-      // cluster barriers, plus its traffic at an SM's share of the copy rate
-      // (44 KB/us); narrow blocks waste part of the 32-byte sectors.
-      const int res = tensors == 1 && nv <= 4 ? 2 : 1;
+      // reductions and stores and of the cluster barriers (measured at the smallest
+      // maps), plus its traffic at an SM's share of the copy rate (44 KB/us); narrow
+      // blocks waste part of the 32-byte sectors.
+      const int res = std::min(tensors == 1 ? 3 : 2, kNormSmem / smem);
       const int64_t ctas = B * (blocks_all / m) * cs;
       const int64_t waves = (ctas + (int64_t)sms * res - 1) / ((int64_t)sms * res);
       const double on_sm = (double)std::min<int64_t>(res, (ctas + sms - 1) / sms);
       const int chunk = (int)vx * 16;
       const double waste = chunk % 32 == 0 || chunk >= C * es ? 1.0 : (double)((chunk + 31) / 32 * 32 + 16) / chunk;
       const double kb = (double)rows * chunk * (tensors + 1) / 1024.0 * waste;
-      const double us = (double)waves * (2.0 + (cs > 1 ? 0.5 : 0.0) + on_sm * kb / 44.0);
+      const double us = (double)waves * (2.0 + (cs > 1 ? 1.0 : 0.0) + on_sm * kb / 44.0);
       if (us < best_us) {
         best_us = us;
-        best.t = sq::NormTile{(int32_t)S, (int32_t)C, groups, cpg, unit * m, (int32_t)vx, ty, (int32_t)rows};
+        best.t = t;
         best.cs = cs;
-        best.nv = nv;
+        best.nv = (int)nv;
         best.tiles = 1;
         best.cluster = true;
       }
@@ -73,14 +78,17 @@ sq_status norm_plan(int64_t B, int64_t S, int64_t C, int32_t groups, int es, int
     return SQ_OK;
   }
   NormPlan p = {};
-  p.threads = unit_vec <= sq::kNormThreads2 ? sq::kNormThreads2 : sq::kNormThreads;
+  p.threads = unit_vec <= sq::kNormThreads ? sq::kNormThreads : sq::kNormThreadsMax;
   int m = 1;
   for (int k = 1; k <= blocks_all; ++k)
     if (blocks_all % k == 0 && unit_vec * k <= p.threads) m = k;
   const int vx = (int)(unit_vec * m), ty = p.threads / vx;
   const int64_t cols = (int64_t)B * (blocks_all / m);
   // one wave of resident CTAs, each a whole number of thread rows
-  const int64_t resident = (int64_t)sms * (p.threads == sq::kNormThreads ? 1 : tensors == 1 ? 3 : 2);
+  const int smem = sq::norm_ring_bytes(p.threads, tensors == 1 ? sq::kNormU1 : sq::kNormU2, tensors) +
+                   4 * sq::norm_smem_floats(p.threads, vx, vn, unit * m) + 1024;
+  const int64_t resident =
+      (int64_t)sms * std::min(p.threads != sq::kNormThreads ? 1 : tensors == 1 ? 3 : 2, kNormSmem / smem);
   int64_t tiles = std::max<int64_t>(1, resident / cols);
   int64_t rows = (S + tiles - 1) / tiles;
   rows = (rows + ty - 1) / ty * ty;
@@ -112,7 +120,7 @@ template <auto KERN, typename... Args>
 sq_status launch_grid(dim3 grid, int threads, int smem, int cluster, bool dependent, cudaStream_t stream,
                       Args... args) {
   if (smem > 48 * 1024) {
-    cudaError_t e = smem_limit<KERN>(200 * 1024);
+    cudaError_t e = smem_limit<KERN>(227 * 1024);
     if (e != cudaSuccess) return cuda_status(e);
   }
   cudaLaunchConfig_t cfg = {};
@@ -141,11 +149,12 @@ sq_status launch_grid(dim3 grid, int threads, int smem, int cluster, bool depend
 
 template <typename XT, int NT>
 sq_status norm_forward_two(const NormPlan& pl, int64_t B, const sq::NormArgs& a, cudaStream_t s) {
-  const int smem = 4 * sq::norm_smem_floats(NT, pl.t.vx, sq::Vec<XT>::n, pl.t.nb);
+  const int ring = sq::norm_ring_bytes(NT, sq::kNormU1, 1);
+  const int smem = ring + 4 * sq::norm_smem_floats(NT, pl.t.vx, sq::Vec<XT>::n, pl.t.nb);
   const dim3 grid((unsigned)pl.tiles, (unsigned)(pl.t.G / pl.t.nb), (unsigned)B);
   sq_status st = launch_grid<sq::group_norm_stats_kernel<XT, NT>>(grid, NT, smem, 1, false, s, a);
   if (st != SQ_OK) return st;
-  return launch_grid<sq::group_norm_apply_kernel<XT, NT>>(grid, NT, 8 * pl.t.nb, 1, true, s, a);
+  return launch_grid<sq::group_norm_apply_kernel<XT, NT>>(grid, NT, ring + 8 * pl.t.nb, 1, true, s, a);
 }
 
 template <typename XT>
@@ -153,18 +162,12 @@ sq_status norm_forward(const NormPlan& pl, int64_t B, sq::NormArgs& a, cudaStrea
   a.t = pl.t;
   a.tiles = pl.tiles;
   if (!pl.cluster)
-    return pl.threads == sq::kNormThreads2 ? norm_forward_two<XT, sq::kNormThreads2>(pl, B, a, s)
-                                           : norm_forward_two<XT, sq::kNormThreads>(pl, B, a, s);
-  constexpr int nt = sq::kNormThreads;
-  const int smem = 4 * sq::norm_smem_floats(nt, pl.t.vx, sq::Vec<XT>::n, pl.t.nb), cs = pl.cs;
-  const dim3 grid((unsigned)(pl.t.G / pl.t.nb * cs), (unsigned)B);
-  switch (pl.nv) {
-    case 1: return launch_grid<sq::group_norm_cluster_kernel<XT, 1>>(grid, nt, smem, cs, false, s, a, cs);
-    case 2: return launch_grid<sq::group_norm_cluster_kernel<XT, 2>>(grid, nt, smem, cs, false, s, a, cs);
-    case 4: return launch_grid<sq::group_norm_cluster_kernel<XT, 4>>(grid, nt, smem, cs, false, s, a, cs);
-    case 8: return launch_grid<sq::group_norm_cluster_kernel<XT, 8>>(grid, nt, smem, cs, false, s, a, cs);
-    default: return launch_grid<sq::group_norm_cluster_kernel<XT, 16>>(grid, nt, smem, cs, false, s, a, cs);
-  }
+    return pl.threads == sq::kNormThreads ? norm_forward_two<XT, sq::kNormThreads>(pl, B, a, s)
+                                          : norm_forward_two<XT, sq::kNormThreadsMax>(pl, B, a, s);
+  const dim3 grid((unsigned)(pl.t.G / pl.t.nb * pl.cs), (unsigned)B);
+  return launch_grid<sq::group_norm_cluster_kernel<XT>>(grid, sq::kNormThreads,
+                                                        norm_cluster_smem(pl.t, pl.nv, sq::Vec<XT>::n, 1), pl.cs,
+                                                        false, s, a, pl.cs, pl.nv);
 }
 
 sq_status norm_params(const sq::NormBwdArgs& a, int64_t B, float* dgamma, float* dbeta, cudaStream_t s) {
@@ -177,10 +180,12 @@ sq_status norm_backward_two(const NormPlan& pl, int64_t B, const sq::NormBwdArgs
                             cudaStream_t s) {
   constexpr int vn = sq::Vec<XT>::n;
   const dim3 grid((unsigned)pl.tiles, (unsigned)(pl.t.G / pl.t.nb), (unsigned)B);
-  const int smem = 4 * sq::norm_smem_floats(NT, pl.t.vx, vn, pl.t.nb);
+  const int ring = sq::norm_ring_bytes(NT, sq::kNormU2, 2);
+  const int smem = ring + 4 * sq::norm_smem_floats(NT, pl.t.vx, vn, pl.t.nb);
   sq_status st = launch_grid<sq::group_norm_bwd_sums_kernel<XT, NT>>(grid, NT, smem, 1, false, s, a);
   if (st != SQ_OK || (st = norm_params(a, B, dgamma, dbeta, s)) != SQ_OK) return st;
-  return launch_grid<sq::group_norm_bwd_apply_kernel<XT, NT>>(grid, NT, 8 * (pl.t.vx * vn + pl.t.nb), 1, true, s, a);
+  return launch_grid<sq::group_norm_bwd_apply_kernel<XT, NT>>(grid, NT, ring + 8 * (pl.t.vx * vn + pl.t.nb), 1, true, s,
+                                                              a);
 }
 
 template <typename XT>
@@ -189,18 +194,12 @@ sq_status norm_backward(const NormPlan& pl, int64_t B, sq::NormBwdArgs& a, float
   a.t = pl.t;
   a.tiles = pl.cluster ? 0 : pl.tiles;
   if (!pl.cluster)
-    return pl.threads == sq::kNormThreads2 ? norm_backward_two<XT, sq::kNormThreads2>(pl, B, a, dgamma, dbeta, s)
-                                           : norm_backward_two<XT, sq::kNormThreads>(pl, B, a, dgamma, dbeta, s);
-  constexpr int nt = sq::kNormThreads;
-  const int smem = 4 * sq::norm_smem_floats(nt, pl.t.vx, sq::Vec<XT>::n, pl.t.nb), cs = pl.cs;
-  const dim3 grid((unsigned)(pl.t.G / pl.t.nb * cs), (unsigned)B);
-  sq_status st;
-  switch (pl.nv) {
-    case 1: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 1>>(grid, nt, smem, cs, false, s, a, cs); break;
-    case 2: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 2>>(grid, nt, smem, cs, false, s, a, cs); break;
-    case 4: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 4>>(grid, nt, smem, cs, false, s, a, cs); break;
-    default: st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT, 8>>(grid, nt, smem, cs, false, s, a, cs); break;
-  }
+    return pl.threads == sq::kNormThreads
+               ? norm_backward_two<XT, sq::kNormThreads>(pl, B, a, dgamma, dbeta, s)
+               : norm_backward_two<XT, sq::kNormThreadsMax>(pl, B, a, dgamma, dbeta, s);
+  const dim3 grid((unsigned)(pl.t.G / pl.t.nb * pl.cs), (unsigned)B);
+  sq_status st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT>>(
+      grid, sq::kNormThreads, norm_cluster_smem(pl.t, pl.nv, sq::Vec<XT>::n, 2), pl.cs, false, s, a, pl.cs, pl.nv);
   if (st != SQ_OK || (dgamma == nullptr && dbeta == nullptr)) return st;
   return norm_params(a, B, dgamma, dbeta, s);
 }

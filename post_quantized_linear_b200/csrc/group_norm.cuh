@@ -10,11 +10,16 @@
 //   of dz gamma_c and dz gamma_c xhat
 //
 // Everything here is bound by memory: an element costs about ten instructions.
-// Where the slab of one image and one block of groups fits the registers of a
+// Where the slab of one image and one block of groups fits the shared memory of a
 // cluster of CTAs, it is read once, the cluster exchanges the group's sums
-// through distributed shared memory and writes the result from registers (one
+// through distributed shared memory and writes the result from the slab (one
 // launch, no workspace).  Larger maps take two passes, the second reading what
 // the first left in L2.  Every sum has a fixed order: results repeat bit for bit.
+//
+// Data moves with 16-byte cp.async copies whose words only the copying thread reads:
+// no barrier, no registers held, loops that stay small (the slab in registers, fully
+// unrolled, spent most of its time fetching instructions: 18 us instead of TBD on
+// 3 x 1023 x 1152 fp32).
 #pragma once
 
 #include <cstdint>
@@ -27,8 +32,8 @@
 
 namespace sq {
 
-constexpr int kNormThreads = 512;    // of the cluster form
-constexpr int kNormThreads2 = 256;   // of the two-pass form (512 for groups wider than 256 vectors)
+constexpr int kNormThreads = 256;     // 512 in two passes over groups wider than 256 vectors
+constexpr int kNormThreadsMax = 512;
 constexpr int ACT_NONE = 0;
 
 // One block of channels (whole groups, a multiple of 16 bytes wide) and how a
@@ -88,6 +93,34 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+// A 16-byte vector as pairs of fp32 values.
+template <typename XT>
+__device__ __forceinline__ void load_pairs(const uint4& u, uint64_t (&v)[Vec<XT>::n / 2]) {
+  if constexpr (Vec<XT>::n == 8) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  } else {
+    v[0] = f2_pack(__uint_as_float(u.x), __uint_as_float(u.y));
+    v[1] = f2_pack(__uint_as_float(u.z), __uint_as_float(u.w));
+  }
+}
+template <int VN>
+__device__ __forceinline__ void unpack_pairs(const uint64_t (&v)[VN / 2], float (&o)[VN]) {
+#pragma unroll
+  for (int i = 0; i < VN / 2; ++i) f2_unpack(v[i], o[2 * i], o[2 * i + 1]);
+}
+// Waits until at most N groups of this thread's copies are in flight.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
 // VN consecutive fp32 values (4 or 8) stored as bf16 or fp32.
 template <int VN>
 __device__ __forceinline__ void store_vec(void* y, int64_t at, bool bf16, const float (&v)[VN]) {
@@ -110,21 +143,60 @@ __device__ __forceinline__ void store_vec(void* y, int64_t at, bool bf16, const 
 }
 
 // -------------------------------------------------------------- activations
-// exp and the quotient by CUDA's fast forms (relative error about 2^-21): the
-// result is stored in bf16, or in fp32 within 1e-6 of its scale.
+// Pairs of fp32 values in 64 bits (one packed instruction for both).
+__device__ __forceinline__ uint64_t f2_both(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// erfc(|z| / sqrt 2) and exp(-z^2 / 2): Abramowitz and Stegun, Handbook of
+// Mathematical Functions, 7.1.26, P(t) exp(-x^2) with t = 1 / (1 + p x), off by at most
+// 1.5e-7; the tail keeps its own scale, since P multiplies the exponential.
+__device__ __forceinline__ float erfc_half(float z, float& e) {
+  const float x = fabsf(z) * 0.70710678f;
+  const float t = rcp_ftz(fmaf(0.3275911f, x, 1.0f));
+  e = ex2_ftz(z * z * (-0.5f * kLog2e));
+  const float p = fmaf(fmaf(fmaf(fmaf(1.061405429f, t, -1.453152027f), t, 1.421413741f), t, -0.284496736f), t,
+                       0.254829592f);
+  return p * t * e;
+}
+
+// act(z) and act'(z).  The hardware's exponential and reciprocal (relative error about
+// 2^-22 each): the result is stored in bf16, or in fp32 within 1e-6 of its scale.
 template <int ACT>
-__device__ __forceinline__ float norm_act(float z) {
-  if constexpr (ACT == ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
-  else if constexpr (ACT == ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-  else return z;
+__device__ __forceinline__ uint64_t norm_act(uint64_t z2) {
+  float z0, z1;
+  if constexpr (ACT == ACT_SILU) {               // z / (1 + exp(-z))
+    float a, b;
+    f2_unpack(f2_mul(z2, f2_both(-kLog2e)), a, b);
+    f2_unpack(f2_add(f2_pack(ex2_ftz(a), ex2_ftz(b)), f2_both(1.0f)), a, b);
+    return f2_mul(z2, f2_pack(rcp_ftz(a), rcp_ftz(b)));
+  } else if constexpr (ACT == ACT_GELU) {        // max(z, 0) - |z| erfc(|z| / sqrt 2) / 2
+    f2_unpack(z2, z0, z1);
+    float e;
+    const float h0 = 0.5f * fabsf(z0) * erfc_half(z0, e), h1 = 0.5f * fabsf(z1) * erfc_half(z1, e);
+    return f2_pack(fmaxf(z0, 0.0f) - h0, fmaxf(z1, 0.0f) - h1);
+  } else {
+    return z2;
+  }
 }
 template <int ACT>
 __device__ __forceinline__ float norm_act_slope(float z) {
   if constexpr (ACT == ACT_SILU) {
-    const float p = __fdividef(1.0f, 1.0f + __expf(-z));
+    const float p = rcp_ftz(1.0f + ex2_ftz(-kLog2e * z));
     return p * fmaf(z, 1.0f - p, 1.0f);
   } else if constexpr (ACT == ACT_GELU) {
-    return fmaf(z * 0.39894228f, __expf(-0.5f * z * z), fmaf(0.5f, erff(z * 0.70710678f), 0.5f));
+    float e;
+    const float h = 0.5f * erfc_half(z, e);
+    return fmaf(z * 0.39894228f, e, z >= 0.0f ? 1.0f - h : h);
   } else {
     return 1.0f;
   }
@@ -257,14 +329,21 @@ __device__ __forceinline__ void cluster_wait() {
 // with b = beta - mean a, off by 2^-24 of |mean a| like the mean itself.
 template <int VN>
 struct NormOut {
-  float a[VN], b[VN], rp, rn;
+  uint64_t a[VN / 2], b[VN / 2];
+  float rp, rn;
   __device__ __forceinline__ void init(const NormArgs& p, int c0, int lc, const float* mean_g,
                                        const float* rstd_g) {
+    float av[VN], bv[VN];
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
       const int g = (lc + i) / p.t.cpg, c = c0 + lc + i;
-      a[i] = rstd_g[g] * (p.gamma ? __ldg(p.gamma + c) : 1.0f);
-      b[i] = fmaf(-mean_g[g], a[i], p.beta ? __ldg(p.beta + c) : 0.0f);
+      av[i] = rstd_g[g] * (p.gamma ? __ldg(p.gamma + c) : 1.0f);
+      bv[i] = fmaf(-mean_g[g], av[i], p.beta ? __ldg(p.beta + c) : 0.0f);
+    }
+#pragma unroll
+    for (int i = 0; i < VN / 2; ++i) {
+      a[i] = f2_pack(av[2 * i], av[2 * i + 1]);
+      b[i] = f2_pack(bv[2 * i], bv[2 * i + 1]);
     }
     rp = rn = 0.0f;
     if (p.q_pos != nullptr) {
@@ -274,11 +353,14 @@ struct NormOut {
       rn = sn > 0.0f ? __frcp_rn(sn) : 0.0f;
     }
   }
-  template <int ACT>
-  __device__ __forceinline__ void put(const NormArgs& p, int img, int row, int c, const float (&x)[VN]) {
-    float v[VN];
+  template <int ACT, typename XT>
+  __device__ __forceinline__ void put(const NormArgs& p, int img, int row, int c, const uint4& raw) const {
+    uint64_t x[VN / 2];
+    load_pairs<XT>(raw, x);
 #pragma unroll
-    for (int i = 0; i < VN; ++i) v[i] = norm_act<ACT>(fmaf(x[i], a[i], b[i]));
+    for (int i = 0; i < VN / 2; ++i) x[i] = norm_act<ACT>(f2_fma(x[i], a[i], b[i]));
+    float v[VN];
+    unpack_pairs<VN>(x, v);
     if (p.q_pos != nullptr) {
       // the codes are those of the bf16 values that y holds
       uint32_t q[VN], n[VN];
@@ -304,25 +386,34 @@ struct NormOut {
   }
 };
 
-// Shared memory of the norm kernels, in floats: scratch (reductions, then the
-// cluster's totals), two totals per channel and four values per group.
+// Shared memory of the norm kernels behind the slab, in floats: scratch (reductions,
+// then the cluster's totals), two totals per channel and four values per group.
 __host__ __device__ inline int norm_smem_floats(int threads, int vx, int vn, int nb) {
   const int w2 = 2 * vx * vn;
   return (threads * vn > w2 ? threads * vn : w2) + w2 + 4 * nb;
 }
+constexpr int kNormBatches = 4;   // groups of copies that a slab's sums wait for one after the other
 
-// ------------------------------------------------- forward, slab in registers
+// Waits for batch b of kNormBatches.
+__device__ __forceinline__ void slab_wait(int b) {
+  if (b == 0) cp_async_wait<3>();
+  else if (b == 1) cp_async_wait<2>();
+  else if (b == 2) cp_async_wait<1>();
+  else cp_async_wait<0>();
+}
+
+// ------------------------------------------------------ forward, slab on chip
 // Cluster of `cs` CTAs per (image, channel block); CTA rank k holds positions
-// k*rows .. of it, NV 16-byte vectors per thread, all requested at once.
-template <typename XT, int NV>
-__global__ void __launch_bounds__(kNormThreads, NV <= 4 ? 2 : 1)
-    group_norm_cluster_kernel(const NormArgs p, int cs) {
-  constexpr int VN = Vec<XT>::n;
-  extern __shared__ __align__(16) float sm[];
+// k*rows .. of it, nv 16-byte vectors per thread.  The group's mean first, then the
+// squared deviations from it: as exact as two passes over memory.
+template <typename XT>
+__global__ void __launch_bounds__(kNormThreads, 3) group_norm_cluster_kernel(const NormArgs p, int cs, int nv) {
+  constexpr int VN = Vec<XT>::n, NT = kNormThreads;
+  extern __shared__ __align__(16) uint8_t smem[];
   const NormTile& t = p.t;
   const int W = t.vx * VN;
-  float* scratch = sm;
-  float* ch = scratch + max(kNormThreads * VN, 2 * W);
+  float* scratch = reinterpret_cast<float*>(smem + (size_t)nv * NT * 16);
+  float* ch = scratch + max(NT * VN, 2 * W);
   float* pub_mean = ch + 2 * W;
   float* pub_m2 = pub_mean + t.nb;
   float* fin_mean = pub_m2 + t.nb;
@@ -334,45 +425,58 @@ __global__ void __launch_bounds__(kNormThreads, NV <= 4 ? 2 : 1)
   const int c0 = cb * t.nb * t.cpg, lc = tx * VN;
   const int r0 = rank * t.rows, r1 = min(t.S, r0 + t.rows);
   const int n_rows = max(0, r1 - r0);
-  const XT* base = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + c0 + lc;
-
-  uint4 raw[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int row = r0 + r + i * t.ty;
-    raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (active && row < r1) raw[i] = load_stream(base + (int64_t)row * p.ldx);
+  const XT* base = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + (int64_t)(r0 + r) * p.ldx + c0 + lc;
+  const int64_t step = (int64_t)t.ty * p.ldx;
+  // this thread's vectors: rows r, r + ty, .. of the CTA's
+  const int mine = active && r < n_rows ? (n_rows - r + t.ty - 1) / t.ty : 0;
+  const int batch = (nv + kNormBatches - 1) / kNormBatches;
+  const uint32_t slab = smem_u32(smem) + threadIdx.x * 16;
+  for (int b = 0; b < kNormBatches; ++b) {
+    for (int i = b * batch; i < min(mine, (b + 1) * batch); ++i) {
+      cp_async16(slab + i * NT * 16, base, 16);
+      base += step;
+    }
+    cp_async_commit();
   }
-  float s[VN];
+  uint64_t s2[VN / 2];
 #pragma unroll
-  for (int k = 0; k < VN; ++k) s[k] = 0.0f;
+  for (int k = 0; k < VN / 2; ++k) s2[k] = 0;
+  for (int b = 0; b < kNormBatches; ++b) {
+    slab_wait(b);
+#pragma unroll 2
+    for (int i = b * batch; i < min(mine, (b + 1) * batch); ++i) {
+      uint64_t v[VN / 2];
+      load_pairs<XT>(lds128(slab + i * NT * 16), v);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float v[VN];
-    Vec<XT>::load_raw(raw[i], v);
-#pragma unroll
-    for (int k = 0; k < VN; ++k) s[k] += v[k];   // absent rows are zeros
-  }
-  reduce_groups<kNormThreads, VN>(s, active, tx, r, t, scratch, ch, pub_mean);
-  const float n_loc = (float)n_rows * (float)t.cpg;
-  for (int g = threadIdx.x; g < t.nb; g += kNormThreads)
-    pub_mean[g] = n_loc > 0.0f ? pub_mean[g] / n_loc : 0.0f;
-  __syncthreads();
-  float m[VN];
-#pragma unroll
-  for (int k = 0; k < VN; ++k) { m[k] = active ? pub_mean[(lc + k) / t.cpg] : 0.0f; s[k] = 0.0f; }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float v[VN];
-    Vec<XT>::load_raw(raw[i], v);
-    if (r0 + r + i * t.ty < r1) {
-#pragma unroll
-      for (int k = 0; k < VN; ++k) { const float d = v[k] - m[k]; s[k] = fmaf(d, d, s[k]); }
+      for (int k = 0; k < VN / 2; ++k) s2[k] = f2_add(s2[k], v[k]);
     }
   }
-  reduce_groups<kNormThreads, VN>(s, active, tx, r, t, scratch, ch, pub_m2);
+  float s[VN];
+  unpack_pairs<VN>(s2, s);
+  reduce_groups<NT, VN>(s, active, tx, r, t, scratch, ch, pub_mean);
+  const float n_loc = (float)n_rows * (float)t.cpg;
+  for (int g = threadIdx.x; g < t.nb; g += NT) pub_mean[g] = n_loc > 0.0f ? pub_mean[g] / n_loc : 0.0f;
+  __syncthreads();
+  uint64_t m[VN / 2];
+#pragma unroll
+  for (int k = 0; k < VN / 2; ++k) {
+    m[k] = active ? f2_pack(-pub_mean[(lc + 2 * k) / t.cpg], -pub_mean[(lc + 2 * k + 1) / t.cpg]) : 0;
+    s2[k] = 0;
+  }
+#pragma unroll 2
+  for (int i = 0; i < mine; ++i) {
+    uint64_t v[VN / 2];
+    load_pairs<XT>(lds128(slab + i * NT * 16), v);
+#pragma unroll
+    for (int k = 0; k < VN / 2; ++k) {
+      const uint64_t d = f2_add(v[k], m[k]);
+      s2[k] = f2_fma(d, d, s2[k]);
+    }
+  }
+  unpack_pairs<VN>(s2, s);
+  reduce_groups<NT, VN>(s, active, tx, r, t, scratch, ch, pub_m2);
   if (cs > 1) { cluster_arrive(); cluster_wait(); }
-  for (int g = threadIdx.x; g < t.nb; g += kNormThreads) {
+  for (int g = threadIdx.x; g < t.nb; g += NT) {
     float n = 0.0f, mean = 0.0f, m2 = 0.0f;
     if (cs > 1) {
       for (int k = 0; k < cs; ++k) {
@@ -393,34 +497,73 @@ __global__ void __launch_bounds__(kNormThreads, NV <= 4 ? 2 : 1)
   }
   __syncthreads();
   if (cs > 1) cluster_arrive();   // this CTA has read its peers' shared memory
-  if (active) {
+  if (mine > 0) {
     NormOut<VN> o;
     o.init(p, c0, lc, fin_mean, fin_rstd);
     with_act(p.act, [&](auto act) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int row = r0 + r + i * t.ty;
-        float v[VN];
-        Vec<XT>::load_raw(raw[i], v);
-        if (row < r1) o.template put<decltype(act)::value>(p, img, row, c0 + lc, v);
-      }
+#pragma unroll 2
+      for (int i = 0; i < mine; ++i)
+        o.template put<decltype(act)::value, XT>(p, img, r0 + r + i * t.ty, c0 + lc, lds128(slab + i * NT * 16));
     });
   }
   __syncwarp();
   if (cs > 1) cluster_wait();     // the peers have read this CTA's
 }
 
-// ------------------------------------------------------- forward, two passes
+// ------------------------------------------------------------------ two passes
+// A thread's rows of a tile, streamed through a ring of its own in shared memory:
+// U rows per step, kNormRing steps in flight.  N tensors of the same shape.
+constexpr int kNormRing = 4;
+template <typename XT, int NT, int U, int N>
+struct NormStream {
+  const XT* at[N];
+  int64_t step[N];
+  uint32_t ring;
+  int left, steps;       // rows not yet asked for; steps of U rows in all
+  __device__ __forceinline__ void begin(uint8_t* smem, int rows) {
+    ring = smem_u32(smem) + threadIdx.x * 16;
+    left = rows;
+    steps = (rows + U - 1) / U;
+#pragma unroll
+    for (int k = 0; k < kNormRing - 1; ++k) issue(k);
+  }
+  __device__ __forceinline__ uint32_t slot(int k, int i, int n) const {
+    return ring + (((k & (kNormRing - 1)) * U + i) * N + n) * NT * 16;
+  }
+  __device__ __forceinline__ void issue(int k) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (i < left) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          cp_async16(slot(k, i, n), at[n], 16);
+          at[n] += step[n];
+        }
+      }
+    left -= U;
+    cp_async_commit();
+  }
+  // step k has landed; the one behind the ring is on its way
+  __device__ __forceinline__ void wait(int k) {
+    cp_async_wait<kNormRing - 2>();
+    issue(k + kNormRing - 1);
+  }
+};
+__host__ __device__ inline int norm_ring_bytes(int threads, int u, int tensors) {
+  return kNormRing * u * tensors * threads * 16;
+}
+constexpr int kNormU1 = 4, kNormU2 = 2;    // rows per step: one tensor, two
+
 // Pass 1: one CTA per (tile of positions, channel block, image) writes mean and
 // M2 of each of its groups.  A thread takes a few rows at a time: their mean
 // and squared deviations per channel, merged into its running ones.
 template <typename XT, int NT>
 __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_stats_kernel(const NormArgs p) {
-  constexpr int VN = Vec<XT>::n, U = 32 / VN;
-  extern __shared__ __align__(16) float sm[];
+  constexpr int VN = Vec<XT>::n, U = kNormU1;
+  extern __shared__ __align__(16) uint8_t smem[];
   const NormTile& t = p.t;
   const int W = t.vx * VN;
-  float* scratch = sm;
+  float* scratch = reinterpret_cast<float*>(smem + norm_ring_bytes(NT, U, 1));
   float* ch = scratch + max(NT * VN, 2 * W);
   float* g_mean = ch + 2 * W;
   float* g_m2 = g_mean + t.nb;
@@ -429,70 +572,67 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_stats_kernel
   const int tx = threadIdx.x % t.vx, r = threadIdx.x / t.vx;
   const bool active = r < t.ty;
   const int c0 = cb * t.nb * t.cpg, lc = tx * VN;
-  const int r0 = tile * t.rows, r1 = min(t.S, r0 + t.rows);
-  const XT* base = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + c0 + lc;
-  float n = 0.0f, mean[VN], m2[VN];
+  const int r0 = tile * t.rows, n_rows = min(t.S, r0 + t.rows) - r0;
+  const int mine = active && r < n_rows ? (n_rows - r + t.ty - 1) / t.ty : 0;
+  NormStream<XT, NT, U, 1> in;
+  in.at[0] = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + (int64_t)(r0 + r) * p.ldx + c0 + lc;
+  in.step[0] = (int64_t)t.ty * p.ldx;
+  in.begin(smem, mine);
+  uint64_t mean[VN / 2], m2[VN / 2];
 #pragma unroll
-  for (int k = 0; k < VN; ++k) mean[k] = m2[k] = 0.0f;
-  if (active) {
-    uint4 raw[U], ahead[U];
-    auto fetch = [&](uint4 (&to)[U], int row) {
+  for (int k = 0; k < VN / 2; ++k) mean[k] = m2[k] = 0;
+  for (int k = 0; k < in.steps; ++k) {
+    in.wait(k);
+    const int cnt = min(U, mine - k * U);
+    const float n0 = (float)(k * U), nc = (float)cnt, f = nc / (n0 + nc);
+    uint64_t v[U][VN / 2], sum[VN / 2], q[VN / 2];
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        to[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (row + i * t.ty < r1)
-          to[i] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)(row + i * t.ty) * p.ldx));
-      }
-    };
-    fetch(ahead, r0 + r);
-    for (int row = r0 + r; row < r1; row += U * t.ty) {
+    for (int i = 0; i < U; ++i) {
+      uint4 u = make_uint4(0u, 0u, 0u, 0u);
+      if (i < cnt) u = lds128(in.slot(k, i, 0));
+      load_pairs<XT>(u, v[i]);
+    }
+    const uint64_t inv = f2_both(-1.0f / nc);
 #pragma unroll
-      for (int i = 0; i < U; ++i) raw[i] = ahead[i];
-      fetch(ahead, row + U * t.ty);      // in flight while this chunk is summed
-      const int cnt = min(U, (r1 - row + t.ty - 1) / t.ty);
-      float s[VN];
+    for (int c = 0; c < VN / 2; ++c) {
+      sum[c] = v[0][c];
 #pragma unroll
-      for (int k = 0; k < VN; ++k) s[k] = 0.0f;
+      for (int i = 1; i < U; ++i) sum[c] = f2_add(sum[c], v[i][c]);
+      sum[c] = f2_mul(sum[c], inv);             // minus the rows' mean
+      q[c] = 0;
+    }
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        float v[VN];
-        Vec<XT>::load_raw(raw[i], v);
+    for (int i = 0; i < U; ++i)
+      if (i < cnt) {
 #pragma unroll
-        for (int k = 0; k < VN; ++k) s[k] += v[k];
-      }
-      const float nc = (float)cnt, inv = 1.0f / nc, nn = n + nc, f = nc / nn;
-      float q[VN];
-#pragma unroll
-      for (int k = 0; k < VN; ++k) { s[k] *= inv; q[k] = 0.0f; }
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        float v[VN];
-        Vec<XT>::load_raw(raw[i], v);
-        if (i < cnt) {
-#pragma unroll
-          for (int k = 0; k < VN; ++k) { const float d = v[k] - s[k]; q[k] = fmaf(d, d, q[k]); }
+        for (int c = 0; c < VN / 2; ++c) {
+          const uint64_t d = f2_add(v[i][c], sum[c]);
+          q[c] = f2_fma(d, d, q[c]);
         }
       }
+    const uint64_t f2 = f2_both(-f), nf = f2_both(n0 * f);
 #pragma unroll
-      for (int k = 0; k < VN; ++k) {
-        const float d = s[k] - mean[k];
-        mean[k] = fmaf(d, f, mean[k]);
-        m2[k] += fmaf(d * d, n * f, q[k]);
-      }
-      n = nn;
+    for (int c = 0; c < VN / 2; ++c) {
+      const uint64_t d = f2_add(sum[c], mean[c]);   // running mean minus the rows' mean
+      mean[c] = f2_fma(d, f2, mean[c]);
+      m2[c] = f2_add(m2[c], f2_fma(f2_mul(d, d), nf, q[c]));
     }
   }
-  float s[VN];
+  cp_async_wait<0>();
+  float mv[VN], qv[VN], s[VN];
+  unpack_pairs<VN>(mean, mv);
+  unpack_pairs<VN>(m2, qv);
+  const float n = (float)mine;
 #pragma unroll
-  for (int k = 0; k < VN; ++k) s[k] = n * mean[k];
+  for (int k = 0; k < VN; ++k) s[k] = n * mv[k];
   reduce_groups<NT, VN>(s, active, tx, r, t, scratch, ch, g_mean);
-  const float n_tile = (float)(r1 - r0) * (float)t.cpg;
+  const float n_tile = (float)n_rows * (float)t.cpg;
   for (int g = threadIdx.x; g < t.nb; g += NT) g_mean[g] /= n_tile;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < VN; ++k) {
-    const float d = active ? mean[k] - g_mean[(lc + k) / t.cpg] : 0.0f;
-    s[k] = fmaf(n * d, d, m2[k]);
+    const float d = active ? mv[k] - g_mean[(lc + k) / t.cpg] : 0.0f;
+    s[k] = fmaf(n * d, d, qv[k]);
   }
   reduce_groups<NT, VN>(s, active, tx, r, t, scratch, ch, g_m2);
   for (int g = threadIdx.x; g < t.nb; g += NT)
@@ -503,18 +643,27 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_stats_kernel
 // likeliest in L2); each CTA merges its groups' tiles first, a warp per group.
 template <typename XT, int NT>
 __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_apply_kernel(const NormArgs p) {
-  constexpr int VN = Vec<XT>::n, U = 4;
-  extern __shared__ __align__(16) float sm[];
+  constexpr int VN = Vec<XT>::n, U = kNormU1;
+  extern __shared__ __align__(16) uint8_t smem[];
   const NormTile& t = p.t;
-  float* fin_mean = sm;
-  float* fin_rstd = sm + t.nb;
+  float* fin_mean = reinterpret_cast<float*>(smem + norm_ring_bytes(NT, U, 1));
+  float* fin_rstd = fin_mean + t.nb;
   const int tile = gridDim.x - 1 - blockIdx.x, cb = gridDim.y - 1 - blockIdx.y,
             img = gridDim.z - 1 - blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = cb * t.nb * t.cpg;
+  const int tx = threadIdx.x % t.vx, r = threadIdx.x / t.vx;
+  const int lc = tx * VN;
+  const int r0 = tile * t.rows, n_rows = min(t.S, r0 + t.rows) - r0;
+  const int mine = r < t.ty && r < n_rows ? (n_rows - r + t.ty - 1) / t.ty : 0;
   grid_dep_wait();
-  for (int g = warp; g < t.nb; g += (NT / 32)) {
+  NormStream<XT, NT, U, 1> in;
+  in.at[0] = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + (int64_t)(r0 + r) * p.ldx + c0 + lc;
+  in.step[0] = (int64_t)t.ty * p.ldx;
+  in.begin(smem, mine);
+  for (int g = warp; g < t.nb; g += NT / 32) {
     float n = 0.0f, mean = 0.0f, m2 = 0.0f;
+#pragma unroll 4
     for (int k = lane; k < p.tiles; k += 32) {
       const float2 v = p.part[((int64_t)img * p.tiles + k) * t.G + cb * t.nb + g];
       const float nk = (float)(min(t.S, (k + 1) * t.rows) - k * t.rows) * (float)t.cpg;
@@ -538,33 +687,21 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_apply_kernel
     }
   }
   __syncthreads();
-  const int tx = threadIdx.x % t.vx, r = threadIdx.x / t.vx;
-  if (r >= t.ty) return;
-  const int lc = tx * VN;
-  const int r0 = tile * t.rows, r1 = min(t.S, r0 + t.rows);
-  const XT* base = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + c0 + lc;
-  NormOut<VN> o;
-  o.init(p, c0, lc, fin_mean, fin_rstd);
-  with_act(p.act, [&](auto act) {
-    uint4 raw[U], ahead[U];
-    auto fetch = [&](int row) {
+  if (mine > 0) {
+    NormOut<VN> o;
+    o.init(p, c0, lc, fin_mean, fin_rstd);
+    with_act(p.act, [&](auto act) {
+      for (int k = 0; k < in.steps; ++k) {
+        in.wait(k);
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (row + i * t.ty < r1) ahead[i] = load_stream(base + (int64_t)(row + i * t.ty) * p.ldx);
-    };
-    fetch(r0 + r);
-    for (int row = r0 + r; row < r1; row += U * t.ty) {
-#pragma unroll
-      for (int i = 0; i < U; ++i) raw[i] = ahead[i];
-      fetch(row + U * t.ty);
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        float v[VN];
-        Vec<XT>::load_raw(raw[i], v);
-        if (row + i * t.ty < r1) o.template put<decltype(act)::value>(p, img, row + i * t.ty, c0 + lc, v);
+        for (int i = 0; i < U; ++i)
+          if (k * U + i < mine)
+            o.template put<decltype(act)::value, XT>(p, img, r0 + r + (k * U + i) * t.ty, c0 + lc,
+                                                     lds128(in.slot(k, i, 0)));
       }
-    }
-  });
+    });
+  }
+  cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------------ gradients
@@ -653,53 +790,59 @@ __device__ __forceinline__ void grad_group_means(const NormBwdArgs& p, int img, 
   __syncthreads();
 }
 
-// Slab of x and dy in the registers of a cluster; total[img] receives the
+// Slabs of x and dy in the shared memory of a cluster; total[img] receives the
 // image's sums for dgamma and dbeta.
-template <typename XT, int NV>
-__global__ void __launch_bounds__(kNormThreads, 1)
-    group_norm_bwd_cluster_kernel(const NormBwdArgs p, int cs) {
-  constexpr int VN = Vec<XT>::n;
-  extern __shared__ __align__(16) float sm[];
+template <typename XT>
+__global__ void __launch_bounds__(kNormThreads, 2)
+    group_norm_bwd_cluster_kernel(const NormBwdArgs p, int cs, int nv) {
+  constexpr int VN = Vec<XT>::n, NT = kNormThreads;
+  extern __shared__ __align__(16) uint8_t smem[];
   const NormTile& t = p.t;
   const int W = t.vx * VN;
-  float* scratch = sm;                           // later the cluster's totals [2][W]
-  float* ch = scratch + max(kNormThreads * VN, 2 * W);   // this CTA's totals [2][W]
+  float* scratch = reinterpret_cast<float*>(smem + (size_t)nv * NT * 32);   // later the cluster's totals [2][W]
+  float* ch = scratch + max(NT * VN, 2 * W);                               // this CTA's totals [2][W]
   float* g1 = ch + 2 * W;
   float* g2 = g1 + t.nb;
   const int rank = blockIdx.x % cs, cb = blockIdx.x / cs, img = blockIdx.y;
   const int tx = threadIdx.x % t.vx, r = threadIdx.x / t.vx;
   const bool active = r < t.ty;
   const int c0 = cb * t.nb * t.cpg, lc = tx * VN;
-  const int r0 = rank * t.rows, r1 = min(t.S, r0 + t.rows);
-  const XT* xb = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + c0 + lc;
-  const XT* gb = static_cast<const XT*>(p.dy) + (int64_t)img * p.dybs + c0 + lc;
+  const int r0 = rank * t.rows, n_rows = max(0, min(t.S, r0 + t.rows) - r0);
+  const int mine = active && r < n_rows ? (n_rows - r + t.ty - 1) / t.ty : 0;
+  const XT* xb = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + (int64_t)(r0 + r) * p.ldx + c0 + lc;
+  const XT* gb = static_cast<const XT*>(p.dy) + (int64_t)img * p.dybs + (int64_t)(r0 + r) * p.lddy + c0 + lc;
   grid_dep_launch();
-  uint4 xr[NV], gr[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int row = r0 + r + i * t.ty;
-    xr[i] = gr[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (active && row < r1) {
-      xr[i] = load_stream(xb + (int64_t)row * p.ldx);
-      gr[i] = load_stream(gb + (int64_t)row * p.lddy);
+  const int batch = (nv + kNormBatches - 1) / kNormBatches;
+  const uint32_t slab = smem_u32(smem) + threadIdx.x * 16;
+  for (int b = 0; b < kNormBatches; ++b) {
+    for (int i = b * batch; i < min(mine, (b + 1) * batch); ++i) {
+      cp_async16(slab + 2 * i * NT * 16, xb, 16);
+      cp_async16(slab + (2 * i + 1) * NT * 16, gb, 16);
+      xb += (int64_t)t.ty * p.ldx;
+      gb += (int64_t)t.ty * p.lddy;
     }
+    cp_async_commit();
   }
   float s1[VN], s2[VN];
 #pragma unroll
   for (int i = 0; i < VN; ++i) s1[i] = s2[i] = 0.0f;
-  if (active) {
+  if (mine > 0) {
     NormGrad<VN> k;
     k.init(p, img, c0, lc);
     with_act(p.act, [&](auto act) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (r0 + r + i * t.ty < r1) k.template sums<decltype(act)::value, XT>(xr[i], gr[i], s1, s2);
+      for (int b = 0; b < kNormBatches; ++b) {
+        slab_wait(b);
+#pragma unroll 1
+        for (int i = b * batch; i < min(mine, (b + 1) * batch); ++i)
+          k.template sums<decltype(act)::value, XT>(lds128(slab + 2 * i * NT * 16),
+                                                    lds128(slab + (2 * i + 1) * NT * 16), s1, s2);
+      }
     });
   }
-  reduce_channels<kNormThreads, VN>(s1, active, tx, r, t, scratch, ch);
-  reduce_channels<kNormThreads, VN>(s2, active, tx, r, t, scratch, ch + W);
+  reduce_channels<NT, VN>(s1, active, tx, r, t, scratch, ch);
+  reduce_channels<NT, VN>(s2, active, tx, r, t, scratch, ch + W);
   if (cs > 1) { cluster_arrive(); cluster_wait(); }
-  for (int c = threadIdx.x; c < 2 * W; c += kNormThreads) {
+  for (int c = threadIdx.x; c < 2 * W; c += NT) {
     float a = 0.0f;
     if (cs > 1) {
       for (int q = 0; q < cs; ++q) a += dsmem_f32(ch + c, q);
@@ -712,18 +855,16 @@ __global__ void __launch_bounds__(kNormThreads, 1)
   }
   __syncthreads();
   if (cs > 1) cluster_arrive();
-  grad_group_means<kNormThreads>(p, img, c0, W, scratch, g1, g2);
-  if (active) {
+  grad_group_means<NT>(p, img, c0, W, scratch, g1, g2);
+  if (mine > 0) {
     NormGradOut<VN> o;
     o.init(p, img, c0, lc, g1, g2);
     with_act(p.act, [&](auto act) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int row = r0 + r + i * t.ty;
-        if (row < r1)
-          o.template put<decltype(act)::value, XT>(
-              p.dx, (int64_t)img * p.dxbs + (int64_t)row * p.lddx + c0 + lc, xr[i], gr[i]);
-      }
+#pragma unroll 1
+      for (int i = 0; i < mine; ++i)
+        o.template put<decltype(act)::value, XT>(
+            p.dx, (int64_t)img * p.dxbs + (int64_t)(r0 + r + i * t.ty) * p.lddx + c0 + lc,
+            lds128(slab + 2 * i * NT * 16), lds128(slab + (2 * i + 1) * NT * 16));
     });
   }
   __syncwarp();
@@ -734,47 +875,42 @@ __global__ void __launch_bounds__(kNormThreads, 1)
 // then dx.
 template <typename XT, int NT>
 __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_sums_kernel(const NormBwdArgs p) {
-  constexpr int VN = Vec<XT>::n, U = 4;
-  extern __shared__ __align__(16) float sm[];
+  constexpr int VN = Vec<XT>::n, U = kNormU2;
+  extern __shared__ __align__(16) uint8_t smem[];
   const NormTile& t = p.t;
   const int W = t.vx * VN;
-  float* scratch = sm;
+  float* scratch = reinterpret_cast<float*>(smem + norm_ring_bytes(NT, U, 2));
   float* ch = scratch + max(NT * VN, 2 * W);
   grid_dep_launch();
   const int tile = blockIdx.x, cb = blockIdx.y, img = blockIdx.z;
   const int tx = threadIdx.x % t.vx, r = threadIdx.x / t.vx;
   const bool active = r < t.ty;
   const int c0 = cb * t.nb * t.cpg, lc = tx * VN;
-  const int r0 = tile * t.rows, r1 = min(t.S, r0 + t.rows);
-  const XT* xb = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + c0 + lc;
-  const XT* gb = static_cast<const XT*>(p.dy) + (int64_t)img * p.dybs + c0 + lc;
+  const int r0 = tile * t.rows, n_rows = min(t.S, r0 + t.rows) - r0;
+  const int mine = active && r < n_rows ? (n_rows - r + t.ty - 1) / t.ty : 0;
+  NormStream<XT, NT, U, 2> in;
+  in.at[0] = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + (int64_t)(r0 + r) * p.ldx + c0 + lc;
+  in.at[1] = static_cast<const XT*>(p.dy) + (int64_t)img * p.dybs + (int64_t)(r0 + r) * p.lddy + c0 + lc;
+  in.step[0] = (int64_t)t.ty * p.ldx;
+  in.step[1] = (int64_t)t.ty * p.lddy;
+  in.begin(smem, mine);
   float s1[VN], s2[VN];
 #pragma unroll
   for (int i = 0; i < VN; ++i) s1[i] = s2[i] = 0.0f;
-  if (active) {
-    uint4 xr[U], gr[U], xa[U], ga[U];
-    auto fetch = [&](int row) {
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (row + i * t.ty < r1) {
-          xa[i] = __ldg(reinterpret_cast<const uint4*>(xb + (int64_t)(row + i * t.ty) * p.ldx));
-          ga[i] = __ldg(reinterpret_cast<const uint4*>(gb + (int64_t)(row + i * t.ty) * p.lddy));
-        }
-    };
-    fetch(r0 + r);
-    NormGrad<VN> k;
-    k.init(p, img, c0, lc);
+  if (mine > 0) {
+    NormGrad<VN> g;
+    g.init(p, img, c0, lc);
     with_act(p.act, [&](auto act) {
-      for (int row = r0 + r; row < r1; row += U * t.ty) {
-#pragma unroll
-        for (int i = 0; i < U; ++i) { xr[i] = xa[i]; gr[i] = ga[i]; }
-        fetch(row + U * t.ty);
+      for (int k = 0; k < in.steps; ++k) {
+        in.wait(k);
 #pragma unroll
         for (int i = 0; i < U; ++i)
-          if (row + i * t.ty < r1) k.template sums<decltype(act)::value, XT>(xr[i], gr[i], s1, s2);
+          if (k * U + i < mine)
+            g.template sums<decltype(act)::value, XT>(lds128(in.slot(k, i, 0)), lds128(in.slot(k, i, 1)), s1, s2);
       }
     });
   }
+  cp_async_wait<0>();
   reduce_channels<NT, VN>(s1, active, tx, r, t, scratch, ch);
   reduce_channels<NT, VN>(s2, active, tx, r, t, scratch, ch + W);
   float* d = p.part + ((int64_t)img * p.tiles + tile) * 2 * t.C + c0;
@@ -786,52 +922,47 @@ __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_sums_kernel(const
 
 template <typename XT, int NT>
 __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_apply_kernel(const NormBwdArgs p) {
-  constexpr int VN = Vec<XT>::n, U = 2;
-  extern __shared__ __align__(16) float sm[];
+  constexpr int VN = Vec<XT>::n, U = kNormU2;
+  extern __shared__ __align__(16) uint8_t smem[];
   const NormTile& t = p.t;
   const int W = t.vx * VN;
-  float* tot = sm;
-  float* g1 = sm + 2 * W;
+  float* tot = reinterpret_cast<float*>(smem + norm_ring_bytes(NT, U, 2));
+  float* g1 = tot + 2 * W;
   float* g2 = g1 + t.nb;
   const int tile = gridDim.x - 1 - blockIdx.x, cb = gridDim.y - 1 - blockIdx.y,
             img = gridDim.z - 1 - blockIdx.z;
   const int c0 = cb * t.nb * t.cpg;
   const int tx = threadIdx.x % t.vx, r = threadIdx.x / t.vx;
-  const bool active = r < t.ty;
   const int lc = tx * VN;
-  const int r0 = tile * t.rows, r1 = min(t.S, r0 + t.rows);
-  const XT* xb = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + c0 + lc;
-  const XT* gb = static_cast<const XT*>(p.dy) + (int64_t)img * p.dybs + c0 + lc;
+  const int r0 = tile * t.rows, n_rows = min(t.S, r0 + t.rows) - r0;
+  const int mine = r < t.ty && r < n_rows ? (n_rows - r + t.ty - 1) / t.ty : 0;
   grid_dep_wait();
-  uint4 xr[U], gr[U], xa[U], ga[U];
-  auto fetch = [&](int row) {
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (active && row + i * t.ty < r1) {
-        xa[i] = load_stream(xb + (int64_t)(row + i * t.ty) * p.ldx);
-        ga[i] = load_stream(gb + (int64_t)(row + i * t.ty) * p.lddy);
-      }
-  };
-  fetch(r0 + r);
+  NormStream<XT, NT, U, 2> in;
+  in.at[0] = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + (int64_t)(r0 + r) * p.ldx + c0 + lc;
+  in.at[1] = static_cast<const XT*>(p.dy) + (int64_t)img * p.dybs + (int64_t)(r0 + r) * p.lddy + c0 + lc;
+  in.step[0] = (int64_t)t.ty * p.ldx;
+  in.step[1] = (int64_t)t.ty * p.lddy;
+  in.begin(smem, mine);
   for (int c = threadIdx.x; c < 2 * W; c += NT)
     tot[c] = p.total[(int64_t)img * 2 * t.C + (c < W ? c0 + c : t.C + c0 + c - W)];
   __syncthreads();
   grad_group_means<NT>(p, img, c0, W, tot, g1, g2);
-  if (!active) return;
-  NormGradOut<VN> o;
-  o.init(p, img, c0, lc, g1, g2);
-  with_act(p.act, [&](auto act) {
-    for (int row = r0 + r; row < r1; row += U * t.ty) {
+  if (mine > 0) {
+    NormGradOut<VN> o;
+    o.init(p, img, c0, lc, g1, g2);
+    with_act(p.act, [&](auto act) {
+      for (int k = 0; k < in.steps; ++k) {
+        in.wait(k);
 #pragma unroll
-      for (int i = 0; i < U; ++i) { xr[i] = xa[i]; gr[i] = ga[i]; }
-      fetch(row + U * t.ty);
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (row + i * t.ty < r1)
-          o.template put<decltype(act)::value, XT>(
-              p.dx, (int64_t)img * p.dxbs + (int64_t)(row + i * t.ty) * p.lddx + c0 + lc, xr[i], gr[i]);
-    }
-  });
+        for (int i = 0; i < U; ++i)
+          if (k * U + i < mine)
+            o.template put<decltype(act)::value, XT>(
+                p.dx, (int64_t)img * p.dxbs + (int64_t)(r0 + r + (k * U + i) * t.ty) * p.lddx + c0 + lc,
+                lds128(in.slot(k, i, 0)), lds128(in.slot(k, i, 1)));
+      }
+    });
+  }
+  cp_async_wait<0>();
 }
 
 // dbeta and dgamma, and (two passes) each image's sums over its tiles.  A block

@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+
 #include <atomic>
 #include <mutex>
 #include <vector>
