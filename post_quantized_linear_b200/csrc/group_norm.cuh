@@ -169,16 +169,25 @@ __device__ __forceinline__ float erfc_half(float z, float& e) {
   return p * t * e;
 }
 
+// 1 / (1 + exp(-z)) of both values with one reciprocal, r = 1 / (a b): the special
+// function unit (four lanes a clock) bounds these loops.  Arguments below -43.6 are taken
+// as that (the sigmoid stays below 2^-63), which keeps a b finite.
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t z2) {
+  float a, b;
+  f2_unpack(f2_mul(z2, f2_both(-kLog2e)), a, b);
+  const uint64_t d = f2_add(f2_pack(ex2_ftz(fminf(a, 63.0f)), ex2_ftz(fminf(b, 63.0f))), f2_both(1.0f));
+  f2_unpack(d, a, b);
+  const float r = rcp_ftz(a * b);
+  return f2_pack(r * b, r * a);
+}
+
 // act(z) and act'(z).  The hardware's exponential and reciprocal (relative error about
 // 2^-22 each): the result is stored in bf16, or in fp32 within 1e-6 of its scale.
 template <int ACT>
 __device__ __forceinline__ uint64_t norm_act(uint64_t z2) {
   float z0, z1;
   if constexpr (ACT == ACT_SILU) {               // z / (1 + exp(-z))
-    float a, b;
-    f2_unpack(f2_mul(z2, f2_both(-kLog2e)), a, b);
-    f2_unpack(f2_add(f2_pack(ex2_ftz(a), ex2_ftz(b)), f2_both(1.0f)), a, b);
-    return f2_mul(z2, f2_pack(rcp_ftz(a), rcp_ftz(b)));
+    return f2_mul(z2, sigmoid2(z2));
   } else if constexpr (ACT == ACT_GELU) {        // max(z, 0) - |z| erfc(|z| / sqrt 2) / 2
     f2_unpack(z2, z0, z1);
     float e;
@@ -189,16 +198,18 @@ __device__ __forceinline__ uint64_t norm_act(uint64_t z2) {
   }
 }
 template <int ACT>
-__device__ __forceinline__ float norm_act_slope(float z) {
-  if constexpr (ACT == ACT_SILU) {
-    const float p = rcp_ftz(1.0f + ex2_ftz(-kLog2e * z));
-    return p * fmaf(z, 1.0f - p, 1.0f);
-  } else if constexpr (ACT == ACT_GELU) {
-    float e;
-    const float h = 0.5f * erfc_half(z, e);
-    return fmaf(z * 0.39894228f, e, z >= 0.0f ? 1.0f - h : h);
+__device__ __forceinline__ uint64_t norm_act_slope(uint64_t z2) {
+  if constexpr (ACT == ACT_SILU) {               // p (1 + z (1 - p))
+    const uint64_t one = f2_both(1.0f), p = sigmoid2(z2);
+    return f2_mul(p, f2_fma(z2, f2_fma(p, f2_both(-1.0f), one), one));
+  } else if constexpr (ACT == ACT_GELU) {        // the normal distribution plus z times its density
+    float z0, z1, e0, e1;
+    f2_unpack(z2, z0, z1);
+    const float h0 = 0.5f * erfc_half(z0, e0), h1 = 0.5f * erfc_half(z1, e1);
+    return f2_fma(f2_mul(z2, f2_both(0.39894228f)), f2_pack(e0, e1),
+                  f2_pack(z0 >= 0.0f ? 1.0f - h0 : h0, z1 >= 0.0f ? 1.0f - h1 : h1));
   } else {
-    return 1.0f;
+    return f2_both(1.0f);
   }
 }
 // The activation is a launch argument: one uniform branch outside the loops.
@@ -207,6 +218,20 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
   if (act == ACT_SILU) f(std::integral_constant<int, ACT_SILU>{});
   else if (act == ACT_GELU) f(std::integral_constant<int, ACT_GELU>{});
   else f(std::integral_constant<int, ACT_NONE>{});
+}
+// So is what the forward writes.
+constexpr int OUT_BF16 = 0, OUT_F32 = 1, OUT_CODES = 2, OUT_CODES_BF16 = 3;
+template <typename F>
+__device__ __forceinline__ void with_act_out(const NormArgs& p, F&& f) {
+  with_act(p.act, [&](auto act) {
+    if (p.q_pos == nullptr) {
+      if (p.y_bf16) f(act, std::integral_constant<int, OUT_BF16>{});
+      else f(act, std::integral_constant<int, OUT_F32>{});
+    } else {
+      if (p.y == nullptr) f(act, std::integral_constant<int, OUT_CODES>{});
+      else f(act, std::integral_constant<int, OUT_CODES_BF16>{});
+    }
+  });
 }
 
 // --------------------------------------------------------------- reductions
@@ -331,8 +356,12 @@ template <int VN>
 struct NormOut {
   uint64_t a[VN / 2], b[VN / 2];
   float rp, rn;
-  __device__ __forceinline__ void init(const NormArgs& p, int c0, int lc, const float* mean_g,
-                                       const float* rstd_g) {
+  uint8_t* y;              // this thread's next vector, and the bytes from one to the next
+  int64_t y_step;
+  int64_t q_at, q_step;
+  // row, ty: the thread's first position and the distance of its positions
+  __device__ __forceinline__ void init(const NormArgs& p, int img, int row, int ty, int c0, int lc,
+                                       const float* mean_g, const float* rstd_g) {
     float av[VN], bv[VN];
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
@@ -345,23 +374,29 @@ struct NormOut {
       a[i] = f2_pack(av[2 * i], av[2 * i + 1]);
       b[i] = f2_pack(bv[2 * i], bv[2 * i + 1]);
     }
+    const int es = p.y_bf16 ? 2 : 4;
+    y = static_cast<uint8_t*>(p.y) + ((int64_t)img * p.ybs + (int64_t)row * p.ldy + c0 + lc) * es;
+    y_step = (int64_t)ty * p.ldy * es;
     rp = rn = 0.0f;
+    q_at = q_step = 0;
     if (p.q_pos != nullptr) {
       const int j = p.kseg.segment_of(c0 + lc);   // bounds are multiples of 128
       const float sp = p.s_pos[j], sn = p.s_neg[j];
       rp = sp > 0.0f ? __frcp_rn(sp) : 0.0f;
       rn = sn > 0.0f ? __frcp_rn(sn) : 0.0f;
+      q_at = ((int64_t)img * p.t.S + row) * p.ldq + c0 + lc;
+      q_step = (int64_t)ty * p.ldq;
     }
   }
-  template <int ACT, typename XT>
-  __device__ __forceinline__ void put(const NormArgs& p, int img, int row, int c, const uint4& raw) const {
+  template <int ACT, int OUT, typename XT>
+  __device__ __forceinline__ void put(const NormArgs& p, const uint4& raw) {
     uint64_t x[VN / 2];
     load_pairs<XT>(raw, x);
 #pragma unroll
     for (int i = 0; i < VN / 2; ++i) x[i] = norm_act<ACT>(f2_fma(x[i], a[i], b[i]));
     float v[VN];
     unpack_pairs<VN>(x, v);
-    if (p.q_pos != nullptr) {
+    if constexpr (OUT == OUT_CODES || OUT == OUT_CODES_BF16) {
       // the codes are those of the bf16 values that y holds
       uint32_t q[VN], n[VN];
 #pragma unroll
@@ -370,19 +405,21 @@ struct NormOut {
         q[i] = code_pos(v[i], rp);
         n[i] = code_neg(v[i], rn);
       }
-      const int64_t at = ((int64_t)img * p.t.S + row) * p.ldq + c;
       if constexpr (VN == 8) {
-        *reinterpret_cast<uint2*>(p.q_pos + at) =
+        *reinterpret_cast<uint2*>(p.q_pos + q_at) =
             make_uint2(pack4_low(q[0], q[1], q[2], q[3]), pack4_low(q[4], q[5], q[6], q[7]));
-        *reinterpret_cast<uint2*>(p.q_neg + at) =
+        *reinterpret_cast<uint2*>(p.q_neg + q_at) =
             make_uint2(pack4_low(n[0], n[1], n[2], n[3]), pack4_low(n[4], n[5], n[6], n[7]));
       } else {
-        *reinterpret_cast<uint32_t*>(p.q_pos + at) = pack4_low(q[0], q[1], q[2], q[3]);
-        *reinterpret_cast<uint32_t*>(p.q_neg + at) = pack4_low(n[0], n[1], n[2], n[3]);
+        *reinterpret_cast<uint32_t*>(p.q_pos + q_at) = pack4_low(q[0], q[1], q[2], q[3]);
+        *reinterpret_cast<uint32_t*>(p.q_neg + q_at) = pack4_low(n[0], n[1], n[2], n[3]);
       }
+      q_at += q_step;
     }
-    if (p.y != nullptr)
-      store_vec<VN>(p.y, (int64_t)img * p.ybs + (int64_t)row * p.ldy + c, p.y_bf16 != 0, v);
+    if constexpr (OUT != OUT_CODES) {
+      store_vec<VN>(y, 0, OUT != OUT_F32, v);
+      y += y_step;
+    }
   }
 };
 
@@ -499,11 +536,11 @@ __global__ void __launch_bounds__(kNormThreads, 3) group_norm_cluster_kernel(con
   if (cs > 1) cluster_arrive();   // this CTA has read its peers' shared memory
   if (mine > 0) {
     NormOut<VN> o;
-    o.init(p, c0, lc, fin_mean, fin_rstd);
-    with_act(p.act, [&](auto act) {
+    o.init(p, img, r0 + r, t.ty, c0, lc, fin_mean, fin_rstd);
+    with_act_out(p, [&](auto act, auto out) {
 #pragma unroll 2
       for (int i = 0; i < mine; ++i)
-        o.template put<decltype(act)::value, XT>(p, img, r0 + r + i * t.ty, c0 + lc, lds128(slab + i * NT * 16));
+        o.template put<decltype(act)::value, decltype(out)::value, XT>(p, lds128(slab + i * NT * 16));
     });
   }
   __syncwarp();
@@ -519,34 +556,45 @@ struct NormStream {
   const XT* at[N];
   int64_t step[N];
   uint32_t ring;
-  int left, steps;       // rows not yet asked for; steps of U rows in all
+  int left;              // rows not yet asked for
   __device__ __forceinline__ void begin(uint8_t* smem, int rows) {
     ring = smem_u32(smem) + threadIdx.x * 16;
     left = rows;
-    steps = (rows + U - 1) / U;
 #pragma unroll
     for (int k = 0; k < kNormRing - 1; ++k) issue(k);
   }
-  __device__ __forceinline__ uint32_t slot(int k, int i, int n) const {
-    return ring + (((k & (kNormRing - 1)) * U + i) * N + n) * NT * 16;
+  __device__ __forceinline__ uint32_t step_at(int k) const { return ring + (k & (kNormRing - 1)) * (U * N * NT * 16); }
+  // the vector of tensor n and row i of a step at `base`
+  __device__ __forceinline__ static uint4 get(uint32_t base, int i, int n) {
+    return lds128(base + (i * N + n) * (NT * 16));
   }
   __device__ __forceinline__ void issue(int k) {
+    const uint32_t base = step_at(k);
+    if (left >= U) {
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (i < left) {
+      for (int i = 0; i < U; ++i)
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-          cp_async16(slot(k, i, n), at[n], 16);
+          cp_async16(base + (i * N + n) * (NT * 16), at[n], 16);
           at[n] += step[n];
         }
-      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < left; ++i)
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          cp_async16(base + (i * N + n) * (NT * 16), at[n], 16);
+          at[n] += step[n];
+        }
+    }
     left -= U;
     cp_async_commit();
   }
-  // step k has landed; the one behind the ring is on its way
-  __device__ __forceinline__ void wait(int k) {
+  // where step k has landed; the one behind the ring is on its way
+  __device__ __forceinline__ uint32_t wait(int k) {
     cp_async_wait<kNormRing - 2>();
     issue(k + kNormRing - 1);
+    return step_at(k);
   }
 };
 __host__ __device__ inline int norm_ring_bytes(int threads, int u, int tensors) {
@@ -581,41 +629,44 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_stats_kernel
   uint64_t mean[VN / 2], m2[VN / 2];
 #pragma unroll
   for (int k = 0; k < VN / 2; ++k) mean[k] = m2[k] = 0;
-  for (int k = 0; k < in.steps; ++k) {
-    in.wait(k);
-    const int cnt = min(U, mine - k * U);
-    const float n0 = (float)(k * U), nc = (float)cnt, f = nc / (n0 + nc);
-    uint64_t v[U][VN / 2], sum[VN / 2], q[VN / 2];
+  // whole steps of U rows, then the rest row by row; f: the new rows' share of all so far
+  int k = 0;
+  for (; (k + 1) * U <= mine; ++k) {
+    const uint32_t at = in.wait(k);
+    const float n0 = (float)(k * U), f = __fdividef((float)U, n0 + (float)U);
+    uint64_t v[U][VN / 2];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      uint4 u = make_uint4(0u, 0u, 0u, 0u);
-      if (i < cnt) u = lds128(in.slot(k, i, 0));
-      load_pairs<XT>(u, v[i]);
-    }
-    const uint64_t inv = f2_both(-1.0f / nc);
+    for (int i = 0; i < U; ++i) load_pairs<XT>(in.get(at, i, 0), v[i]);
+    const uint64_t inv = f2_both(-1.0f / (float)U), f2 = f2_both(-f), nf = f2_both(n0 * f);
 #pragma unroll
     for (int c = 0; c < VN / 2; ++c) {
-      sum[c] = v[0][c];
+      uint64_t sum = v[0][c], q = 0;
 #pragma unroll
-      for (int i = 1; i < U; ++i) sum[c] = f2_add(sum[c], v[i][c]);
-      sum[c] = f2_mul(sum[c], inv);             // minus the rows' mean
-      q[c] = 0;
-    }
+      for (int i = 1; i < U; ++i) sum = f2_add(sum, v[i][c]);
+      sum = f2_mul(sum, inv);                       // minus the rows' mean
 #pragma unroll
-    for (int i = 0; i < U; ++i)
-      if (i < cnt) {
-#pragma unroll
-        for (int c = 0; c < VN / 2; ++c) {
-          const uint64_t d = f2_add(v[i][c], sum[c]);
-          q[c] = f2_fma(d, d, q[c]);
-        }
+      for (int i = 0; i < U; ++i) {
+        const uint64_t d = f2_add(v[i][c], sum);
+        q = f2_fma(d, d, q);
       }
-    const uint64_t f2 = f2_both(-f), nf = f2_both(n0 * f);
-#pragma unroll
-    for (int c = 0; c < VN / 2; ++c) {
-      const uint64_t d = f2_add(sum[c], mean[c]);   // running mean minus the rows' mean
+      const uint64_t d = f2_add(sum, mean[c]);      // running mean minus the rows' mean
       mean[c] = f2_fma(d, f2, mean[c]);
-      m2[c] = f2_add(m2[c], f2_fma(f2_mul(d, d), nf, q[c]));
+      m2[c] = f2_add(m2[c], f2_fma(f2_mul(d, d), nf, q));
+    }
+  }
+  if (k * U < mine) {
+    const uint32_t at = in.wait(k);
+#pragma unroll 1
+    for (int i = 0; k * U + i < mine; ++i) {
+      const float n0 = (float)(k * U + i), f = __fdividef(1.0f, n0 + 1.0f);
+      uint64_t v[VN / 2];
+      load_pairs<XT>(in.get(at, i, 0), v);
+#pragma unroll
+      for (int c = 0; c < VN / 2; ++c) {
+        const uint64_t d = f2_fma(mean[c], f2_both(-1.0f), v[c]);
+        mean[c] = f2_fma(d, f2_both(f), mean[c]);
+        m2[c] = f2_fma(f2_mul(d, d), f2_both(n0 * f), m2[c]);
+      }
     }
   }
   cp_async_wait<0>();
@@ -661,43 +712,51 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_apply_kernel
   in.at[0] = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + (int64_t)(r0 + r) * p.ldx + c0 + lc;
   in.step[0] = (int64_t)t.ty * p.ldx;
   in.begin(smem, mine);
+  // mean and M2 of the whole image from the tiles' (all but the last have t.rows positions)
+  const float n_tile = (float)t.rows * (float)t.cpg;
+  const float n_last = (float)(t.S - (p.tiles - 1) * t.rows) * (float)t.cpg;
+  const float n_all = (float)t.S * (float)t.cpg;
   for (int g = warp; g < t.nb; g += NT / 32) {
-    float n = 0.0f, mean = 0.0f, m2 = 0.0f;
+    const float2* d = p.part + (int64_t)img * p.tiles * t.G + cb * t.nb + g;
+    float mean = 0.0f, m2 = 0.0f;
+#pragma unroll 4
+    for (int k = lane; k < p.tiles; k += 32)
+      mean = fmaf(d[(int64_t)k * t.G].x, k == p.tiles - 1 ? n_last : n_tile, mean);
+    mean = warp_sum(mean) / n_all;
 #pragma unroll 4
     for (int k = lane; k < p.tiles; k += 32) {
-      const float2 v = p.part[((int64_t)img * p.tiles + k) * t.G + cb * t.nb + g];
-      const float nk = (float)(min(t.S, (k + 1) * t.rows) - k * t.rows) * (float)t.cpg;
-      chan_merge(n, mean, m2, nk, v.x, v.y);
+      const float2 v = d[(int64_t)k * t.G];
+      const float e = v.x - mean;
+      m2 += fmaf(e * e, k == p.tiles - 1 ? n_last : n_tile, v.y);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float n2 = __shfl_down_sync(0xffffffffu, n, o), mean2 = __shfl_down_sync(0xffffffffu, mean, o),
-                  m22 = __shfl_down_sync(0xffffffffu, m2, o);
-      if (lane < o) chan_merge(n, mean, m2, n2, mean2, m22);
-    }
+    m2 = warp_sum(m2);
     if (lane == 0) {
-      const float rstd = 1.0f / sqrtf(m2 / n + p.eps);
+      const float rstd = 1.0f / sqrtf(m2 / n_all + p.eps);
       fin_mean[g] = mean;
       fin_rstd[g] = rstd;
       if (p.stats != nullptr && tile == 0) {
-        float* d = p.stats + ((int64_t)img * t.G + cb * t.nb + g) * 2;
-        d[0] = mean;
-        d[1] = rstd;
+        float* st = p.stats + ((int64_t)img * t.G + cb * t.nb + g) * 2;
+        st[0] = mean;
+        st[1] = rstd;
       }
     }
   }
   __syncthreads();
   if (mine > 0) {
     NormOut<VN> o;
-    o.init(p, c0, lc, fin_mean, fin_rstd);
-    with_act(p.act, [&](auto act) {
-      for (int k = 0; k < in.steps; ++k) {
-        in.wait(k);
+    o.init(p, img, r0 + r, t.ty, c0, lc, fin_mean, fin_rstd);
+    with_act_out(p, [&](auto act, auto out) {
+      constexpr int A = decltype(act)::value, O = decltype(out)::value;
+      int k = 0;
+      for (; (k + 1) * U <= mine; ++k) {
+        const uint32_t at = in.wait(k);
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (k * U + i < mine)
-            o.template put<decltype(act)::value, XT>(p, img, r0 + r + (k * U + i) * t.ty, c0 + lc,
-                                                     lds128(in.slot(k, i, 0)));
+        for (int i = 0; i < U; ++i) o.template put<A, O, XT>(p, in.get(at, i, 0));
+      }
+      if (k * U < mine) {
+        const uint32_t at = in.wait(k);
+#pragma unroll 1
+        for (int i = 0; k * U + i < mine; ++i) o.template put<A, O, XT>(p, in.get(at, i, 0));
       }
     });
   }
@@ -712,56 +771,85 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_apply_kernel
 // forward has them, dx = a dz + (x p + q').
 template <int VN>
 struct NormGrad {
-  float mean[VN], a[VN], be[VN];
+  uint64_t mean[VN / 2], a[VN / 2], be[VN / 2];   // mean: its negative
   __device__ __forceinline__ void init(const NormBwdArgs& p, int img, int c0, int lc) {
+    float m[VN], av[VN], bv[VN];
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
       const int c = c0 + lc + i;
       const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (int64_t)img * p.t.G + c / p.t.cpg);
-      mean[i] = st.x;
-      a[i] = st.y * (p.gamma ? __ldg(p.gamma + c) : 1.0f);
-      be[i] = p.beta ? __ldg(p.beta + c) : 0.0f;
+      m[i] = -st.x;
+      av[i] = st.y * (p.gamma ? __ldg(p.gamma + c) : 1.0f);
+      bv[i] = p.beta ? __ldg(p.beta + c) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < VN / 2; ++i) {
+      mean[i] = f2_pack(m[2 * i], m[2 * i + 1]);
+      a[i] = f2_pack(av[2 * i], av[2 * i + 1]);
+      be[i] = f2_pack(bv[2 * i], bv[2 * i + 1]);
     }
   }
   template <int ACT, typename XT>
-  __device__ __forceinline__ void sums(const uint4& xr, const uint4& gr, float (&s1)[VN], float (&s2)[VN]) const {
-    float x[VN], g[VN];
-    Vec<XT>::load_raw(xr, x);
-    Vec<XT>::load_raw(gr, g);
+  __device__ __forceinline__ void sums(const uint4& xr, const uint4& gr, uint64_t (&s1)[VN / 2],
+                                       uint64_t (&s2)[VN / 2]) const {
+    uint64_t x[VN / 2], g[VN / 2];
+    load_pairs<XT>(xr, x);
+    load_pairs<XT>(gr, g);
 #pragma unroll
-    for (int i = 0; i < VN; ++i) {
-      const float d = x[i] - mean[i], dz = g[i] * norm_act_slope<ACT>(fmaf(d, a[i], be[i]));
-      s1[i] += dz;
-      s2[i] = fmaf(dz, d, s2[i]);
+    for (int i = 0; i < VN / 2; ++i) {
+      const uint64_t d = f2_add(x[i], mean[i]);
+      uint64_t dz = g[i];
+      if constexpr (ACT != ACT_NONE) dz = f2_mul(dz, norm_act_slope<ACT>(f2_fma(d, a[i], be[i])));
+      s1[i] = f2_add(s1[i], dz);
+      s2[i] = f2_fma(dz, d, s2[i]);
     }
   }
 };
 
 template <int VN>
 struct NormGradOut {
-  float a[VN], b[VN], pp[VN], q[VN];
+  uint64_t a[VN / 2], b[VN / 2], pp[VN / 2], q[VN / 2];
+  uint8_t* dx;             // this thread's next vector, and the bytes from one to the next
+  int64_t step;
   // g1, g2: m1 and m2 of the block's groups
-  __device__ __forceinline__ void init(const NormBwdArgs& p, int img, int c0, int lc, const float* g1,
-                                       const float* g2) {
+  __device__ __forceinline__ void init(const NormBwdArgs& p, int img, int row, int ty, int c0, int lc,
+                                       const float* g1, const float* g2) {
+    constexpr int ES = 16 / VN;
+    float av[VN], bv[VN], pv[VN], qv[VN];
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
       const int c = c0 + lc + i, g = (lc + i) / p.t.cpg;
       const float2 st = __ldg(reinterpret_cast<const float2*>(p.stats) + (int64_t)img * p.t.G + c / p.t.cpg);
-      a[i] = st.y * (p.gamma ? __ldg(p.gamma + c) : 1.0f);
-      b[i] = fmaf(-st.x, a[i], p.beta ? __ldg(p.beta + c) : 0.0f);
-      pp[i] = -st.y * st.y * g2[g];
-      q[i] = -fmaf(st.x, pp[i], st.y * g1[g]);
+      av[i] = st.y * (p.gamma ? __ldg(p.gamma + c) : 1.0f);
+      bv[i] = fmaf(-st.x, av[i], p.beta ? __ldg(p.beta + c) : 0.0f);
+      pv[i] = -st.y * st.y * g2[g];
+      qv[i] = -fmaf(st.x, pv[i], st.y * g1[g]);
     }
+#pragma unroll
+    for (int i = 0; i < VN / 2; ++i) {
+      a[i] = f2_pack(av[2 * i], av[2 * i + 1]);
+      b[i] = f2_pack(bv[2 * i], bv[2 * i + 1]);
+      pp[i] = f2_pack(pv[2 * i], pv[2 * i + 1]);
+      q[i] = f2_pack(qv[2 * i], qv[2 * i + 1]);
+    }
+    dx = static_cast<uint8_t*>(p.dx) + ((int64_t)img * p.dxbs + (int64_t)row * p.lddx + c0 + lc) * ES;
+    step = (int64_t)ty * p.lddx * ES;
   }
   template <int ACT, typename XT>
-  __device__ __forceinline__ void put(void* dx, int64_t at, const uint4& xr, const uint4& gr) const {
-    float x[VN], g[VN], o[VN];
-    Vec<XT>::load_raw(xr, x);
-    Vec<XT>::load_raw(gr, g);
+  __device__ __forceinline__ void put(const uint4& xr, const uint4& gr) {
+    uint64_t x[VN / 2], g[VN / 2];
+    load_pairs<XT>(xr, x);
+    load_pairs<XT>(gr, g);
 #pragma unroll
-    for (int i = 0; i < VN; ++i)
-      o[i] = fmaf(g[i] * norm_act_slope<ACT>(fmaf(x[i], a[i], b[i])), a[i], fmaf(x[i], pp[i], q[i]));
-    store_vec<VN>(dx, at, VN == 8, o);
+    for (int i = 0; i < VN / 2; ++i) {
+      uint64_t dz = g[i];
+      if constexpr (ACT != ACT_NONE) dz = f2_mul(dz, norm_act_slope<ACT>(f2_fma(x[i], a[i], b[i])));
+      x[i] = f2_fma(dz, a[i], f2_fma(x[i], pp[i], q[i]));
+    }
+    float o[VN];
+    unpack_pairs<VN>(x, o);
+    store_vec<VN>(dx, 0, VN == 8, o);
+    dx += step;
   }
 };
 
@@ -823,9 +911,9 @@ __global__ void __launch_bounds__(kNormThreads, 2)
     }
     cp_async_commit();
   }
-  float s1[VN], s2[VN];
+  uint64_t t1[VN / 2], t2[VN / 2];
 #pragma unroll
-  for (int i = 0; i < VN; ++i) s1[i] = s2[i] = 0.0f;
+  for (int i = 0; i < VN / 2; ++i) t1[i] = t2[i] = 0;
   if (mine > 0) {
     NormGrad<VN> k;
     k.init(p, img, c0, lc);
@@ -835,10 +923,13 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 #pragma unroll 1
         for (int i = b * batch; i < min(mine, (b + 1) * batch); ++i)
           k.template sums<decltype(act)::value, XT>(lds128(slab + 2 * i * NT * 16),
-                                                    lds128(slab + (2 * i + 1) * NT * 16), s1, s2);
+                                                    lds128(slab + (2 * i + 1) * NT * 16), t1, t2);
       }
     });
   }
+  float s1[VN], s2[VN];
+  unpack_pairs<VN>(t1, s1);
+  unpack_pairs<VN>(t2, s2);
   reduce_channels<NT, VN>(s1, active, tx, r, t, scratch, ch);
   reduce_channels<NT, VN>(s2, active, tx, r, t, scratch, ch + W);
   if (cs > 1) { cluster_arrive(); cluster_wait(); }
@@ -858,13 +949,11 @@ __global__ void __launch_bounds__(kNormThreads, 2)
   grad_group_means<NT>(p, img, c0, W, scratch, g1, g2);
   if (mine > 0) {
     NormGradOut<VN> o;
-    o.init(p, img, c0, lc, g1, g2);
+    o.init(p, img, r0 + r, t.ty, c0, lc, g1, g2);
     with_act(p.act, [&](auto act) {
 #pragma unroll 1
       for (int i = 0; i < mine; ++i)
-        o.template put<decltype(act)::value, XT>(
-            p.dx, (int64_t)img * p.dxbs + (int64_t)(r0 + r + i * t.ty) * p.lddx + c0 + lc,
-            lds128(slab + 2 * i * NT * 16), lds128(slab + (2 * i + 1) * NT * 16));
+        o.template put<decltype(act)::value, XT>(lds128(slab + 2 * i * NT * 16), lds128(slab + (2 * i + 1) * NT * 16));
     });
   }
   __syncwarp();
@@ -894,23 +983,32 @@ __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_sums_kernel(const
   in.step[0] = (int64_t)t.ty * p.ldx;
   in.step[1] = (int64_t)t.ty * p.lddy;
   in.begin(smem, mine);
-  float s1[VN], s2[VN];
+  uint64_t t1[VN / 2], t2[VN / 2];
 #pragma unroll
-  for (int i = 0; i < VN; ++i) s1[i] = s2[i] = 0.0f;
+  for (int i = 0; i < VN / 2; ++i) t1[i] = t2[i] = 0;
   if (mine > 0) {
     NormGrad<VN> g;
     g.init(p, img, c0, lc);
     with_act(p.act, [&](auto act) {
-      for (int k = 0; k < in.steps; ++k) {
-        in.wait(k);
+      int k = 0;
+      for (; (k + 1) * U <= mine; ++k) {
+        const uint32_t at = in.wait(k);
 #pragma unroll
         for (int i = 0; i < U; ++i)
-          if (k * U + i < mine)
-            g.template sums<decltype(act)::value, XT>(lds128(in.slot(k, i, 0)), lds128(in.slot(k, i, 1)), s1, s2);
+          g.template sums<decltype(act)::value, XT>(in.get(at, i, 0), in.get(at, i, 1), t1, t2);
+      }
+      if (k * U < mine) {
+        const uint32_t at = in.wait(k);
+#pragma unroll 1
+        for (int i = 0; k * U + i < mine; ++i)
+          g.template sums<decltype(act)::value, XT>(in.get(at, i, 0), in.get(at, i, 1), t1, t2);
       }
     });
   }
   cp_async_wait<0>();
+  float s1[VN], s2[VN];
+  unpack_pairs<VN>(t1, s1);
+  unpack_pairs<VN>(t2, s2);
   reduce_channels<NT, VN>(s1, active, tx, r, t, scratch, ch);
   reduce_channels<NT, VN>(s2, active, tx, r, t, scratch, ch + W);
   float* d = p.part + ((int64_t)img * p.tiles + tile) * 2 * t.C + c0;
@@ -949,16 +1047,19 @@ __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_apply_kernel(cons
   grad_group_means<NT>(p, img, c0, W, tot, g1, g2);
   if (mine > 0) {
     NormGradOut<VN> o;
-    o.init(p, img, c0, lc, g1, g2);
+    o.init(p, img, r0 + r, t.ty, c0, lc, g1, g2);
     with_act(p.act, [&](auto act) {
-      for (int k = 0; k < in.steps; ++k) {
-        in.wait(k);
+      int k = 0;
+      for (; (k + 1) * U <= mine; ++k) {
+        const uint32_t at = in.wait(k);
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (k * U + i < mine)
-            o.template put<decltype(act)::value, XT>(
-                p.dx, (int64_t)img * p.dxbs + (int64_t)(r0 + r + (k * U + i) * t.ty) * p.lddx + c0 + lc,
-                lds128(in.slot(k, i, 0)), lds128(in.slot(k, i, 1)));
+        for (int i = 0; i < U; ++i) o.template put<decltype(act)::value, XT>(in.get(at, i, 0), in.get(at, i, 1));
+      }
+      if (k * U < mine) {
+        const uint32_t at = in.wait(k);
+#pragma unroll 1
+        for (int i = 0; k * U + i < mine; ++i)
+          o.template put<decltype(act)::value, XT>(in.get(at, i, 0), in.get(at, i, 1));
       }
     });
   }
@@ -968,11 +1069,11 @@ __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_apply_kernel(cons
 // dbeta and dgamma, and (two passes) each image's sums over its tiles.  A block
 // has 32 channels; its warps share the tiles of an image and their sums are added in
 // order, so every result repeats bit for bit.
-constexpr int kParamWarps = 16;
+constexpr int kParamWarps = 16, kParamImages = 8;
 __global__ void __launch_bounds__(32 * kParamWarps) group_norm_bwd_params_kernel(const NormBwdArgs p, int32_t B,
                                                                                  float* __restrict__ dgamma,
                                                                                  float* __restrict__ dbeta) {
-  __shared__ float sh[2][kParamWarps][32];
+  __shared__ float sh[kParamImages][2][kParamWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int C = p.t.C, c = blockIdx.x * 32 + lane;
   grid_dep_launch();
@@ -980,34 +1081,39 @@ __global__ void __launch_bounds__(32 * kParamWarps) group_norm_bwd_params_kernel
   float sum1 = 0.0f, sum2 = 0.0f;                // this warp's images
   const float* stat = p.stats + (int64_t)(min(c, C - 1) / p.t.cpg) * 2 + 1;
   if (p.tiles > 0) {
-    for (int b = 0; b < B; ++b) {
-      float a1 = 0.0f, a2 = 0.0f;
-      if (c < C) {
-        const float* d = p.part + (int64_t)b * p.tiles * 2 * C + c;
-#pragma unroll 4
-        for (int k = warp; k < p.tiles; k += kParamWarps) {
-          a1 += d[(int64_t)k * 2 * C];
-          a2 += d[(int64_t)k * 2 * C + C];
+    // kParamImages images at a time, all their loads in flight together
+    for (int b0 = 0; b0 < B; b0 += kParamImages) {
+      const int nb = min(kParamImages, B - b0);
+#pragma unroll 1
+      for (int b = 0; b < nb; ++b) {
+        float a1 = 0.0f, a2 = 0.0f;
+        if (c < C) {
+          const float* d = p.part + (int64_t)(b0 + b) * p.tiles * 2 * C + c;
+#pragma unroll 8
+          for (int k = warp; k < p.tiles; k += kParamWarps) {
+            a1 += d[(int64_t)k * 2 * C];
+            a2 += d[(int64_t)k * 2 * C + C];
+          }
         }
+        sh[b][0][warp][lane] = a1;
+        sh[b][1][warp][lane] = a2;
       }
-      sh[0][warp][lane] = a1;
-      sh[1][warp][lane] = a2;
       __syncthreads();
-      if (warp < 2 && c < C) {
+      // warp w: image w / 2, sum w % 2
+      if (warp < 2 * nb && c < C) {
         float a = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kParamWarps; ++k) a += sh[warp][k][lane];
-        p.total[((int64_t)b * 2 + warp) * C + c] = a;
-        sum1 += warp == 0 ? a : a * stat[(int64_t)b * p.t.G * 2];
+        for (int k = 0; k < kParamWarps; ++k) a += sh[warp >> 1][warp & 1][k][lane];
+        p.total[((int64_t)(b0 + (warp >> 1)) * 2 + (warp & 1)) * C + c] = a;
+        sh[warp >> 1][warp & 1][0][lane] = warp & 1 ? a * stat[(int64_t)(b0 + (warp >> 1)) * p.t.G * 2] : a;
       }
       __syncthreads();
+      if (warp < 2)
+        for (int b = 0; b < nb; ++b) sum1 += sh[b][warp][0][lane];
+      __syncthreads();
     }
-    if (warp < 2) sh[warp][0][lane] = sum1;
-    __syncthreads();
-    if (warp == 0 && c < C) {
-      if (dbeta != nullptr) dbeta[c] = sh[0][0][lane];
-      if (dgamma != nullptr) dgamma[c] = sh[1][0][lane];
-    }
+    float* out = warp == 0 ? dbeta : dgamma;
+    if (warp < 2 && c < C && out != nullptr) out[c] = sum1;
     return;
   }
   if (c < C) {
@@ -1017,13 +1123,13 @@ __global__ void __launch_bounds__(32 * kParamWarps) group_norm_bwd_params_kernel
       sum2 = fmaf(p.total[((int64_t)b * 2 + 1) * C + c], stat[(int64_t)b * p.t.G * 2], sum2);
     }
   }
-  sh[0][warp][lane] = sum1;
-  sh[1][warp][lane] = sum2;
+  sh[0][0][warp][lane] = sum1;
+  sh[0][1][warp][lane] = sum2;
   __syncthreads();
   if (warp < 2 && c < C) {
     float a = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kParamWarps; ++k) a += sh[warp][k][lane];
+    for (int k = 0; k < kParamWarps; ++k) a += sh[0][warp][k][lane];
     float* out = warp == 0 ? dbeta : dgamma;
     if (out != nullptr) out[c] = a;
   }
