@@ -475,37 +475,56 @@ def linear_from_codes_hadamard(q_pos: torch.Tensor, q_neg: torch.Tensor, qw: Qua
 # channels last: maps are [B, S, C] with S = H*W (for an NCHW tensor in the
 # channels_last memory format, ``t.permute(0, 2, 3, 1).flatten(1, 2)``).
 
+_NORM_ACTS = {"none": 0, "silu": _lib.SQ_ACT_SILU, "gelu": _lib.SQ_ACT_GELU}
+# the current device's index without the lazy-initialization check; the public call where it is missing
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _norm_act_code(act: str) -> int:
-    return 0 if act == "none" else _act_code(act)
+    code = _NORM_ACTS.get(act)
+    if code is None:
+        raise ValueError(f"unknown activation {act!r}: 'none', 'silu' or 'gelu'")
+    return code
 
 
-def _check_map(x: torch.Tensor, name: str, like: Optional[torch.Tensor] = None):
-    if x.dim() != 3 or x.stride(2) != 1:
+def _stream_ptr(stream: Optional[torch.cuda.Stream], dev: int):
+    """The raw handle of the given stream, else of the current one of device ``dev``."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(dev)
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _map(x: torch.Tensor, name: str, shape=None):
+    """(device, position stride, image stride) of a checked channels-last map [B, S, C]; a
+    single position or image has no stride that matters."""
+    st = x.stride()
+    sh = x.shape
+    if len(st) != 3 or (st[2] != 1 and sh[2] != 1):
         raise ValueError(f"{name} must be a 3-D [B, S, C] tensor with unit channel stride")
-    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    if like is not None and x.shape != like.shape:
-        raise ValueError(f"{name} must have the shape {tuple(like.shape)}, not {tuple(x.shape)}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if shape is not None and sh != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(sh)}")
+    return x.get_device(), st[1] if sh[1] > 1 else max(sh[2], 1), st[0] if sh[0] > 1 else 0
 
 
-def _check_f32(t: Optional[torch.Tensor], shape, name: str):
-    """An optional contiguous fp32 CUDA tensor of the given shape: its pointer or None."""
+def _same_device(dev: int, *others: int):
+    """Launches go to the current device: every tensor has to be there."""
+    cur = _current_device()
+    if dev != cur or any(d != cur for d in others):
+        raise ValueError("tensors must be on the current CUDA device")
+
+
+def _check_f32(t: Optional[torch.Tensor], shape, name: str, dev: int):
+    """An optional contiguous fp32 tensor of the given shape on device ``dev``: its pointer or None."""
     if t is None:
         return None
-    if (t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous()
-            or not t.is_cuda or t.get_device() != torch.cuda.current_device()):
+    if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)} "
                          "on the current device")
     return t.data_ptr()
-
-
-def _row_stride(x: torch.Tensor) -> int:
-    """Element stride of positions (a single position or an empty map has none that matters)."""
-    return x.stride(1) if x.shape[1] > 1 else max(x.shape[2], 1)
-
-
-def _image_stride(x: torch.Tensor) -> int:
-    return x.stride(0) if x.shape[0] > 1 else 0
 
 
 @functools.lru_cache(maxsize=4096)
@@ -524,16 +543,6 @@ def _workspace(n: int, device, stream):
     return ws
 
 
-def _norm_workspace(x: torch.Tensor, groups: int, backward: int, stream):
-    """(keep-alive tensor, pointer, bytes) of a norm call's workspace."""
-    B, S, C = x.shape
-    n = _norm_workspace_size(x.get_device(), B, S, C, groups, _dtype_code(x.dtype), backward)
-    if n == 0:
-        return None, None, 0
-    ws = _workspace(n, x.device, stream)
-    return ws, ws.data_ptr(), n
-
-
 def group_norm_act(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = None,
                    beta: Optional[torch.Tensor] = None, eps: float = 1e-5, act: str = "none",
                    out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
@@ -542,18 +551,26 @@ def group_norm_act(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] =
     act: 'none', 'silu' or 'gelu'.  ``out`` may be ``x`` itself.  With
     ``return_stats`` also the fp32 [B, groups, 2] means and reciprocal deviations
     that ``group_norm_act_backward`` takes."""
-    _check_map(x, "x")
-    B, S, C = x.shape
+    dev, ldx, xbs = _map(x, "x")
+    shape = x.shape
+    B, S, C = shape
     if out is None:
-        out = torch.empty((B, S, C), dtype=out_dtype or x.dtype, device=x.device)
-    _check_map(out, "out", x)
-    stats = torch.empty((B, groups, 2), dtype=torch.float32, device=x.device) if return_stats else None
-    ws, wp, wn = _norm_workspace(x, groups, 0, stream)
-    _lib.check("sq_group_norm_act", _lib.load().sq_group_norm_act(
-        x.data_ptr(), _dtype_code(x.dtype), B, S, C, _row_stride(x), _image_stride(x), groups,
-        _check_f32(gamma, (C,), "gamma"), _check_f32(beta, (C,), "beta"), eps, _norm_act_code(act),
-        out.data_ptr(), _dtype_code(out.dtype), _row_stride(out), _image_stride(out),
-        None if stats is None else stats.data_ptr(), wp, wn, _stream(stream)))
+        out = x.new_empty(shape, dtype=out_dtype)
+        ldy, ybs, dy = C, S * C, dev
+    else:
+        dy, ldy, ybs = _map(out, "out", shape)
+    _same_device(dev, dy)
+    xt = _dtype_code(x.dtype)
+    stats = x.new_empty((B, groups, 2), dtype=torch.float32) if return_stats else None
+    wn = _norm_workspace_size(dev, B, S, C, groups, xt, 0)
+    ws = _workspace(wn, x.device, stream) if wn else None
+    st = _lib.load().sq_group_norm_act(
+        x.data_ptr(), xt, B, S, C, ldx, xbs, groups, _check_f32(gamma, (C,), "gamma", dev),
+        _check_f32(beta, (C,), "beta", dev), eps, _norm_act_code(act), out.data_ptr(),
+        _dtype_code(out.dtype), ldy, ybs, None if stats is None else stats.data_ptr(),
+        None if ws is None else ws.data_ptr(), wn, _stream_ptr(stream, dev))
+    if st:
+        raise SegQuantError("sq_group_norm_act", st)
     return (out, stats) if return_stats else out
 
 
@@ -565,12 +582,15 @@ def quantize_activations_norm(x: torch.Tensor, groups: int, gamma: Optional[torc
     [B*S, C] each (row stride a multiple of 16), in one pass over ``x`` [B, S, C]; they
     feed ``linear_from_codes``.  With ``return_y`` (q+, q-, y), y bf16 [B*S, C] (the
     input of adapters beside the layer)."""
-    _check_map(x, "x")
+    dev, ldx, xbs = _map(x, "x")
     B, S, C = x.shape
     J = len(kseg) - 1
+    _same_device(dev)
+    ldq = (C + 15) // 16 * 16
     if out is None:
-        ldq = (C + 15) // 16 * 16
-        qp, qn = (t[:, :C] for t in torch.empty((2, B * S, ldq), dtype=torch.int8, device=x.device).unbind())
+        qp, qn = x.new_empty((2, B * S, ldq), dtype=torch.int8).unbind()
+        if ldq != C:
+            qp, qn = qp[:, :C], qn[:, :C]
     else:
         qp, qn = out
         for t, name in ((qp, "q_pos"), (qn, "q_neg")):
@@ -579,15 +599,21 @@ def quantize_activations_norm(x: torch.Tensor, groups: int, gamma: Optional[torc
                 raise ValueError(f"{name} must be int8")
         if qp.stride(0) != qn.stride(0):
             raise ValueError("q_pos and q_neg must share a row stride")
-    y = torch.empty((B * S, C), dtype=torch.bfloat16, device=x.device) if return_y else None
+        if B * S > 1:
+            ldq = qp.stride(0)
+    y = x.new_empty((B * S, C), dtype=torch.bfloat16) if return_y else None
     seg, keep = _lib.segments(kseg)
-    ws, wp, wn = _norm_workspace(x, groups, 0, stream)
-    _lib.check("sq_quantize_activations_norm", _lib.load().sq_quantize_activations_norm(
-        x.data_ptr(), _dtype_code(x.dtype), B, S, C, _row_stride(x), _image_stride(x), groups,
-        _check_f32(gamma, (C,), "gamma"), _check_f32(beta, (C,), "beta"), eps, _norm_act_code(act),
-        ctypes.byref(seg), _check_f32(s_pos, (J,), "s_pos"), _check_f32(s_neg, (J,), "s_neg"),
-        qp.data_ptr(), qn.data_ptr(), qp.stride(0) if B * S > 1 else (C + 15) // 16 * 16,
-        None if y is None else y.data_ptr(), C, wp, wn, _stream(stream)))
+    xt = _dtype_code(x.dtype)
+    wn = _norm_workspace_size(dev, B, S, C, groups, xt, 0)
+    ws = _workspace(wn, x.device, stream) if wn else None
+    st = _lib.load().sq_quantize_activations_norm(
+        x.data_ptr(), xt, B, S, C, ldx, xbs, groups, _check_f32(gamma, (C,), "gamma", dev),
+        _check_f32(beta, (C,), "beta", dev), eps, _norm_act_code(act), ctypes.byref(seg),
+        _check_f32(s_pos, (J,), "s_pos", dev), _check_f32(s_neg, (J,), "s_neg", dev), qp.data_ptr(),
+        qn.data_ptr(), ldq, None if y is None else y.data_ptr(), C,
+        None if ws is None else ws.data_ptr(), wn, _stream_ptr(stream, dev))
+    if st:
+        raise SegQuantError("sq_quantize_activations_norm", st)
     return (qp, qn, y) if return_y else (qp, qn)
 
 
@@ -597,32 +623,39 @@ def group_norm_act_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tens
     """Gradients (dx, dgamma, dbeta) of ``group_norm_act``: dx of x's type, dgamma and
     dbeta fp32 [C] (also where gamma or beta is None: those of ones and zeros).
     ``stats`` as returned by the forward call; ``dx`` may be ``x`` or ``dy``."""
-    _check_map(x, "x")
-    _check_map(dy, "dy", x)
-    B, S, C = x.shape
-    if dy.dtype != x.dtype:
-        raise TypeError("dy must have x's dtype")
-    if stats.dim() != 3 or stats.shape[0] != B:
+    dev, ldx, xbs = _map(x, "x")
+    shape = x.shape
+    d2, lddy, dybs = _map(dy, "dy", shape)
+    B, S, C = shape
+    if stats.dim() != 3:
         raise ValueError("stats must be the [B, groups, 2] tensor of the forward call")
     groups = stats.shape[1]
     if dx is None:
-        dx = torch.empty((B, S, C), dtype=x.dtype, device=x.device)
-    _check_map(dx, "dx", x)
-    if dx.dtype != x.dtype:
-        raise TypeError("dx must have x's dtype")
-    grads = torch.empty((2, C), dtype=torch.float32, device=x.device)
-    ws, wp, wn = _norm_workspace(x, groups, 1, stream)
+        dx = x.new_empty(shape)
+        d3, lddx, dxbs = dev, C, S * C
+    else:
+        d3, lddx, dxbs = _map(dx, "dx", shape)
+    if dy.dtype != x.dtype or dx.dtype != x.dtype:
+        raise TypeError("dy and dx must have x's dtype")
+    _same_device(dev, d2, d3)
+    grads = x.new_empty((2, C), dtype=torch.float32)
+    xt = _dtype_code(x.dtype)
+    wn = _norm_workspace_size(dev, B, S, C, groups, xt, 1)
+    ws = _workspace(wn, x.device, stream) if wn else None
     g = grads.data_ptr()
-    _lib.check("sq_group_norm_act_backward", _lib.load().sq_group_norm_act_backward(
-        dy.data_ptr(), _row_stride(dy), _image_stride(dy), x.data_ptr(), _dtype_code(x.dtype), B, S, C,
-        _row_stride(x), _image_stride(x), groups, _check_f32(stats, (B, groups, 2), "stats"),
-        _check_f32(gamma, (C,), "gamma"), _check_f32(beta, (C,), "beta"), _norm_act_code(act),
-        dx.data_ptr(), _row_stride(dx), _image_stride(dx), g, g + 4 * C, wp, wn, _stream(stream)))
-    return dx, grads[0], grads[1]
+    st = _lib.load().sq_group_norm_act_backward(
+        dy.data_ptr(), lddy, dybs, x.data_ptr(), xt, B, S, C, ldx, xbs, groups,
+        _check_f32(stats, (B, groups, 2), "stats", dev), _check_f32(gamma, (C,), "gamma", dev),
+        _check_f32(beta, (C,), "beta", dev), _norm_act_code(act), dx.data_ptr(), lddx, dxbs, g, g + 4 * C,
+        None if ws is None else ws.data_ptr(), wn, _stream_ptr(stream, dev))
+    if st:
+        raise SegQuantError("sq_group_norm_act_backward", st)
+    dgamma, dbeta = grads.unbind()
+    return dx, dgamma, dbeta
 
 
 # ------------------------------------------------------- low-rank adapters
-@dataclasses.dataclass
+@dataclasses.dataclass(frozen=True)
 class Adapters:
     """L low-rank adapters of a [N, K] projection: a bf16 [L, R, K], b bf16 [L, N, R],
     scale fp32 [L] (None: 1).  Adapters of smaller rank are padded with zeros."""
@@ -657,26 +690,26 @@ class Adapters:
 
 
 def _check_rows(t: torch.Tensor, rows: int, cols: int, name: str):
-    _check_2d(t, name)
-    if t.shape[0] != rows or t.shape[1] != cols:
+    """(device, row stride) of a checked [rows, cols] matrix."""
+    st = t.stride()
+    if len(st) != 2 or st[1] != 1:
+        raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], not {list(t.shape)}")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current device")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device(), st[0] if rows > 1 else cols
 
 
-def _check_requests(bounds: torch.Tensor, index: torch.Tensor, adapters: Adapters) -> int:
-    n = index.shape[0] if index.dim() == 1 else -1
-    if (bounds.dtype != torch.int32 or index.dtype != torch.int32 or n < 0 or bounds.dim() != 1
-            or bounds.shape[0] != n + 1 or not bounds.is_contiguous() or not index.is_contiguous()):
+def _check_requests(bounds: torch.Tensor, index: torch.Tensor, adapters: Adapters) -> Tuple[int, int]:
+    """(requests, device) of checked request tensors."""
+    n = index.numel()
+    if (bounds.dtype is not torch.int32 or index.dtype is not torch.int32 or index.dim() != 1
+            or bounds.shape != (n + 1,) or not bounds.is_contiguous() or not index.is_contiguous()):
         raise ValueError("bounds must be int32 [requests + 1] and index int32 [requests]")
-    dev = torch.cuda.current_device()
-    if bounds.get_device() != dev or index.get_device() != dev or adapters.a.get_device() != dev:
-        raise ValueError("bounds, index and adapters must be on the current device")
-    return n
-
-
-def _ld(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    dev = adapters.a.get_device()
+    _same_device(dev, bounds.get_device(), index.get_device())
+    return n, dev
 
 
 def adapter_add(y: torch.Tensor, x: torch.Tensor, adapters: Adapters, bounds: torch.Tensor,
@@ -688,16 +721,19 @@ def adapter_add(y: torch.Tensor, x: torch.Tensor, adapters: Adapters, bounds: to
     fused q | k | v projection with adapters of its own per part, call it on column
     slices of ``y``.  With ``return_hidden`` returns (y, hidden), hidden = x a^T in fp32
     [M, R] for ``adapter_backward``; otherwise y."""
-    n = _check_requests(bounds, index, adapters)
+    n, dev = _check_requests(bounds, index, adapters)
     c = adapters.c_struct()
     M = x.shape[0]
-    _check_rows(x, M, c.K, "x")
-    _check_rows(y, M, c.N, "y")
-    hidden = torch.empty((M, c.R), dtype=torch.float32, device=x.device) if return_hidden else None
-    _lib.check("sq_adapter_add", _lib.load().sq_adapter_add(
-        x.data_ptr(), _dtype_code(x.dtype), M, _ld(x), ctypes.byref(c), bounds.data_ptr(),
-        index.data_ptr(), n, y.data_ptr(), _dtype_code(y.dtype), _ld(y),
-        None if hidden is None else hidden.data_ptr(), _stream(stream)))
+    dx, ldx = _check_rows(x, M, c.K, "x")
+    dy, ldy = _check_rows(y, M, c.N, "y")
+    if dx != dev or dy != dev:
+        raise ValueError("x and y must be on the current CUDA device")
+    hidden = x.new_empty((M, c.R), dtype=torch.float32) if return_hidden else None
+    st = _lib.load().sq_adapter_add(
+        x.data_ptr(), _dtype_code(x.dtype), M, ldx, c, bounds.data_ptr(), index.data_ptr(), n, y.data_ptr(),
+        _dtype_code(y.dtype), ldy, None if hidden is None else hidden.data_ptr(), _stream_ptr(stream, dev))
+    if st:
+        raise SegQuantError("sq_adapter_add", st)
     return (y, hidden) if return_hidden else y
 
 
@@ -706,20 +742,24 @@ def adapter_backward(dy: torch.Tensor, x: torch.Tensor, hidden: torch.Tensor, ad
     """Gradients (dx, da, db) of the term ``adapter_add`` adds: dx [M, K] of x's type
     (zeros in rows without an adapter), da fp32 [L, R, K], db fp32 [L, N, R], each the sum
     over all requests of its adapter.  ``hidden`` as returned by ``adapter_add``."""
-    n = _check_requests(bounds, index, adapters)
+    n, dev = _check_requests(bounds, index, adapters)
     c = adapters.c_struct()
-    M, R = x.shape[0], c.R
-    _check_rows(x, M, c.K, "x")
-    _check_rows(dy, M, c.N, "dy")
-    dx = torch.empty((M, c.K), dtype=x.dtype, device=x.device)
-    da = torch.empty((c.L, R, c.K), dtype=torch.float32, device=x.device)
-    db = torch.empty((c.L, c.N, R), dtype=torch.float32, device=x.device)
+    M, R, K, N, L = x.shape[0], c.R, c.K, c.N, c.L
+    d1, ldx = _check_rows(x, M, K, "x")
+    d2, lddy = _check_rows(dy, M, N, "dy")
+    if d1 != dev or d2 != dev:
+        raise ValueError("x and dy must be on the current CUDA device")
+    dx = x.new_empty((M, K))
+    da = x.new_empty((L, R, K), dtype=torch.float32)
+    db = x.new_empty((L, N, R), dtype=torch.float32)
     wn = _adapter_workspace_size(M, R)
     ws = _workspace(wn, x.device, stream)
-    _lib.check("sq_adapter_backward", _lib.load().sq_adapter_backward(
-        dy.data_ptr(), _dtype_code(dy.dtype), M, _ld(dy), x.data_ptr(), _dtype_code(x.dtype), _ld(x),
-        _check_f32(hidden, (M, R), "hidden"), ctypes.byref(c), bounds.data_ptr(), index.data_ptr(), n,
-        dx.data_ptr(), c.K, da.data_ptr(), db.data_ptr(), ws.data_ptr(), wn, _stream(stream)))
+    st = _lib.load().sq_adapter_backward(
+        dy.data_ptr(), _dtype_code(dy.dtype), M, lddy, x.data_ptr(), _dtype_code(x.dtype), ldx,
+        _check_f32(hidden, (M, R), "hidden", dev), c, bounds.data_ptr(), index.data_ptr(), n,
+        dx.data_ptr(), K, da.data_ptr(), db.data_ptr(), ws.data_ptr(), wn, _stream_ptr(stream, dev))
+    if st:
+        raise SegQuantError("sq_adapter_backward", st)
     return dx, da, db
 
 

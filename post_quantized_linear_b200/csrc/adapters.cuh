@@ -41,44 +41,57 @@ struct AdapterItem {
 
 // Item `slot` when requests are cut into pieces of T rows.  The rows before the
 // first request and behind the last count as two more requests, without an
-// adapter.  Up to 62 requests: a warp counts the pieces of all of them and sums the
+// adapter.  Up to kExactRequests: a warp counts the pieces of all of them and sums the
 // counts, so the items come without gaps.  More: request r's pieces begin at slot
 // floor(start_r / T) + r, which leaves room for a request of any length before the
 // next one's, so its own bounds alone place them and a 32-way search finds the
-// request of a slot.  M / T + Q + 3 slots hold every piece in both.
+// request of a slot.  adapter_slots() slots hold every piece in both.
 // Pieces of a request with bounds outside the batch or an index beyond the adapters
 // are left out, so no read or write leaves the tensors; check_requests raises the
 // range status for them.
+constexpr int kLaneRequests = 8, kExactRequests = 32 * kLaneRequests - 2;
+__host__ __device__ inline int64_t adapter_slots(int M, int Q, int T) {
+  // pieces: every T rows of the batch end at most one, and so does every request's end
+  return T == 1 && Q <= kExactRequests ? M : (int64_t)M / T + Q + 3;
+}
 __device__ __forceinline__ AdapterItem adapter_item(const AdapterArgs& p, int slot, int T) {
   const int lane = threadIdx.x & 31;
   const int count = p.Q + 2;
   auto start = [&](int r) { return r == 0 ? 0 : r <= p.Q + 1 ? __ldg(p.bounds + r - 1) : p.M; };
   AdapterItem it;
-  int s, e, piece, lo;
-  if (count <= 64) {
-    // lane: requests 2 lane and 2 lane + 1
-    const int r = 2 * lane;
-    const int b0 = r < count ? start(r) : p.M, b1 = r < count ? start(r + 1) : p.M,
-              b2 = r + 1 < count ? start(r + 2) : p.M;
-    const int l0 = r >= 1 && r <= p.Q ? __ldg(p.index + r - 1) : -1, l1 = r + 1 <= p.Q ? __ldg(p.index + r) : -1;
-    const int n0 = max(0, b1 - b0 + T - 1) / T, n1 = max(0, b2 - b1 + T - 1) / T;
-    int sum = n0 + n1;
+  it.row = it.n = 0;
+  it.l = -1;
+  int lo, piece;
+  if (count <= 32 * kLaneRequests) {
+    // a lane: `per` requests side by side
+    const int per = (count + 31) >> 5, r0 = lane * per;
+    int n[kLaneRequests], sum = 0;
+    int from = r0 < count ? start(r0) : p.M;
+#pragma unroll
+    for (int i = 0; i < kLaneRequests; ++i) {
+      n[i] = 0;
+      if (i < per && r0 + i < count) {
+        const int to = start(r0 + i + 1);
+        n[i] = max(0, to - from + T - 1) / T;
+        from = to;
+      }
+      sum += n[i];
+    }
+    const int own = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
     }
     const unsigned m = __ballot_sync(0xffffffffu, sum > slot);
-    it.row = it.n = 0;
-    it.l = -1;
     if (m == 0) return it;
+    int left = slot - (sum - own), k = 0;       // within this lane's requests
+#pragma unroll
+    for (int i = 0; i < kLaneRequests - 1; ++i)
+      if (k == i && left >= n[i]) { left -= n[i]; k = i + 1; }
     const int src = __ffs(m) - 1;
-    const int first = slot - (sum - n0 - n1);              // within the lane's two requests
-    const bool second = first >= n0;
-    s = __shfl_sync(0xffffffffu, second ? b1 : b0, src);
-    e = __shfl_sync(0xffffffffu, second ? b2 : b1, src);
-    it.l = __shfl_sync(0xffffffffu, second ? l1 : l0, src);
-    piece = __shfl_sync(0xffffffffu, second ? first - n0 : first, src);
+    lo = __shfl_sync(0xffffffffu, r0 + k, src);
+    piece = __shfl_sync(0xffffffffu, left, src);
   } else {
     lo = 0;
     int span = count;
@@ -91,11 +104,11 @@ __device__ __forceinline__ AdapterItem adapter_item(const AdapterArgs& p, int sl
       span = min(step, span - k * step);
       lo += k * step;
     }
-    s = start(lo);
-    e = start(lo + 1);
-    it.l = (lo == 0 || lo == p.Q + 1) ? -1 : __ldg(p.index + lo - 1);
-    piece = slot - (s / T + lo);
+    piece = slot - (start(lo) / T + lo);
   }
+  if (lo >= count) return it;
+  const int s = start(lo), e = start(lo + 1);
+  it.l = lo == 0 || lo == p.Q + 1 ? -1 : __ldg(p.index + lo - 1);
   it.row = s + piece * T;
   it.n = min(T, e - it.row);
   if (s < 0 || e > p.M || it.l >= p.L || piece < 0 || it.n < 0) it.n = 0;
@@ -113,20 +126,37 @@ __device__ __forceinline__ void check_requests(const AdapterArgs& p, int threads
 }
 
 // ------------------------------------------------------- few rows, fp32 rows
-// One cluster of CTAs per piece of up to eight rows: each CTA contracts its
+// One cluster of CTAs per piece of one or eight rows: each CTA contracts its
 // slice of the long axis on the fp32 lanes, the partial h (or u) are added
 // through distributed shared memory in rank order, and each CTA then writes its
 // slice of the columns.  This is the form for batches of requests of a few rows
 // (one conditioning vector each), which are bound by launch and load latency
 // and by the adapters' bytes, and for fp32 rows.
 constexpr int kFewRows = 8;
-constexpr int kFewThreads = 512;
+constexpr int kFewThreads = 256;
+constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kFewChunk = 512;   // elements of the long axis staged at a time
 
 template <typename T>
 __device__ __forceinline__ float ld_elem(const T* p) { return to_f32(*p); }
 __device__ __forceinline__ void st_elem(float* p, float v) { *p = v; }
 __device__ __forceinline__ void st_elem(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+// Eight consecutive elements widened to fp32.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  if constexpr (Vec<T>::n == 8) {
+    Vec<T>::load(p, v);
+  } else {
+    float a[4], b[4];
+    Vec<T>::load(p, a);
+    Vec<T>::load(p + 4, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+  }
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
 // Slice k of n elements cut into cs slices of whole 8-element vectors.
 __device__ __forceinline__ void long_slice(int n, int cs, int k, int& from, int& to) {
@@ -135,18 +165,48 @@ __device__ __forceinline__ void long_slice(int n, int cs, int k, int& from, int&
   to = min(n, from + per);
 }
 
-// BWD = false: x A^T, then y += scale h B^T.  BWD = true: scale dy B, then dx = u A.
-template <typename XT, typename YT, bool BWD>
-__global__ void __launch_bounds__(kFewThreads, 1)
+// Sums of a vector of 8 ranks per thread over the threads that share it:
+// thread tid holds v[] for ranks 8 * (tid % rv) .., out[r * pitch] receives the total.
+// red: kFewThreads * 8 floats.
+__device__ __forceinline__ void reduce_rank_vectors(const float (&v)[8], bool active, int rv, float* red, float* out,
+                                                    int pitch) {
+  const int tid = threadIdx.x, outs = 8 * rv, lanes = kFewThreads / rv;
+  __syncthreads();
+  if (active) {
+    *reinterpret_cast<float4*>(red + tid * 8) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(red + tid * 8 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  __syncthreads();
+  // `ways` threads share a total, then one adds theirs
+  const int ways = min(lanes, kFewThreads / outs);
+  const int o = tid % outs, wy = tid / outs;
+  float t = 0.0f;
+  if (wy < ways)
+    for (int j = wy; j < lanes; j += ways) t += red[j * outs + o];
+  __syncthreads();
+  if (wy < ways) red[wy * outs + o] = t;
+  __syncthreads();
+  if (tid < outs) {
+    float a = 0.0f;
+    for (int j = 0; j < ways; ++j) a += red[j * outs + tid];
+    out[tid * pitch] = a;
+  }
+}
+
+// T rows (1 or 8).  BWD = false: x A^T, then y += scale h B^T.  BWD = true:
+// scale dy B, then dx = u A.
+template <int T, typename XT, typename YT, bool BWD>
+__global__ void __launch_bounds__(kFewThreads, T == 1 ? 4 : 2)
     adapter_few_rows_kernel(const AdapterArgs p, int cs) {
-  __shared__ __align__(16) float xs[kFewChunk * kFewRows];            // [k][row]
-  __shared__ float part[kFewRows * kAdapterMaxRank];                  // [r][row], this CTA's share
-  __shared__ __align__(16) float full[kFewRows * kAdapterMaxRank];    // [r][row], times scale
-  __shared__ __align__(16) float red[kFewThreads * kFewRows];
+  constexpr int XP = kFewChunk + 4;                                   // row pitch: shifts the banks
+  __shared__ __align__(16) float xs[T == 1 ? 4 : T * XP];             // [row][k]
+  __shared__ __align__(16) float part[T * kAdapterMaxRank];           // [r][row], this CTA's share
+  __shared__ __align__(16) float full[T * kAdapterMaxRank];           // [r][row], times scale
+  __shared__ __align__(16) float red[kFewThreads * 8];
   const int rank = blockIdx.x % cs;
   const int tid = threadIdx.x;
   if (blockIdx.x == 0) check_requests(p, kFewThreads);
-  const AdapterItem it = adapter_item(p, blockIdx.x / cs, kFewRows);
+  const AdapterItem it = adapter_item(p, blockIdx.x / cs, T);
   const int D = BWD ? p.N : p.K, E = BWD ? p.K : p.N, R = p.R;   // contracted, written
   int e0, e1;
   long_slice(E, cs, rank, e0, e1);
@@ -161,145 +221,181 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     return;
   }
   const XT* x = static_cast<const XT*>(p.x) + (int64_t)it.row * p.ldx;
+  YT* y = static_cast<YT*>(p.y) + (int64_t)it.row * p.ldy;
   const __nv_bfloat16* wa = p.a + (int64_t)it.l * R * p.K;
   const __nv_bfloat16* wb = p.b + (int64_t)it.l * p.N * R;
   int d0, d1;
   long_slice(D, cs, rank, d0, d1);
+  // what the second product reads, on its way to L2 while the first one runs
+  if (!BWD) {
+    for (int64_t i = (int64_t)e0 * R + tid * 64; i < (int64_t)e1 * R; i += kFewThreads * 64) prefetch_l2(wb + i);
+    if (T == 1)
+      for (int c = e0 + tid * (128 / (int)sizeof(YT)); c < e1; c += kFewThreads * (128 / (int)sizeof(YT)))
+        prefetch_l2(y + c);
+  } else {
+    for (int i = tid; i < R * ((e1 - e0 + 63) / 64); i += kFewThreads)
+      prefetch_l2(wa + (int64_t)(i % R) * p.K + e0 + i / R * 64);
+  }
   const int RV = R / 8;
   const int warp = tid >> 5, lane = tid & 31;
-
-  // BWD: thread = (vector of 8 ranks, one of `nl` lanes over n), 8 x 8 sums.
-  // Forward: warp = (four ranks, one of `kg` groups over k), 4 x 8 sums a lane.
+  // BWD: thread = (vector of 8 ranks, one of `nl` lanes over n), 8 x T sums.
+  // Forward: warp = (four ranks, one of `kg` groups over k), 4 x T sums a lane.
   const int rv = tid % RV, nl_i = tid / RV, nl = kFewThreads / RV;
-  const int quads = (R + 3) / 4, kg = max(1, (kFewThreads / 32) / quads);
-  float acc[BWD ? 64 : 32];
-  if (BWD) {
+
+  if constexpr (BWD) {
+    float acc[T][8];
 #pragma unroll
-    for (int i = 0; i < (BWD ? 64 : 32); ++i) acc[i] = 0.0f;
-  }
-  for (int i = tid; i < kFewRows * R; i += kFewThreads) part[i] = 0.0f;
-  for (int c0 = d0; c0 < d1; c0 += kFewChunk) {
-    const int len = min(kFewChunk, d1 - c0);
-    __syncthreads();
-    for (int i = tid; i < len * kFewRows; i += kFewThreads) {
-      const int m = i / len, k = i % len;
-      xs[k * kFewRows + m] = m < it.n ? ld_elem(x + (int64_t)m * p.ldx + c0 + k) : 0.0f;
-    }
-    __syncthreads();
-    if constexpr (BWD) {
+    for (int m = 0; m < T; ++m)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[m][i] = 0.0f;
+    for (int c0 = d0; c0 < d1; c0 += kFewChunk) {
+      const int len = min(kFewChunk, d1 - c0);
+      if constexpr (T > 1) {
+        __syncthreads();
+        if (warp < it.n)
+          for (int k = lane * 8; k < len; k += 256) {
+            float v[8];
+            load8(x + (int64_t)warp * p.ldx + c0 + k, v);
+            *reinterpret_cast<float4*>(xs + warp * XP + k) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(xs + warp * XP + k + 4) = make_float4(v[4], v[5], v[6], v[7]);
+          }
+        else if (warp < T)
+          for (int k = lane; k < len; k += 32) xs[warp * XP + k] = 0.0f;
+        __syncthreads();
+      }
       if (nl_i < nl) {
+#pragma unroll 2
         for (int k = nl_i; k < len; k += nl) {
           float w[8];
           Vec<__nv_bfloat16>::load(wb + (int64_t)(c0 + k) * R + rv * 8, w);
-          const float4 v0 = *reinterpret_cast<const float4*>(xs + k * kFewRows);
-          const float4 v1 = *reinterpret_cast<const float4*>(xs + k * kFewRows + 4);
-          const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int m = 0; m < T; ++m) {
+            const float v = T == 1 ? ld_elem(x + c0 + k) : xs[m * XP + k];
 #pragma unroll
-            for (int m = 0; m < 8; ++m) acc[i * 8 + m] = fmaf(w[i], v[m], acc[i * 8 + m]);
-        }
-      }
-    } else {
-      // quads beyond the warps go round again; kg > 1 only when they all fit
-      for (int q = kg > 1 ? warp % quads : warp; q < quads; q += (kg > 1 ? quads : kFewThreads / 32)) {
-        const int g = kg > 1 ? warp / quads : 0;
-        float s[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = 0.0f;
-        if (g < kg) {
-          for (int k = (g * 32 + lane) * 8; k < len; k += kg * 256) {
-            float w[4][8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (q * 4 + i < R) Vec<__nv_bfloat16>::load(wa + (int64_t)(q * 4 + i) * p.K + c0 + k, w[i]);
-              else
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[i][j] = 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 v0 = *reinterpret_cast<const float4*>(xs + (k + j) * kFewRows);
-              const float4 v1 = *reinterpret_cast<const float4*>(xs + (k + j) * kFewRows + 4);
-              const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int m = 0; m < 8; ++m) s[i * 8 + m] = fmaf(w[i][j], v[m], s[i * 8 + m]);
-            }
+            for (int i = 0; i < 8; ++i) acc[m][i] = fmaf(w[i], v, acc[m][i]);
           }
         }
-        // fold 32 sums over 32 lanes: lane i ends with the total of sum i
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (i < o) {
-              const float give = (lane & o) ? s[i] : s[i + o];
-              const float keep = (lane & o) ? s[i + o] : s[i];
-              s[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-            }
-          }
-        }
-        if (g < kg) red[(g * quads + q) * 32 + lane] = s[0];
-      }
-      __syncthreads();
-      for (int i = tid; i < R * kFewRows; i += kFewThreads) {
-        float t = part[i];
-        for (int g = 0; g < kg; ++g) t += red[(g * quads + i / 32) * 32 + i % 32];
-        part[i] = t;
       }
     }
-  }
-  if constexpr (BWD) {
-    // add the nl lanes' sums, one rank of each vector at a time
+#pragma unroll 1
+    for (int m = 0; m < T; ++m) {
+      float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      __syncthreads();
-      if (nl_i < nl) {
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
 #pragma unroll
-        for (int m = 0; m < 8; ++m) red[tid * 8 + m] = acc[i * 8 + m];
+      for (int q = 0; q < T; ++q)
+        if (q == m) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = acc[q][i];
+        }
+      if (m < it.n) reduce_rank_vectors(v, nl_i < nl, RV, red, part + m, T);
+    }
+  } else {
+    const int quads = (R + 3) / 4, kg = max(1, kFewWarps / quads);
+    for (int i = tid; i < T * R; i += kFewThreads) part[i] = 0.0f;
+    for (int c0 = d0; c0 < d1; c0 += kFewChunk) {
+      const int len = min(kFewChunk, d1 - c0);
+      if constexpr (T > 1) {
+        __syncthreads();
+        if (warp < it.n)
+          for (int k = lane * 8; k < len; k += 256) {
+            float v[8];
+            load8(x + (int64_t)warp * p.ldx + c0 + k, v);
+            *reinterpret_cast<float4*>(xs + warp * XP + k) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(xs + warp * XP + k + 4) = make_float4(v[4], v[5], v[6], v[7]);
+          }
+        else if (warp < T)
+          for (int k = lane; k < len; k += 32) xs[warp * XP + k] = 0.0f;
+        __syncthreads();
+      }
+      // quads beyond the warps go round again; kg > 1 only when they all fit
+      for (int q = kg > 1 ? warp % quads : warp; q < quads; q += (kg > 1 ? quads : kFewWarps)) {
+        const int g = kg > 1 ? warp / quads : 0;
+        float s[4 * T];
+#pragma unroll
+        for (int i = 0; i < 4 * T; ++i) s[i] = 0.0f;
+        if (g < kg) {
+          for (int k = (g * 32 + lane) * 8; k < len; k += kg * 256) {
+            uint4 raw[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              raw[i] = make_uint4(0u, 0u, 0u, 0u);
+              if (q * 4 + i < R)
+                raw[i] = __ldg(reinterpret_cast<const uint4*>(wa + (int64_t)(q * 4 + i) * p.K + c0 + k));
+            }
+#pragma unroll
+            for (int m = 0; m < T; ++m) {
+              float v[8];
+              if constexpr (T == 1) {
+                load8(x + c0 + k, v);
+              } else {
+                const float4 v0 = *reinterpret_cast<const float4*>(xs + m * XP + k);
+                const float4 v1 = *reinterpret_cast<const float4*>(xs + m * XP + k + 4);
+                v[0] = v0.x; v[1] = v0.y; v[2] = v0.z; v[3] = v0.w;
+                v[4] = v1.x; v[5] = v1.y; v[6] = v1.z; v[7] = v1.w;
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float w[8];
+                Vec<__nv_bfloat16>::load_raw(raw[i], w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[i * T + m] = fmaf(w[j], v[j], s[i * T + m]);
+              }
+            }
+          }
+        }
+        if constexpr (T == 8) {
+          // fold 32 sums over 32 lanes: lane i ends with the total of sum i
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (i < o) {
+                const float give = (lane & o) ? s[i] : s[i + o];
+                const float keep = (lane & o) ? s[i + o] : s[i];
+                s[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+              }
+            }
+          }
+          if (g < kg) red[(g * quads + q) * 32 + lane] = s[0];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i] = warp_sum(s[i]);
+          if (g < kg && lane < 4) red[(g * quads + q) * 4 + lane] = lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3];
+        }
       }
       __syncthreads();
-      // 8 * RV totals; `ways` threads share each, then one adds theirs
-      const int outs = 8 * RV;
-      const int ways = min(nl, kFewThreads / outs);
-      const int o = tid % outs, wy = tid / outs;
-      float t = 0.0f;
-      if (wy < ways)
-        for (int j = wy; j < nl; j += ways) t += red[j * outs + o];
-      __syncthreads();
-      if (wy < ways) red[wy * outs + o] = t;
-      __syncthreads();
-      if (tid < outs) {
-        float a = 0.0f;
-        for (int j = 0; j < ways; ++j) a += red[j * outs + tid];
-        part[(tid / 8 * 8 + i) * kFewRows + tid % 8] = a;
+      for (int i = tid; i < R * T; i += kFewThreads) {
+        float t = part[i];
+        for (int g = 0; g < kg; ++g) t += red[g * quads * 4 * T + i];
+        part[i] = t;
       }
+      if (T == 1) __syncthreads();
     }
   }
   __syncthreads();
   if (cs > 1) { cluster_arrive(); cluster_wait(); }
-  const float scale = p.scale != nullptr ? p.scale[it.l] : 1.0f;
-  for (int i = tid; i < kFewRows * R; i += kFewThreads) {
+  const float scale = p.scale != nullptr ? __ldg(p.scale + it.l) : 1.0f;
+  for (int i = tid; i < T * R; i += kFewThreads) {
+    const int m = i % T;
     float t = 0.0f;
-    if (cs > 1) {
-      for (int k = 0; k < cs; ++k) t += dsmem_f32(part + i, k);
-    } else {
-      t = part[i];
+    if (m < it.n) {
+      if (cs > 1) {
+        for (int k = 0; k < cs; ++k) t += dsmem_f32(part + i, k);
+      } else {
+        t = part[i];
+      }
     }
     full[i] = t * scale;
-    const int m = i % kFewRows;
     if (p.h != nullptr && rank == 0 && m < it.n)
-      p.h[(int64_t)(it.row + m) * R + i / kFewRows] = BWD ? t * scale : t;
+      p.h[(int64_t)(it.row + m) * R + i / T] = BWD ? t * scale : t;
   }
   __syncthreads();
   if (cs > 1) cluster_arrive();
-  YT* y = static_cast<YT*>(p.y) + (int64_t)it.row * p.ldy;
   for (int c = e0 + tid; c < e1; c += kFewThreads) {
-    float o[kFewRows];
+    float o[T];
 #pragma unroll
-    for (int m = 0; m < kFewRows; ++m) o[m] = 0.0f;
+    for (int m = 0; m < T; ++m) o[m] = 0.0f;
     for (int r = 0; r < R; r += 8) {
       float w[8];
       if constexpr (BWD) {
@@ -308,17 +404,25 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       } else {
         Vec<__nv_bfloat16>::load(wb + (int64_t)c * R + r, w);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 v0 = *reinterpret_cast<const float4*>(full + (r + i) * kFewRows);
-        const float4 v1 = *reinterpret_cast<const float4*>(full + (r + i) * kFewRows + 4);
+      if constexpr (T == 1) {
+        const float4 v0 = *reinterpret_cast<const float4*>(full + r);
+        const float4 v1 = *reinterpret_cast<const float4*>(full + r + 4);
         const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-        for (int m = 0; m < 8; ++m) o[m] = fmaf(w[i], v[m], o[m]);
+        for (int i = 0; i < 8; ++i) o[0] = fmaf(w[i], v[i], o[0]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 v0 = *reinterpret_cast<const float4*>(full + (r + i) * T);
+          const float4 v1 = *reinterpret_cast<const float4*>(full + (r + i) * T + 4);
+          const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+          for (int m = 0; m < T; ++m) o[m] = fmaf(w[i], v[m], o[m]);
+        }
       }
     }
 #pragma unroll
-    for (int m = 0; m < kFewRows; ++m)
+    for (int m = 0; m < T; ++m)
       if (m < it.n) {
         YT* d = y + (int64_t)m * p.ldy + c;
         st_elem(d, BWD ? o[m] : to_f32(*d) + o[m]);
@@ -329,9 +433,55 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 }
 
 // ------------------------------------------------- gradients of the adapters
-// out[l][r][c] = sum over the rows of requests that use l of f[m][r] * g[m][c]
-// (TRANS: written as out[l][c][r]), times scale_l when asked.  One CTA per
-// (64 columns, adapter): rows in order, so the sums repeat bit for bit.
+constexpr int kGradPiece = 64;
+
+// The pieces of kGradPiece rows of adapter l's requests, found by a warp together, 32
+// requests at a time; the CTAs of a cluster take them in turn.
+struct GradPieces {
+  const int32_t* bounds;
+  const int32_t* index;
+  int M, Q, l, rank, cs;
+  int base = -32, pos = 0, end = 0, s = 0, e = 0, turn = 0;
+  unsigned mask = 0;
+  __device__ __forceinline__ bool next(int& m0, int& n) {
+    const int lane = threadIdx.x & 31;
+    while (pos >= end) {
+      while (mask == 0) {
+        base += 32;
+        if (base >= Q) return false;
+        const int q = base + lane;
+        bool hit = false;
+        if (q < Q && __ldg(index + q) == l) {
+          s = max(0, __ldg(bounds + q));
+          e = min(M, __ldg(bounds + q + 1));
+          hit = s < e;
+        }
+        mask = __ballot_sync(0xffffffffu, hit);
+      }
+      const int src = __ffs(mask) - 1;
+      mask &= mask - 1;
+      pos = __shfl_sync(0xffffffffu, s, src);
+      end = __shfl_sync(0xffffffffu, e, src);
+    }
+    m0 = pos;
+    n = min(kGradPiece, end - pos);
+    pos += kGradPiece;
+    return true;
+  }
+  __device__ __forceinline__ bool mine(int& m0, int& n) {
+    while (next(m0, n)) {
+      const bool is = turn == rank;
+      turn = turn + 1 == cs ? 0 : turn + 1;
+      if (is) return true;
+    }
+    return false;
+  }
+};
+
+// fp32 rows: out[l][r][c] = sum over the rows of requests that use l of f[m][r] * g[m][c]
+// (TRANS: written as out[l][c][r]), times scale_l when asked.  One cluster per
+// (64 columns, adapter): its CTAs share the pieces and add their sums in rank order,
+// so they repeat bit for bit.
 struct AdapterGradArgs {
   const float* f;                // [M, R]
   const void* g;                 // [M, C]
@@ -340,15 +490,18 @@ struct AdapterGradArgs {
   const int32_t* bounds;
   const int32_t* index;
   float* out;
-  int32_t M, C, R, L, Q;
+  int32_t M, C, R, L, Q, cs;
 };
 constexpr int kGradCols = 64, kGradRows = 32, kGradThreads = 256;
 
 template <typename GT, bool TRANS>
 __global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const AdapterGradArgs p) {
-  __shared__ __align__(16) float fs[kGradRows][kAdapterMaxRank];
-  __shared__ __align__(16) float gs[kGradRows][kGradCols];
-  const int tid = threadIdx.x, l = blockIdx.y, c0 = blockIdx.x * kGradCols;
+  // rows of f and g, then the sums [rank][column]
+  __shared__ __align__(16) float sh[kAdapterMaxRank * kGradCols];
+  static_assert(kGradRows * (kAdapterMaxRank + kGradCols) <= kAdapterMaxRank * kGradCols, "");
+  float* fs = sh;                                   // [row][rank]
+  float* gs = sh + kGradRows * kAdapterMaxRank;     // [row][column]
+  const int tid = threadIdx.x, l = blockIdx.y, rank = blockIdx.x % p.cs, c0 = blockIdx.x / p.cs * kGradCols;
   // thread: 8 columns (cx) and the ranks ry, ry + 32, ...
   const int cx = (tid % 8) * 8, ry = tid / 8;
   float acc[4][8];
@@ -356,31 +509,37 @@ __global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const Adapte
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
-  for (int q = 0; q < p.Q; ++q) {
-    if (p.index[q] != l) continue;
-    const int s = max(0, p.bounds[q]), e = min(p.M, p.bounds[q + 1]);
-    for (int m0 = s; m0 < e; m0 += kGradRows) {
-      const int n = min(kGradRows, e - m0);
+  GradPieces pieces{p.bounds, p.index, p.M, p.Q, l, rank, p.cs};
+  const int R4 = p.R / 4;
+  int first, count;
+  while (pieces.mine(first, count)) {
+    for (int m0 = first; m0 < first + count; m0 += kGradRows) {
+      const int n = min(kGradRows, first + count - m0);
       __syncthreads();
-      for (int i = tid; i < kGradRows * p.R; i += kGradThreads) {
-        const int m = i / p.R, r = i % p.R;
-        fs[m][r] = m < n ? p.f[(int64_t)(m0 + m) * p.R + r] : 0.0f;
+      for (int i = tid; i < n * R4; i += kGradThreads) {
+        const int m = i / R4, r = i % R4 * 4;
+        *reinterpret_cast<float4*>(fs + m * kAdapterMaxRank + r) =
+            __ldg(reinterpret_cast<const float4*>(p.f + (int64_t)(m0 + m) * p.R + r));
       }
-      for (int i = tid; i < kGradRows * kGradCols; i += kGradThreads) {
-        const int m = i / kGradCols, c = i % kGradCols;
-        gs[m][c] = m < n && c0 + c < p.C
-                       ? ld_elem(static_cast<const GT*>(p.g) + (int64_t)(m0 + m) * p.ldg + c0 + c)
-                       : 0.0f;
+      // C is a multiple of 16
+      for (int i = tid; i < n * (kGradCols / 8); i += kGradThreads) {
+        const int m = i / (kGradCols / 8), c = i % (kGradCols / 8) * 8;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        if (c0 + c < p.C) load8(static_cast<const GT*>(p.g) + (int64_t)(m0 + m) * p.ldg + c0 + c, v);
+        *reinterpret_cast<float4*>(gs + m * kGradCols + c) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(gs + m * kGradCols + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
       }
       __syncthreads();
       for (int m = 0; m < n; ++m) {
-        const float4 v0 = *reinterpret_cast<const float4*>(&gs[m][cx]);
-        const float4 v1 = *reinterpret_cast<const float4*>(&gs[m][cx + 4]);
+        const float4 v0 = *reinterpret_cast<const float4*>(gs + m * kGradCols + cx);
+        const float4 v1 = *reinterpret_cast<const float4*>(gs + m * kGradCols + cx + 4);
         const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (ry + 32 * i < p.R) {
-            const float w = fs[m][ry + 32 * i];
+            const float w = fs[m * kAdapterMaxRank + ry + 32 * i];
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(w, v[j], acc[i][j]);
           }
@@ -388,19 +547,40 @@ __global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const Adapte
       }
     }
   }
-  const float scale = p.scale != nullptr ? p.scale[l] : 1.0f;
+  if (p.cs > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (ry + 32 * i < p.R) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 4)
+          *reinterpret_cast<float4*>(sh + (ry + 32 * i) * kGradCols + cx + j) =
+              make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+      }
+    cluster_arrive();
+    cluster_wait();
+  }
+  const float scale = p.scale != nullptr ? __ldg(p.scale + l) : 1.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ry + 32 * i;
-    if (r < p.R) {
+    // the CTAs of the cluster write the ranks in turn
+    if (r < p.R && (p.cs == 1 || r % p.cs == rank)) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int c = c0 + cx + j;
+        float v = acc[i][j];
+        if (p.cs > 1) {
+          v = 0.0f;
+          for (int k = 0; k < p.cs; ++k) v += dsmem_f32(sh + r * kGradCols + cx + j, k);
+        }
         if (c < p.C)
-          p.out[TRANS ? ((int64_t)l * p.C + c) * p.R + r : ((int64_t)l * p.R + r) * p.C + c] = acc[i][j] * scale;
+          p.out[TRANS ? ((int64_t)l * p.C + c) * p.R + r : ((int64_t)l * p.R + r) * p.C + c] = v * scale;
       }
     }
   }
+  __syncwarp();
+  if (p.cs > 1) { cluster_arrive(); cluster_wait(); }
 }
 
 }  // namespace sq

@@ -424,49 +424,7 @@ struct AdapterGradTileArgs {
   long long wait_budget;
   int32_t starve;
 };
-constexpr int kGradPiece = 64;
 __host__ __device__ inline int adapter_grad_f_bytes(int rp) { return (3 * rp + 63) / 64 * 8192; }
-
-// The pieces of adapter l's requests, found by a warp together, 32 requests at a time.
-struct GradPieces {
-  int base = -32, pos = 0, end = 0, s = 0, e = 0;
-  unsigned mask = 0;
-  __device__ __forceinline__ bool next(const AdapterGradTileArgs& p, int l, int& m0, int& n) {
-    const int lane = threadIdx.x & 31;
-    while (pos >= end) {
-      while (mask == 0) {
-        base += 32;
-        if (base >= p.Q) return false;
-        const int q = base + lane;
-        bool hit = false;
-        if (q < p.Q && __ldg(p.index + q) == l) {
-          s = max(0, __ldg(p.bounds + q));
-          e = min(p.M, __ldg(p.bounds + q + 1));
-          hit = s < e;
-        }
-        mask = __ballot_sync(0xffffffffu, hit);
-      }
-      const int src = __ffs(mask) - 1;
-      mask &= mask - 1;
-      pos = __shfl_sync(0xffffffffu, s, src);
-      end = __shfl_sync(0xffffffffu, e, src);
-    }
-    m0 = pos;
-    n = min(kGradPiece, end - pos);
-    pos += kGradPiece;
-    return true;
-  }
-  // the next piece of this rank
-  int turn = 0;
-  __device__ __forceinline__ bool mine(const AdapterGradTileArgs& p, int l, int rank, int& m0, int& n) {
-    while (next(p, l, m0, n)) {
-      const bool is = turn == rank;
-      turn = turn + 1 == p.cs ? 0 : turn + 1;
-      if (is) return true;
-    }
-    return false;
-  }
-};
 
 template <int RB>
 __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
@@ -514,7 +472,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  GradPieces pieces;
+  GradPieces pieces{p.bounds, p.index, p.M, p.Q, l, rank, cs};
   int m0, n, i = 0;
   bool ok = true;
   if (warp == 0) {
@@ -522,7 +480,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
     const CUtensorMap* tg = which ? &tg1 : &tg0;
     if (lane == 0) tma_prefetch_desc(tg);
     ok = p.starve == 0;
-    while (ok && pieces.mine(p, l, rank, m0, n)) {
+    while (ok && pieces.mine(m0, n)) {
       const int s = i % NS;
       if (i >= NS && !(ok = wait_warp(smem_u32(empty + s), (i / NS - 1) & 1, abort_flag, budget))) break;
       if (lane == 0) {
@@ -538,7 +496,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     const int cols = 3 * RP, n1 = cols > 256 ? 192 : cols, n2 = cols - n1;
-    while (ok && pieces.mine(p, l, rank, m0, n)) {
+    while (ok && pieces.mine(m0, n)) {
       const int s = i % NS;
       if (!(ok = wait_warp(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
       if (!(ok = wait_warp(smem_u32(ready + s), (i / NS) & 1, abort_flag, budget))) break;
@@ -584,7 +542,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
         }
       }
     };
-    bool more = pieces.mine(p, l, rank, m0, n);
+    bool more = pieces.mine(m0, n);
     if (more) fetch(m0, n);
     while (more) {
       const int s = i % NS, cnt = n;
@@ -610,7 +568,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
           }
         }
       }
-      more = pieces.mine(p, l, rank, m0, n);
+      more = pieces.mine(m0, n);
       if (more) fetch(m0, n);                              // in flight while this piece is handed over
       if (cnt < kGradPiece) {
         // rows behind the piece belong to other requests: cleared, whatever they hold

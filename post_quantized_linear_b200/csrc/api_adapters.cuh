@@ -44,28 +44,44 @@ sq::AdapterArgs adapter_args(const sq_adapters* ad, const int32_t* bounds, const
   return a;
 }
 
-template <bool BWD>
-sq_status launch_few_rows(const sq::AdapterArgs& a, sq_dtype xt, sq_dtype yt, cudaStream_t s) {
-  const int64_t slots = (int64_t)a.M / sq::kFewRows + a.Q + 3;
-  // enough CTAs for one wave over the SMs, no slice shorter than a warp's loads
+template <int T, bool BWD>
+sq_status launch_few_rows_t(const sq::AdapterArgs& a, sq_dtype xt, sq_dtype yt, cudaStream_t s) {
+  const int64_t slots = sq::adapter_slots(a.M, a.Q, T);
+  const int D = BWD ? a.N : a.K;
+  // as many CTAs per piece as the SMs hold at once, each with a warp's load of the long axis
+  const int64_t room = (int64_t)num_sms() * (T == 1 ? 4 : 2);
   int cs = 1;
-  while (cs < 8 && slots * cs * 2 <= 3 * (int64_t)num_sms() && std::min(a.K, a.N) >= 512 * cs) cs *= 2;
+  while (cs < 8 && slots * cs * 2 <= room && D >= 256 * cs) cs *= 2;
   const dim3 grid((unsigned)(slots * cs));
   if (xt == SQ_BF16)
     return yt == SQ_BF16
-               ? launch_grid<sq::adapter_few_rows_kernel<__nv_bfloat16, __nv_bfloat16, BWD>>(grid, sq::kFewThreads, 0, cs, false, s, a, cs)
-               : launch_grid<sq::adapter_few_rows_kernel<__nv_bfloat16, float, BWD>>(grid, sq::kFewThreads, 0, cs, false, s, a, cs);
+               ? launch_grid<sq::adapter_few_rows_kernel<T, __nv_bfloat16, __nv_bfloat16, BWD>>(grid, sq::kFewThreads, 0, cs, false, s, a, cs)
+               : launch_grid<sq::adapter_few_rows_kernel<T, __nv_bfloat16, float, BWD>>(grid, sq::kFewThreads, 0, cs, false, s, a, cs);
   return yt == SQ_BF16
-             ? launch_grid<sq::adapter_few_rows_kernel<float, __nv_bfloat16, BWD>>(grid, sq::kFewThreads, 0, cs, false, s, a, cs)
-             : launch_grid<sq::adapter_few_rows_kernel<float, float, BWD>>(grid, sq::kFewThreads, 0, cs, false, s, a, cs);
+             ? launch_grid<sq::adapter_few_rows_kernel<T, float, __nv_bfloat16, BWD>>(grid, sq::kFewThreads, 0, cs, false, s, a, cs)
+             : launch_grid<sq::adapter_few_rows_kernel<T, float, float, BWD>>(grid, sq::kFewThreads, 0, cs, false, s, a, cs);
+}
+
+// Pieces of one row where requests have one on average, of eight elsewhere.
+template <bool BWD>
+sq_status launch_few_rows(const sq::AdapterArgs& a, sq_dtype xt, sq_dtype yt, cudaStream_t s) {
+  return a.M <= a.Q ? launch_few_rows_t<1, BWD>(a, xt, yt, s)
+                    : launch_few_rows_t<sq::kFewRows, BWD>(a, xt, yt, s);
 }
 
 template <bool TRANS>
-sq_status launch_adapter_grad(const sq::AdapterGradArgs& g, sq_dtype gt, cudaStream_t s) {
-  const dim3 grid((unsigned)((g.C + sq::kGradCols - 1) / sq::kGradCols), (unsigned)g.L);
+sq_status launch_adapter_grad(sq::AdapterGradArgs g, sq_dtype gt, cudaStream_t s) {
+  const int tiles = (g.C + sq::kGradCols - 1) / sq::kGradCols;
+  // the cluster shares an adapter's pieces: enough CTAs for two waves
+  const int used = std::max(1, std::min(g.L, g.Q));
+  const int64_t per = std::max<int64_t>(1, (int64_t)g.M / sq::kGradPiece / used);
+  int cs = 1;
+  while (cs < 8 && cs * 2 <= per && (int64_t)tiles * used * cs * 2 <= 6 * (int64_t)num_sms()) cs *= 2;
+  g.cs = cs;
+  const dim3 grid((unsigned)(tiles * cs), (unsigned)g.L);
   if (gt == SQ_BF16)
-    return launch_grid<sq::adapter_grad_kernel<__nv_bfloat16, TRANS>>(grid, sq::kGradThreads, 0, 1, false, s, g);
-  return launch_grid<sq::adapter_grad_kernel<float, TRANS>>(grid, sq::kGradThreads, 0, 1, false, s, g);
+    return launch_grid<sq::adapter_grad_kernel<__nv_bfloat16, TRANS>>(grid, sq::kGradThreads, 0, cs, false, s, g);
+  return launch_grid<sq::adapter_grad_kernel<float, TRANS>>(grid, sq::kGradThreads, 0, cs, false, s, g);
 }
 
 // A tiled map of rank 2 or 3, boxes with 128-byte swizzled rows; strides in bytes
@@ -145,7 +161,7 @@ sq_status launch_tile_rb(const sq::AdapterArgs& a, const CUtensorMap& tx, const 
   t.cs = cs;
   cudaError_t e = smem_limit<kern>(kSmemPerSm);
   if (e != cudaSuccess) return cuda_status(e);
-  const int64_t slots = (int64_t)a.M / sq::kTileRows + a.Q + 3;
+  const int64_t slots = sq::adapter_slots(a.M, a.Q, sq::kTileRows);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(slots * cs));
   cfg.blockDim = dim3(sq::kTileThreads);

@@ -58,7 +58,7 @@ struct NormArgs {
   const float* s_pos;
   const float* s_neg;
   float* stats;                  // [B][G][2] mean, rstd; or null
-  float2* part;                  // two passes: [B][tiles][G] mean, M2 of each tile
+  float2* part;                  // two passes: [B][G][tiles] mean, M2 of each tile
   SegBounds kseg;
   NormTile t;
   int32_t tiles;
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_stats_kernel
   }
   reduce_groups<NT, VN>(s, active, tx, r, t, scratch, ch, g_m2);
   for (int g = threadIdx.x; g < t.nb; g += NT)
-    p.part[((int64_t)img * p.tiles + tile) * t.G + cb * t.nb + g] = make_float2(g_mean[g], g_m2[g]);
+    p.part[((int64_t)img * t.G + cb * t.nb + g) * p.tiles + tile] = make_float2(g_mean[g], g_m2[g]);
 }
 
 // Pass 2: the same tiles in the opposite order (the last ones read are the
@@ -717,15 +717,15 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_apply_kernel
   const float n_last = (float)(t.S - (p.tiles - 1) * t.rows) * (float)t.cpg;
   const float n_all = (float)t.S * (float)t.cpg;
   for (int g = warp; g < t.nb; g += NT / 32) {
-    const float2* d = p.part + (int64_t)img * p.tiles * t.G + cb * t.nb + g;
+    const float2* d = p.part + ((int64_t)img * t.G + cb * t.nb + g) * p.tiles;
     float mean = 0.0f, m2 = 0.0f;
 #pragma unroll 4
     for (int k = lane; k < p.tiles; k += 32)
-      mean = fmaf(d[(int64_t)k * t.G].x, k == p.tiles - 1 ? n_last : n_tile, mean);
+      mean = fmaf(d[k].x, k == p.tiles - 1 ? n_last : n_tile, mean);
     mean = warp_sum(mean) / n_all;
 #pragma unroll 4
     for (int k = lane; k < p.tiles; k += 32) {
-      const float2 v = d[(int64_t)k * t.G];
+      const float2 v = d[k];
       const float e = v.x - mean;
       m2 += fmaf(e * e, k == p.tiles - 1 ? n_last : n_tile, v.y);
     }

@@ -7,6 +7,8 @@ independent).  Between the two products of a row, h (or u) is fp32; the tensor-c
 form multiplies it as a sum of bf16 parts, off by at most 2^-17 of itself for bf16
 outputs and 2^-24 for fp32 outputs.  The output's rounding: eps / 2 relative.
 """
+import types
+
 import pytest
 import torch
 
@@ -146,8 +148,7 @@ def test_gradients_match_differences():
     grads = pq.adapter_backward(dy, x, hidden, ad, bounds, idx)
 
     def f(x, a, b):
-        t = pq.Adapters(ad.a, ad.b, ad.scale)
-        t.a, t.b = a, b
+        t = types.SimpleNamespace(a=a, b=b, scale=ad.scale)
         return (forward64(zero, x, t, bounds, idx)[0][0] * dy.double()).sum()
 
     at = [x.double(), ad.a.double(), ad.b.double()]
