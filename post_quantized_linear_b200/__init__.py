@@ -555,7 +555,10 @@ def group_norm_act(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] =
     shape = x.shape
     B, S, C = shape
     if out is None:
-        out = x.new_empty(shape, dtype=out_dtype)
+        if (out_dtype is None or out_dtype is x.dtype) and x.is_contiguous():
+            out = torch.empty_like(x)
+        else:
+            out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
         ldy, ybs, dy = C, S * C, dev
     else:
         dy, ldy, ybs = _map(out, "out", shape)
@@ -631,7 +634,7 @@ def group_norm_act_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tens
         raise ValueError("stats must be the [B, groups, 2] tensor of the forward call")
     groups = stats.shape[1]
     if dx is None:
-        dx = x.new_empty(shape)
+        dx = torch.empty_like(x) if x.is_contiguous() else torch.empty(shape, dtype=x.dtype, device=x.device)
         d3, lddx, dxbs = dev, C, S * C
     else:
         d3, lddx, dxbs = _map(dx, "dx", shape)

@@ -52,6 +52,27 @@ __device__ __forceinline__ void dsmem_store_u32x4(uint32_t addr, const uint32_t 
 // async proxy's.
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
+__device__ __forceinline__ void store_u32x8(void* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    uint4* q = static_cast<uint4*>(p);
+    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+// Cuts 8 fp32 values into their nearest bf16 (packed into w) and the rest (left in v).
+__device__ __forceinline__ void split_bf16(float (&v)[8], uint32_t (&w)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+    v[2 * j] -= __uint_as_float(w[j] << 16);
+    v[2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+
 constexpr int kTileRows = 128;
 constexpr int kTileThreads = 320;          // TMA warp, MMA warp, eight epilogue warps
 constexpr int kTileEpiWarps = 8;
@@ -64,6 +85,10 @@ struct AdapterTileArgs {
   int32_t stages;      // ring slots
   int32_t slot_bytes;  // kTileX + the weight tile
   int32_t parts;       // bf16 parts that h is multiplied as
+  int32_t wide;        // y's rows take 32-byte stores
+  const float* hidden;         // backward: h of the forward pass [M, R], and
+  __nv_bfloat16* f_u;          // u and h as three bf16 parts side by side, [M][3][rank padded to 16],
+  __nv_bfloat16* f_h;          // the operands of the adapters' gradients
   long long wait_budget;
   int32_t starve;
 };
@@ -120,8 +145,8 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
   uint8_t* hbuf = smem + NS * args.slot_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(hbuf + adapter_h_bytes(RP, args.parts));
   uint64_t* full = bars;             // [4]
-  uint64_t* empty1 = full + 4;       // [4] slot free after a tile of the first product
-  uint64_t* empty3 = empty1 + 4;     // [4] slot free after a tile of the second
+  uint64_t* empty1 = full + 4;       // [4] slot free: its products are done
+  uint64_t* empty3 = empty1 + 4;     // [4] forward, second product: its tile of y is read
   uint64_t* d_full = empty3 + 4;     // [2]
   uint64_t* d_empty = d_full + 2;    // [2]
   uint64_t* h_full = d_empty + 2;
@@ -177,7 +202,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
       for (; i < nk + nt && ok; ++i) {
         const int s = i % NS, prev = i - NS;
         if (prev >= 0) {
-          if (prev < nk) {
+          if (BWD || prev < nk) {
             ok = wait1(smem_u32(empty1 + s), (prev / NS) & 1, abort_flag, budget);
           } else {
             const int first = nk + ((s - nk % NS) + NS) % NS;   // first tile of the second product in slot s
@@ -248,6 +273,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
                       id2, acc);
             acc = 1;
           }
+        if (BWD) umma_commit(smem_u32(empty1 + s));   // the slot held the weight tile alone
         umma_commit(smem_u32(d_full + b));
       }
       umma_commit(smem_u32(drain_bar));
@@ -315,25 +341,27 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
           const int u = u0 + et + 256 * k;
           if (u < u1) {
             const int hr = u / octs, col = (u % octs) * 8;
-            float o[8];
+            const int64_t gr = it.row + hr;
+            if (!BWD && p.h != nullptr && col < R) store_vec<8>(p.h, gr * R + col, false, v[k]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float scaled = v[k][j] * scale;
-              o[j] = BWD ? scaled : v[k][j];
-              v[k][j] = col < R ? scaled : 0.0f;   // the padding of the rank is an operand, too
-            }
-            if (p.h != nullptr && col < R)
-              store_vec<8>(p.h, (int64_t)(it.row + hr) * R + col, false, o);
+            for (int j = 0; j < 8; ++j) v[k][j] = col < R ? v[k][j] * scale : 0.0f;   // the padding is an operand, too
             const uint32_t d = smem_u32(hbuf) + (col >> 6) * kTileX + hr * 128 + ((((col & 63) >> 3) ^ (hr & 7)) << 4);
-            for (int part = 0; part < args.parts; ++part) {
+            for (int part = 0; part < (BWD ? 3 : args.parts); ++part) {
               uint32_t w[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                w[j] = pack_bf16(v[k][2 * j], v[k][2 * j + 1]);
-                v[k][2 * j] -= __uint_as_float(w[j] << 16);
-                v[k][2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+              split_bf16(v[k], w);
+              if (part < args.parts)
+                for (int q = 0; q < cs; ++q) dsmem_store_u32x4(mapa_shared(d + part * rt * kTileX, q), w);
+              if (BWD)
+                *reinterpret_cast<uint4*>(args.f_u + (gr * 3 + part) * RP + col) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (BWD && col < R) {
+              float hv[8];
+              load8(args.hidden + gr * R + col, hv);
+              for (int part = 0; part < 3; ++part) {
+                uint32_t w[4];
+                split_bf16(hv, w);
+                *reinterpret_cast<uint4*>(args.f_h + (gr * 3 + part) * RP + col) = make_uint4(w[0], w[1], w[2], w[3]);
               }
-              for (int q = 0; q < cs; ++q) dsmem_store_u32x4(mapa_shared(d + part * rt * kTileX, q), w);
             }
           }
         }
@@ -342,57 +370,62 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
         if (lane < cs) mbar_arrive_remote(mapa_shared(smem_u32(h_ready), lane));
       }
     }
+    // a thread: 64 bytes of its row of every tile, y from shared memory, out in 32-byte
+    // sectors straight from registers
     const int rows = min(32, it.n - quad * 32);     // rows of the piece in this quarter (may be < 1)
+    YT* out = static_cast<YT*>(p.y) + (int64_t)(it.row + row) * p.ldy;
     for (int j = 0; j < nt && ok; ++j) {
       const int i = nk + j, s = i % NS, b = j & 1;
+      if (!BWD && !(ok = wait_warp(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
       if (!(ok = wait_warp(smem_u32(d_full + b), (j >> 1) & 1, abort_flag, budget))) break;
-      if (!(ok = wait_warp(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
       tc_fence_after();
       if (rows > 0) {
-        uint8_t* tile = smem + s * args.slot_bytes + quad * 4096;
-        uint8_t* mine = tile + lane * 128;
+        const uint32_t mine = smem_u32(smem + s * args.slot_bytes) + row * 128;
+        const uint32_t acc = t_lane + D2 + b * BN + half * (BN / 2);
+        uint32_t u[BN / 2];
 #pragma unroll
-        for (int g = 0; g < BN / 2; g += 16) {
-          uint32_t u[16];
-          tmem_ld16(t_lane + D2 + b * BN + half * (BN / 2) + g, u);
-          tmem_wait_ld();
+        for (int g = 0; g < BN / 2; g += 16) tmem_ld16(acc + g, *reinterpret_cast<uint32_t(*)[16]>(u + g));
+        uint4 y[4];
+        if constexpr (!BWD) {
 #pragma unroll
-          for (int q = 0; q < 16 * ES / 16; ++q) {   // 16-byte chunks
-            uint4* at = reinterpret_cast<uint4*>(mine + (((half * 4 + g * ES / 16 + q) ^ (lane & 7)) << 4));
-            constexpr int PER = 16 / ES;
-            float o[PER];
-            if constexpr (!BWD) {
-              Vec<YT>::load_raw(*at, o);
-            } else {
-#pragma unroll
-              for (int k = 0; k < PER; ++k) o[k] = 0.0f;
-            }
-#pragma unroll
-            for (int k = 0; k < PER; ++k) o[k] += __uint_as_float(u[q * PER + k]);
-            store_vec<PER>(at, 0, ES == 2, o);
-          }
+          for (int q = 0; q < 4; ++q) y[q] = lds128(mine + (((half * 4 + q) ^ (lane & 7)) << 4));
         }
+        tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(d_empty + b));
-        // out in rows of 64 bytes: four lanes per row
-        const int c = (t0 + j) * BN + half * (BN / 2) + (lane & 3) * (16 / ES);
-        if (c < E) {
+        if (lane == 0) {
+          mbar_arrive(smem_u32(d_empty + b));
+          if (!BWD) mbar_arrive(smem_u32(empty3 + s));
+        }
+        const int c = (t0 + j) * BN + half * (BN / 2);
+        uint32_t w[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {                // 16-byte chunks
+          constexpr int PER = 16 / ES;
+          float o[PER];
+          if constexpr (!BWD) {
+            Vec<YT>::load_raw(y[q], o);
+          } else {
+#pragma unroll
+            for (int k = 0; k < PER; ++k) o[k] = 0.0f;
+          }
+#pragma unroll
+          for (int k = 0; k < PER; ++k) o[k] += __uint_as_float(u[q * PER + k]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int r = k * 8 + (lane >> 2);
-            if (r < rows) {
-              const uint4 o = *reinterpret_cast<const uint4*>(tile + r * 128 + (((half * 4 + (lane & 3)) ^ (r & 7)) << 4));
-              *reinterpret_cast<uint4*>(static_cast<YT*>(p.y) + (int64_t)(it.row + quad * 32 + r) * p.ldy + c) = o;
-            }
+            if constexpr (ES == 2) w[4 * q + k] = pack_bf16(o[2 * k], o[2 * k + 1]);
+            else w[4 * q + k] = __float_as_uint(o[k]);
           }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
+        if (lane < rows) {
+          // the columns come in multiples of 16
+          if (c < E) store_u32x8(out + c, *reinterpret_cast<const uint32_t(*)[8]>(w), args.wide != 0);
+          if (c + 32 / ES < E) store_u32x8(out + c + 32 / ES, *reinterpret_cast<const uint32_t(*)[8]>(w + 8), args.wide != 0);
+        }
       } else if (lane == 0) {
         mbar_arrive(smem_u32(d_empty + b));
+        if (!BWD) mbar_arrive(smem_u32(empty3 + s));
       }
-      if (lane == 0) mbar_arrive(smem_u32(empty3 + s));
     }
   }
   tc_fence_before();
@@ -409,26 +442,31 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
 // the rank per cluster and adapter, contracted over the rows of all its requests
 // in pieces of 64, which the CTAs of the cluster take in turn; their sums are
 // added through distributed shared memory in rank order.
-// f (u or h, fp32) enters as three bf16 parts side by side along the rank axis
-// (exact to 2^-24, since the sums are fp32 results), g (x or dy) as it is.
+// f (u or h) comes as three bf16 parts side by side along the rank axis (exact to
+// 2^-24, since the sums are fp32 results), g (x or dy) as it is; both operands are
+// MN-major, so TMA brings them as they lie in memory.
+// The tensor core cuts its fp32 sums towards zero at every step, a bias that grows
+// with the chain (1.4e-6 of the sum after 16 pieces, where fp32 additions have 5e-7):
+// after kGradChain pieces the sums move to registers and are added there.
 struct AdapterGradTileArgs {
-  const float* f[2];             // u, hidden: [M, R]
   float* out[2];                 // da, db
   const float* scale;            // of the second, or null
   const int32_t* bounds;
   const int32_t* index;
   int32_t C[2];                  // K, N
-  int32_t tiles0;                // tiles of the first product (0: none)
+  int32_t tiles0;                // tiles of the first
   int32_t M, R, L, Q;
   int32_t cs, stages;
   long long wait_budget;
   int32_t starve;
 };
-__host__ __device__ inline int adapter_grad_f_bytes(int rp) { return (3 * rp + 63) / 64 * 8192; }
+constexpr int kGradChain = 8;
+__host__ __device__ inline int adapter_grad_atoms(int rp) { return (3 * rp + 63) / 64; }   // 64 ranks wide
 
 template <int RB>
 __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
     adapter_grad_tile_kernel(const __grid_constant__ CUtensorMap tg0, const __grid_constant__ CUtensorMap tg1,
+                             const __grid_constant__ CUtensorMap tf0, const __grid_constant__ CUtensorMap tf1,
                              const __grid_constant__ AdapterGradTileArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -439,25 +477,31 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
   const int which = tile < p.tiles0 ? 0 : 1;
   if (which) tile -= p.tiles0;
   const int C = p.C[which], c0 = tile * 128;
-  const float* f = p.f[which];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slot_bytes = kTileX + adapter_grad_f_bytes(RP);
+  const int atoms = adapter_grad_atoms(RP), slot_bytes = kTileX + atoms * 8192;
+  const int cols = 3 * RP, buf = (cols + 31) & ~31, NB = 2 * buf <= TM ? 2 : 1;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + max(NS * slot_bytes, cs > 1 ? 128 * RP * 4 : 0));
-  uint64_t* full = bars;           // [4] g has landed
-  uint64_t* ready = full + 4;      // [4] f's parts are written (and g's rows behind the piece cleared)
-  uint64_t* empty = ready + 4;     // [4]
-  uint64_t* d_full = empty + 4;
-  uint64_t* p_full = d_full + 1;
+  uint64_t* full = bars;           // [4] f and g have landed
+  uint64_t* empty = full + 4;      // [4]
+  uint64_t* d_full = empty + 4;    // [2] a chain's sums are complete
+  uint64_t* d_empty = d_full + 2;  // [2] and read
+  uint64_t* brief = d_empty + 2;   // a short piece has landed: the rows behind it are to be cleared
+  uint64_t* ready = brief + 1;     // and they are
+  uint64_t* p_full = ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(p_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const long long budget = p.wait_budget;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(smem_u32(full + i), 1);
-      mbar_init(smem_u32(ready + i), kTileEpiWarps);
       mbar_init(smem_u32(empty + i), 1);
     }
-    mbar_init(smem_u32(d_full), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(d_full + i), 1);
+      mbar_init(smem_u32(d_empty + i), kTileEpiWarps);
+    }
+    mbar_init(smem_u32(brief), 1);
+    mbar_init(smem_u32(ready), kTileEpiWarps);
     mbar_init(smem_u32(p_full), kTileEpiWarps * cs);
     *abort_flag = 0;
     fence_mbar_init();
@@ -478,16 +522,21 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
   if (warp == 0) {
     // -------------------------------------------------------- TMA producer
     const CUtensorMap* tg = which ? &tg1 : &tg0;
-    if (lane == 0) tma_prefetch_desc(tg);
+    const CUtensorMap* tf = which ? &tf1 : &tf0;
+    if (lane == 0) {
+      tma_prefetch_desc(tg);
+      tma_prefetch_desc(tf);
+    }
     ok = p.starve == 0;
     while (ok && pieces.mine(m0, n)) {
       const int s = i % NS;
       if (i >= NS && !(ok = wait_warp(smem_u32(empty + s), (i / NS - 1) & 1, abort_flag, budget))) break;
       if (lane == 0) {
         const uint32_t st = smem_u32(smem + s * slot_bytes), bar = smem_u32(full + s);
-        mbar_arrive_expect_tx(bar, kTileX);
+        mbar_arrive_expect_tx(bar, slot_bytes);
         tma_load_2d(st, tg, bar, c0, m0);
         tma_load_2d(st + 8192, tg, bar, c0 + 64, m0);
+        for (int a = 0; a < atoms; ++a) tma_load_2d(st + kTileX + a * 8192, tf, bar, a * 64, m0);
       }
       ++i;
     }
@@ -495,115 +544,94 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    const int cols = 3 * RP, n1 = cols > 256 ? 192 : cols, n2 = cols - n1;
-    while (ok && pieces.mine(m0, n)) {
-      const int s = i % NS;
+    const int n1 = cols > 256 ? 192 : cols, n2 = cols - n1;
+    int chain = 0, shorts = 0;
+    bool more = pieces.mine(m0, n);
+    while (more) {
+      const int s = i % NS, b = chain % NB;
+      const bool first = i % kGradChain == 0;
+      if (first && chain >= NB &&
+          !(ok = wait_warp(smem_u32(d_empty + b), (chain / NB - 1) & 1, abort_flag, budget)))
+        break;
       if (!(ok = wait_warp(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
-      if (!(ok = wait_warp(smem_u32(ready + s), (i / NS) & 1, abort_flag, budget))) break;
+      if (n < kGradPiece) {
+        if (lane == 0) mbar_arrive(smem_u32(brief));
+        if (!(ok = wait_warp(smem_u32(ready), shorts & 1, abort_flag, budget))) break;
+        ++shorts;
+      }
       tc_fence_after();
+      more = pieces.mine(m0, n);
       if (lane == 0) {
-        const uint32_t st = smem_u32(smem + s * slot_bytes), ft = st + kTileX;
+        const uint32_t st = smem_u32(smem + s * slot_bytes), ft = st + kTileX, d = tmem + b * buf;
 #pragma unroll
         for (int ks = 0; ks < kGradPiece / 16; ++ks) {
           const uint64_t a = smem_desc_mn_sw128(st + ks * 2048, 8192);
-          umma_bf16(tmem, a, smem_desc_mn_sw128(ft + ks * 2048, 8192), idesc_bf16(128, n1) | kIdescAMn | kIdescBMn,
-                    (i > 0 || ks > 0) ? 1u : 0u);
+          const uint32_t acc = !first || ks > 0 ? 1u : 0u;
+          umma_bf16(d, a, smem_desc_mn_sw128(ft + ks * 2048, 8192), idesc_bf16(128, n1) | kIdescAMn | kIdescBMn, acc);
           if (n2 > 0)
-            umma_bf16(tmem + n1, a, smem_desc_mn_sw128(ft + 3 * 8192 + ks * 2048, 8192),
-                      idesc_bf16(128, n2) | kIdescAMn | kIdescBMn, (i > 0 || ks > 0) ? 1u : 0u);
+            umma_bf16(d + n1, a, smem_desc_mn_sw128(ft + 3 * 8192 + ks * 2048, 8192),
+                      idesc_bf16(128, n2) | kIdescAMn | kIdescBMn, acc);
         }
         umma_commit(smem_u32(empty + s));
+        if (!more || (i + 1) % kGradChain == 0) umma_commit(smem_u32(d_full + b));
       }
       __syncwarp();
       ++i;
+      if (i % kGradChain == 0) ++chain;
     }
-    if (lane == 0) {
-      umma_commit(smem_u32(d_full));
-      wait_drain(smem_u32(d_full), 0, kDrainBudget);
-    }
+    if (lane == 0 && i > 0)        // every product has landed when the last commit has
+      wait_drain(smem_u32(empty + (i - 1) % NS), ((i - 1) / NS) & 1, kDrainBudget);
     __syncwarp();
   } else {
-    // ------------------------------- f's parts into shared memory, then the sums
+    // ----------------------- short pieces cleared, the chains' sums added up
     const int tid = threadIdx.x - 64;
-    const int vecs = R / 8, units = kGradPiece * vecs;     // 8 ranks of one row each
-    constexpr int MAXU = kGradPiece * (RB / 8) / 256;      // units per thread
-    float v[MAXU][8];
-    auto fetch = [&](int m, int cnt) {
-#pragma unroll
-      for (int k = 0; k < MAXU; ++k) {
-        const int u = tid + 256 * k, r = u / vecs, c = u % vecs;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
-        if (u < units && r < cnt) {
-          const float4* src = reinterpret_cast<const float4*>(f + (int64_t)(m + r) * R + c * 8);
-          const float4 a = __ldg(src), b = __ldg(src + 1);
-          v[k][0] = a.x; v[k][1] = a.y; v[k][2] = a.z; v[k][3] = a.w;
-          v[k][4] = b.x; v[k][5] = b.y; v[k][6] = b.z; v[k][7] = b.w;
-        }
-      }
-    };
-    bool more = pieces.mine(m0, n);
-    if (more) fetch(m0, n);
-    while (more) {
-      const int s = i % NS, cnt = n;
-      if (i >= NS && !(ok = wait_warp(smem_u32(empty + s), (i / NS - 1) & 1, abort_flag, budget))) break;
-      uint8_t* st = smem + s * slot_bytes;
-      uint8_t* ft = st + kTileX;
-#pragma unroll
-      for (int k = 0; k < MAXU; ++k) {
-        const int u = tid + 256 * k, r = u / vecs, c = u % vecs;
-        if (u < units) {
-#pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              w[j] = pack_bf16(v[k][2 * j], v[k][2 * j + 1]);
-              v[k][2 * j] -= __uint_as_float(w[j] << 16);
-              v[k][2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
-            }
-            const int col = part * RP + c * 8;
-            *reinterpret_cast<uint4*>(ft + (col >> 6) * 8192 + r * 128 + ((((col & 63) >> 3) ^ (r & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      }
-      more = pieces.mine(m0, n);
-      if (more) fetch(m0, n);                              // in flight while this piece is handed over
-      if (cnt < kGradPiece) {
-        // rows behind the piece belong to other requests: cleared, whatever they hold
-        if (!(ok = wait_warp(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
-        for (int u = tid; u < (kGradPiece - cnt) * 16; u += 256)
-          *reinterpret_cast<uint4*>(st + (u >> 3 & 1) * 8192 + (cnt + (u >> 4)) * 128 + (u & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(ready + s));
-      ++i;
-    }
-    const int any = i;                                     // this CTA had pieces
-    if (ok) ok = wait_warp(smem_u32(d_full), 0, abort_flag, budget);
     const int quad = warp & 3, half = (warp - 2) >> 2, row = quad * 32 + lane;
     const int hc = RP / 2, r0 = half * hc;
     const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
     float t[RB / 2];
-    if (ok) {
-      tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < RB / 2; c += 8) {
-        uint32_t a[8], b[8], d[8];
-        if (c < hc) {
-          tmem_ld8(t_lane + r0 + c, a);
-          tmem_ld8(t_lane + RP + r0 + c, b);
-          tmem_ld8(t_lane + 2 * RP + r0 + c, d);
-        }
-        tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          t[c + k] = c < hc && any ? __uint_as_float(a[k]) + (__uint_as_float(b[k]) + __uint_as_float(d[k])) : 0.0f;
+    for (int c = 0; c < RB / 2; ++c) t[c] = 0.0f;
+    int chain = 0, shorts = 0;
+    bool more = pieces.mine(m0, n);
+    while (more) {
+      const int s = i % NS, cnt = n;
+      if (cnt < kGradPiece) {
+        // rows behind the piece belong to other requests: cleared, whatever they hold
+        if (!(ok = wait_warp(smem_u32(brief), shorts & 1, abort_flag, budget))) break;
+        ++shorts;
+        uint8_t* st = smem + s * slot_bytes;
+        const int per = 8 * (2 + atoms);               // 16-byte words of a row
+        for (int u = tid; u < (kGradPiece - cnt) * per; u += 256)
+          *reinterpret_cast<uint4*>(st + (u % per >> 3) * 8192 + (cnt + u / per) * 128 + (u & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(ready));
       }
-      tc_fence_before();
+      more = pieces.mine(m0, n);
+      ++i;
+      if (!more || i % kGradChain == 0) {
+        const int b = chain % NB;
+        if (!(ok = wait_warp(smem_u32(d_full + b), (chain / NB) & 1, abort_flag, budget))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < RB / 2; c += 8) {
+          if (c < hc) {
+            uint32_t a[8], bb[8], d[8];
+            tmem_ld8(t_lane + b * buf + r0 + c, a);
+            tmem_ld8(t_lane + b * buf + RP + r0 + c, bb);
+            tmem_ld8(t_lane + b * buf + 2 * RP + r0 + c, d);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              t[c + k] += __uint_as_float(a[k]) + (__uint_as_float(bb[k]) + __uint_as_float(d[k]));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(d_empty + b));
+        ++chain;
+      }
     }
     const bool mine = cs == 1 || (quad * 2 + half) % cs == rank;
     if (cs > 1) {

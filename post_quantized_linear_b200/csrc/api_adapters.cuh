@@ -136,14 +136,14 @@ int resident_clusters(int cs, int threads, int smem) {
 }
 
 template <int RB, typename YT, bool BWD>
-sq_status launch_tile_rb(const sq::AdapterArgs& a, const CUtensorMap& tx, const CUtensorMap& tw1,
+sq_status launch_tile_rb(sq::AdapterTileArgs t, const CUtensorMap& tx, const CUtensorMap& tw1,
                          const CUtensorMap& tw2, const CUtensorMap& ty, cudaStream_t s) {
   constexpr auto kern = sq::adapter_tile_kernel<RB, YT, BWD>;
+  const sq::AdapterArgs& a = t.p;
   const int D = BWD ? a.N : a.K, E = BWD ? a.K : a.N;
   const int rp = (a.R + 15) / 16 * 16;
-  sq::AdapterTileArgs t = {};
-  t.p = a;
   t.parts = sizeof(YT) == 2 ? 2 : 3;
+  t.wide = reinterpret_cast<uintptr_t>(a.y) % 32 == 0 && a.ldy * (int64_t)sizeof(YT) % 32 == 0;
   t.slot_bytes = sq::kTileX + (RB == 64 ? 8192 : 16384);
   t.wait_budget = g_wait_budget;
   t.starve = g_debug_starve;
@@ -178,7 +178,8 @@ sq_status launch_tile_rb(const sq::AdapterArgs& a, const CUtensorMap& tx, const 
 }
 
 template <bool BWD>
-sq_status launch_tile(const sq::AdapterArgs& a, sq_dtype yt, cudaStream_t s) {
+sq_status launch_tile(const sq::AdapterTileArgs& t, sq_dtype yt, cudaStream_t s) {
+  const sq::AdapterArgs& a = t.p;
   const uint64_t K = a.K, N = a.N, R = a.R, L = a.L, M = a.M;
   const uint32_t rp = (uint32_t)((R + 15) / 16 * 16), bn = yt == SQ_BF16 ? 64 : 32;
   CUtensorMap tx, tw1, tw2, ty;
@@ -193,11 +194,14 @@ sq_status launch_tile(const sq::AdapterArgs& a, sq_dtype yt, cudaStream_t s) {
     if ((st = make_adapter_map(&tw2, SQ_BF16, a.b, 3, R, N, L, R * 2, N * R * 2, 64, bn)) != SQ_OK) return st;
     if ((st = make_adapter_map(&ty, yt, a.y, 2, N, M, 1, a.ldy * elt_size(yt), 0, bn, 32)) != SQ_OK) return st;
   }
+  if constexpr (BWD)
+    return R <= 64 ? launch_tile_rb<64, __nv_bfloat16, true>(t, tx, tw1, tw2, ty, s)
+                   : launch_tile_rb<128, __nv_bfloat16, true>(t, tx, tw1, tw2, ty, s);
   if (R <= 64)
-    return yt == SQ_BF16 ? launch_tile_rb<64, __nv_bfloat16, BWD>(a, tx, tw1, tw2, ty, s)
-                         : launch_tile_rb<64, float, BWD>(a, tx, tw1, tw2, ty, s);
-  return yt == SQ_BF16 ? launch_tile_rb<128, __nv_bfloat16, BWD>(a, tx, tw1, tw2, ty, s)
-                       : launch_tile_rb<128, float, BWD>(a, tx, tw1, tw2, ty, s);
+    return yt == SQ_BF16 ? launch_tile_rb<64, __nv_bfloat16, false>(t, tx, tw1, tw2, ty, s)
+                         : launch_tile_rb<64, float, false>(t, tx, tw1, tw2, ty, s);
+  return yt == SQ_BF16 ? launch_tile_rb<128, __nv_bfloat16, false>(t, tx, tw1, tw2, ty, s)
+                       : launch_tile_rb<128, float, false>(t, tx, tw1, tw2, ty, s);
 }
 
 // The first product in bf16 tiles of 128 rows pays where requests have rows to fill
@@ -207,18 +211,17 @@ bool use_tiles(const sq::AdapterArgs& a, sq_dtype xt) {
 }
 
 template <int RB>
-sq_status launch_grad_tile_rb(sq::AdapterGradTileArgs g, const CUtensorMap& t0, const CUtensorMap& t1, int tiles,
-                              cudaStream_t s) {
+sq_status launch_grad_tile_rb(sq::AdapterGradTileArgs g, const CUtensorMap (&t)[4], int tiles, cudaStream_t s) {
   constexpr auto kern = sq::adapter_grad_tile_kernel<RB>;
   const int rp = (g.R + 15) / 16 * 16;
-  const int slot = sq::kTileX + sq::adapter_grad_f_bytes(rp);
+  const int slot = sq::kTileX + sq::adapter_grad_atoms(rp) * 8192;
   const int room = (RB == 64 ? kSmemPerSm / 2 - 1024 : kSmemPerSm) - sq::kTileBars - 1024;
   g.stages = std::min(4, room / slot);
-  // the cluster shares an adapter's pieces: as many CTAs as fill the SMs twice
+  // the cluster shares an adapter's pieces: as many CTAs as are resident at once
   const int64_t per = std::max<int64_t>(1, (int64_t)g.M / sq::kGradPiece / std::max(1, std::min(g.L, g.Q)));
-  const int64_t ctas = (int64_t)tiles * std::min(g.L, std::max(g.Q, 1));
+  const int64_t ctas = (int64_t)tiles * std::max(1, std::min(g.L, g.Q));
   int cs = 1;
-  while (cs < 8 && cs * 2 <= per && ctas * cs * 2 <= (int64_t)num_sms() * (RB == 64 ? 4 : 2)) cs *= 2;
+  while (cs < 8 && cs < per && ctas * (cs + 1) <= (int64_t)num_sms() * (RB == 64 ? 2 : 1)) ++cs;
   g.cs = cs;
   // At least the share of shared memory that the CTA has of TMEM (half, or all): a CTA
   // that is resident never waits for TMEM of another cluster's.
@@ -238,33 +241,35 @@ sq_status launch_grad_tile_rb(sq::AdapterGradTileArgs g, const CUtensorMap& t0, 
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, kern, t0, t1, g));
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, t[0], t[1], t[2], t[3], g));
 }
 
-// Both gradients (or the bf16 one of them) on the tensor cores.
-sq_status launch_grad_tiles(const sq::AdapterArgs& a, const float* u, const float* hidden, const void* x,
-                            int64_t ldx, const void* dy, int64_t lddy, float* da, float* db, cudaStream_t s) {
-  CUtensorMap t0, t1;
+// Both gradients on the tensor cores, from the parts of u and h that launch_tile<true> wrote.
+sq_status launch_grad_tiles(const sq::AdapterTileArgs& t, const void* x, int64_t ldx, const void* dy, int64_t lddy,
+                            float* da, float* db, cudaStream_t s) {
+  const sq::AdapterArgs& a = t.p;
+  const uint64_t cols = 3 * (uint64_t)((a.R + 15) / 16 * 16);
+  CUtensorMap maps[4];
   sq_status st;
-  if (da != nullptr &&
-      (st = make_adapter_map(&t0, SQ_BF16, x, 2, a.K, a.M, 1, ldx * 2, 0, 64, sq::kGradPiece)) != SQ_OK)
-    return st;
-  if (db != nullptr &&
-      (st = make_adapter_map(&t1, SQ_BF16, dy, 2, a.N, a.M, 1, lddy * 2, 0, 64, sq::kGradPiece)) != SQ_OK)
-    return st;
-  if (da == nullptr) t0 = t1;
-  if (db == nullptr) t1 = t0;
+  if ((st = make_adapter_map(&maps[0], SQ_BF16, x, 2, a.K, a.M, 1, ldx * 2, 0, 64, sq::kGradPiece)) != SQ_OK) return st;
+  if ((st = make_adapter_map(&maps[1], SQ_BF16, dy, 2, a.N, a.M, 1, lddy * 2, 0, 64, sq::kGradPiece)) != SQ_OK) return st;
+  if ((st = make_adapter_map(&maps[2], SQ_BF16, t.f_u, 2, cols, a.M, 1, cols * 2, 0, 64, sq::kGradPiece)) != SQ_OK) return st;
+  if ((st = make_adapter_map(&maps[3], SQ_BF16, t.f_h, 2, cols, a.M, 1, cols * 2, 0, 64, sq::kGradPiece)) != SQ_OK) return st;
   sq::AdapterGradTileArgs g = {};
-  g.f[0] = u; g.f[1] = hidden;
   g.out[0] = da; g.out[1] = db;
   g.scale = a.scale; g.bounds = a.bounds; g.index = a.index;
   g.C[0] = a.K; g.C[1] = a.N;
-  g.tiles0 = da != nullptr ? (a.K + 127) / 128 : 0;
+  g.tiles0 = (a.K + 127) / 128;
   g.M = a.M; g.R = a.R; g.L = a.L; g.Q = a.Q;
   g.wait_budget = g_wait_budget;
   g.starve = g_debug_starve;
-  const int tiles = g.tiles0 + (db != nullptr ? (a.N + 127) / 128 : 0);
-  return a.R <= 64 ? launch_grad_tile_rb<64>(g, t0, t1, tiles, s) : launch_grad_tile_rb<128>(g, t0, t1, tiles, s);
+  const int tiles = g.tiles0 + (a.N + 127) / 128;
+  return a.R <= 64 ? launch_grad_tile_rb<64>(g, maps, tiles, s) : launch_grad_tile_rb<128>(g, maps, tiles, s);
+}
+
+// Bytes of a backward call's workspace: u in fp32, or u and h as three bf16 parts.
+size_t adapter_bwd_bytes(int64_t M, int32_t R) {
+  return (size_t)M * (size_t)((R + 15) / 16 * 16) * 3 * sizeof(__nv_bfloat16) * 2;
 }
 
 }  // namespace
@@ -284,12 +289,15 @@ sq_status sq_adapter_add(const void* x, sq_dtype xt, int64_t M, int64_t ldx, con
   sq::AdapterArgs a = adapter_args(adapters, bounds, index, requests, M);
   a.x = x; a.ldx = ldx; a.y = y; a.ldy = ldy; a.h = hidden;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return use_tiles(a, xt) ? launch_tile<false>(a, yt, s) : launch_few_rows<false>(a, xt, yt, s);
+  if (!use_tiles(a, xt)) return launch_few_rows<false>(a, xt, yt, s);
+  sq::AdapterTileArgs t = {};
+  t.p = a;
+  return launch_tile<false>(t, yt, s);
 }
 
 sq_status sq_adapter_backward_workspace_size(int64_t M, int32_t R, size_t* bytes) {
   if (bytes == nullptr || M < 0 || R <= 0) return SQ_ERR_INVALID_ARG;
-  *bytes = sizeof(float) * (size_t)M * (size_t)R;
+  *bytes = adapter_bwd_bytes(M, R);
   return SQ_OK;
 }
 
@@ -303,36 +311,33 @@ sq_status sq_adapter_backward(const void* dy, sq_dtype dyt, int64_t M, int64_t l
   if (!aligned16(da) || !aligned16(db)) return SQ_ERR_ALIGNMENT;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   sq::AdapterArgs a = adapter_args(adapters, bounds, index, requests, M);
-  float* u = static_cast<float*>(workspace);
   if (M > 0) {
     if ((st = check_matrix(dy, dyt, adapters->N, lddy)) != SQ_OK) return st;
     if ((st = check_matrix(x, xt, adapters->K, ldx)) != SQ_OK) return st;
     if ((st = check_matrix(dx, xt, adapters->K, lddx)) != SQ_OK) return st;
-    if (hidden == nullptr || workspace == nullptr || workspace_bytes < sizeof(float) * (size_t)M * adapters->R)
+    if (hidden == nullptr || workspace == nullptr || workspace_bytes < adapter_bwd_bytes(M, adapters->R))
       return SQ_ERR_INVALID_ARG;
     if (!aligned16(hidden) || !aligned16(workspace)) return SQ_ERR_ALIGNMENT;
-    a.x = dy; a.ldx = lddy; a.y = dx; a.ldy = lddx; a.h = u;
-    st = use_tiles(a, dyt) ? launch_tile<true>(a, xt, s) : launch_few_rows<true>(a, dyt, xt, s);
-    if (st != SQ_OK) return st;
-  }
-  // bf16 rows by tensor cores (three exact parts of u and h), fp32 rows by the fp32 lanes
-  const bool ta = M > 0 && xt == SQ_BF16, tb = M > 0 && dyt == SQ_BF16;
-  if (ta || tb) {
-    st = launch_grad_tiles(a, u, hidden, x, ldx, dy, lddy, ta ? da : nullptr, tb ? db : nullptr, s);
-    if (st != SQ_OK) return st;
+    a.x = dy; a.ldx = lddy; a.y = dx; a.ldy = lddx;
+    if (use_tiles(a, dyt) && xt == SQ_BF16) {
+      sq::AdapterTileArgs t = {};
+      t.p = a;
+      t.hidden = hidden;
+      t.f_u = static_cast<__nv_bfloat16*>(workspace);
+      t.f_h = t.f_u + (size_t)M * (size_t)((a.R + 15) / 16 * 16) * 3;
+      if ((st = launch_tile<true>(t, xt, s)) != SQ_OK) return st;
+      return launch_grad_tiles(t, x, ldx, dy, lddy, da, db, s);
+    }
+    a.h = static_cast<float*>(workspace);
+    if ((st = launch_few_rows<true>(a, dyt, xt, s)) != SQ_OK) return st;
   }
   sq::AdapterGradArgs g = {};
   g.bounds = bounds; g.index = index; g.M = (int32_t)M; g.R = adapters->R; g.L = adapters->L;
   g.Q = M > 0 ? requests : 0;
-  if (!ta) {
-    g.f = u; g.g = x; g.ldg = ldx; g.C = (int32_t)adapters->K; g.out = da;
-    if ((st = launch_adapter_grad<false>(g, xt, s)) != SQ_OK) return st;
-  }
-  if (!tb) {
-    g.f = hidden; g.g = dy; g.ldg = lddy; g.C = (int32_t)adapters->N; g.out = db; g.scale = adapters->scale;
-    return launch_adapter_grad<true>(g, dyt, s);
-  }
-  return SQ_OK;
+  g.f = static_cast<const float*>(workspace); g.g = x; g.ldg = ldx; g.C = (int32_t)adapters->K; g.out = da;
+  if ((st = launch_adapter_grad<false>(g, xt, s)) != SQ_OK) return st;
+  g.f = hidden; g.g = dy; g.ldg = lddy; g.C = (int32_t)adapters->N; g.out = db; g.scale = adapters->scale;
+  return launch_adapter_grad<true>(g, dyt, s);
 }
 
 }  // extern "C"

@@ -24,7 +24,7 @@ int norm_cluster_smem(const sq::NormTile& t, int nv, int vn, int tensors) {
 }
 
 // Chooses the tiles of `tensors` read (1 forward: x; 2 backward: x and dy).
-sq_status norm_plan(int64_t B, int64_t S, int64_t C, int32_t groups, int es, int tensors, NormPlan* out) {
+sq_status norm_plan_for(int64_t B, int64_t S, int64_t C, int32_t groups, int es, int tensors, NormPlan* out) {
   const int vn = 16 / es;
   const int cpg = (int)(C / groups);
   const int unit = vn / gcd_i(vn, cpg);                 // groups in whole vectors
@@ -98,6 +98,23 @@ sq_status norm_plan(int64_t B, int64_t S, int64_t C, int32_t groups, int es, int
   p.cs = 1;
   p.cluster = false;
   *out = p;
+  return SQ_OK;
+}
+
+// The thread's last plan serves a call of the same sizes (the choice costs as much host
+// time as an argument check of the whole call).
+sq_status norm_plan(int64_t B, int64_t S, int64_t C, int32_t groups, int es, int tensors, NormPlan* out) {
+  thread_local int64_t key[7] = {};
+  thread_local NormPlan last;
+  const int64_t k[7] = {B, S, C, groups, es, tensors, num_sms()};
+  if (std::memcmp(k, key, sizeof(k)) != 0) {
+    NormPlan p;
+    const sq_status st = norm_plan_for(B, S, C, groups, es, tensors, &p);
+    if (st != SQ_OK) return st;
+    last = p;
+    std::memcpy(key, k, sizeof(k));
+  }
+  *out = last;
   return SQ_OK;
 }
 
