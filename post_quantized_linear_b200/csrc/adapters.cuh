@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(kFewThreads, T == 1 ? 4 : 2)
   __shared__ __align__(16) float red[kFewThreads * 8];
   const int rank = blockIdx.x % cs;
   const int tid = threadIdx.x;
+  grid_dep_wait();
   if (blockIdx.x == 0) check_requests(p, kFewThreads);
   const AdapterItem it = adapter_item(p, blockIdx.x / cs, T);
   const int D = BWD ? p.N : p.K, E = BWD ? p.K : p.N, R = p.R;   // contracted, written
@@ -380,11 +381,7 @@ __global__ void __launch_bounds__(kFewThreads, T == 1 ? 4 : 2)
     const int m = i % T;
     float t = 0.0f;
     if (m < it.n) {
-      if (cs > 1) {
-        for (int k = 0; k < cs; ++k) t += dsmem_f32(part + i, k);
-      } else {
-        t = part[i];
-      }
+      t = cs > 1 ? dsmem_sum(part + i, cs) : part[i];
     }
     full[i] = t * scale;
     if (p.h != nullptr && rank == 0 && m < it.n)
@@ -494,6 +491,38 @@ struct AdapterGradArgs {
 };
 constexpr int kGradCols = 64, kGradRows = 32, kGradThreads = 256;
 
+__device__ __forceinline__ float4 dsmem_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+// Eight consecutive values at p summed over the cluster's CTAs in rank order, four
+// CTAs' reads in flight together.
+__device__ __forceinline__ void dsmem_sum8(const float* p, int cs, float (&v)[8]) {
+  const uint32_t at = smem_u32(p);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  for (int q = 0; q < cs; q += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[k] = b[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (q + k < cs) {
+        const uint32_t from = mapa_shared(at, q + k);
+        a[k] = dsmem_f32x4(from);
+        b[k] = dsmem_f32x4(from + 16);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[0] += a[k].x; v[1] += a[k].y; v[2] += a[k].z; v[3] += a[k].w;
+      v[4] += b[k].x; v[5] += b[k].y; v[6] += b[k].z; v[7] += b[k].w;
+    }
+  }
+}
+
 template <typename GT, bool TRANS>
 __global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const AdapterGradArgs p) {
   // rows of f and g, then the sums [rank][column]
@@ -509,6 +538,7 @@ __global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const Adapte
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+  grid_dep_wait();
   GradPieces pieces{p.bounds, p.index, p.M, p.Q, l, rank, p.cs};
   const int R4 = p.R / 4;
   int first, count;
@@ -566,16 +596,15 @@ __global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const Adapte
     const int r = ry + 32 * i;
     // the CTAs of the cluster write the ranks in turn
     if (r < p.R && (p.cs == 1 || r % p.cs == rank)) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = acc[i][j];
+      if (p.cs > 1) dsmem_sum8(sh + r * kGradCols + cx, p.cs, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int c = c0 + cx + j;
-        float v = acc[i][j];
-        if (p.cs > 1) {
-          v = 0.0f;
-          for (int k = 0; k < p.cs; ++k) v += dsmem_f32(sh + r * kGradCols + cx + j, k);
-        }
         if (c < p.C)
-          p.out[TRANS ? ((int64_t)l * p.C + c) * p.R + r : ((int64_t)l * p.R + r) * p.C + c] = v * scale;
+          p.out[TRANS ? ((int64_t)l * p.C + c) * p.R + r : ((int64_t)l * p.R + r) * p.C + c] = v[j] * scale;
       }
     }
   }

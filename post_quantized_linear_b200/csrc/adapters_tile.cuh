@@ -35,14 +35,6 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
 }
 constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;   // operand is MN-major
 
-__device__ __forceinline__ float4 dsmem_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));
-  return v;
-}
-
 __device__ __forceinline__ void dsmem_store_u32x4(uint32_t addr, const uint32_t (&w)[4]) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3])
@@ -62,6 +54,14 @@ __device__ __forceinline__ void store_u32x8(void* p, const uint32_t (&w)[8], boo
     q[0] = make_uint4(w[0], w[1], w[2], w[3]);
     q[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+               : "memory");
+}
+// The two epilogue warps of a TMEM lane quarter.
+__device__ __forceinline__ void quarter_sync(int quad) {
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
 }
 // Cuts 8 fp32 values into their nearest bf16 (packed into w) and the rest (left in v).
 __device__ __forceinline__ void split_bf16(float (&v)[8], uint32_t (&w)[4]) {
@@ -117,13 +117,15 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
                         const __grid_constant__ AdapterTileArgs args) {
   constexpr int ES = sizeof(YT);
   constexpr int BN = 128 / ES;             // columns of an output tile
-  constexpr int D2 = 128;                  // TMEM column of the output accumulators
+  constexpr int D2 = RB;                   // TMEM column of the output accumulators,
+  constexpr int ND = RB == 64 ? 3 : 2;     // and how many tiles of them there are room for
   const AdapterArgs& p = args.p;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int cs = args.cs, NS = args.stages;
   const int rank = blockIdx.x % cs;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_wait();
   if (blockIdx.x == 0) check_requests(p, kTileThreads);
   const AdapterItem it = adapter_item(p, blockIdx.x / cs, kTileRows);
   const int D = BWD ? p.N : p.K, E = BWD ? p.K : p.N, R = p.R;
@@ -147,9 +149,9 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
   uint64_t* full = bars;             // [4]
   uint64_t* empty1 = full + 4;       // [4] slot free: its products are done
   uint64_t* empty3 = empty1 + 4;     // [4] forward, second product: its tile of y is read
-  uint64_t* d_full = empty3 + 4;     // [2]
-  uint64_t* d_empty = d_full + 2;    // [2]
-  uint64_t* h_full = d_empty + 2;
+  uint64_t* d_full = empty3 + 4;     // [3]
+  uint64_t* d_empty = d_full + 3;    // [3]
+  uint64_t* h_full = d_empty + 3;
   uint64_t* h_ready = h_full + 1;
   uint64_t* p_full = h_ready + 1;    // every CTA's partial h is written
   uint64_t* p_free = p_full + 1;     // every CTA has read this one's
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
       mbar_init(smem_u32(empty1 + i), 1);
       mbar_init(smem_u32(empty3 + i), kTileEpiWarps);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < ND; ++i) {
       mbar_init(smem_u32(d_full + i), 1);
       mbar_init(smem_u32(d_empty + i), kTileEpiWarps);
     }
@@ -258,8 +260,8 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
       const uint32_t id2 = idesc_bf16(kTileRows, BN) | (BWD ? kIdescBMn : 0u);
       const uint32_t hb = smem_u32(hbuf);
       for (int j = 0; j < nt && ok; ++j) {
-        const int i = nk + j, s = i % NS, b = j & 1;
-        if (j >= 2 && !(ok = wait1(smem_u32(d_empty + b), ((j >> 1) - 1) & 1, abort_flag, budget))) break;
+        const int i = nk + j, s = i % NS, b = j % ND;
+        if (j >= ND && !(ok = wait1(smem_u32(d_empty + b), (j / ND - 1) & 1, abort_flag, budget))) break;
         if (!(ok = wait1(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
         tc_fence_after();
         const uint32_t wt = smem_u32(smem + s * args.slot_bytes) + kTileX;
@@ -321,13 +323,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
         if (u < u1) {
-          const uint32_t at = smem_u32(hbuf) + ((u / octs) * (RP + 4) + (u % octs) * 8) * 4;
-          for (int q = 0; q < cs; ++q) {
-            const uint32_t from = mapa_shared(at, q);
-            const float4 a = dsmem_f32x4(from), b = dsmem_f32x4(from + 16);
-            v[k][0] += a.x; v[k][1] += a.y; v[k][2] += a.z; v[k][3] += a.w;
-            v[k][4] += b.x; v[k][5] += b.y; v[k][6] += b.z; v[k][7] += b.w;
-          }
+          dsmem_sum8(reinterpret_cast<const float*>(hbuf) + (u / octs) * (RP + 4) + (u % octs) * 8, cs, v[k]);
         }
       }
       __syncwarp();
@@ -370,17 +366,23 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
         if (lane < cs) mbar_arrive_remote(mapa_shared(smem_u32(h_ready), lane));
       }
     }
-    // a thread: 64 bytes of its row of every tile, y from shared memory, out in 32-byte
-    // sectors straight from registers
+    // Output tiles; a thread has 64 bytes of its row.  Forward: they are added to y's, read
+    // from the ring (the slot goes back at once), and stored in whole 32-byte sectors: that
+    // costs the load/store unit a line per row, but held the ring's slots shorter than TMA
+    // stores from them (62 us instead of 67 on the ragged batch of 16384 x 2304 -> 3456).
+    // Backward: no ring to hold up; tiles are put together in the first product's room (the
+    // slots' x tiles), and a quarter's 32 rows go out in one TMA store where the piece has
+    // them all, else row by row (69 us instead of 73 for all gradients of 8192 x 4608 -> 1152).
     const int rows = min(32, it.n - quad * 32);     // rows of the piece in this quarter (may be < 1)
+    const bool issuer = half == 0 && lane == 0;     // of the quarter's stores
     YT* out = static_cast<YT*>(p.y) + (int64_t)(it.row + row) * p.ldy;
     for (int j = 0; j < nt && ok; ++j) {
-      const int i = nk + j, s = i % NS, b = j & 1;
+      const int i = nk + j, s = i % NS, b = j % ND;
       if (!BWD && !(ok = wait_warp(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
-      if (!(ok = wait_warp(smem_u32(d_full + b), (j >> 1) & 1, abort_flag, budget))) break;
+      if (!(ok = wait_warp(smem_u32(d_full + b), (j / ND) & 1, abort_flag, budget))) break;
       tc_fence_after();
       if (rows > 0) {
-        const uint32_t mine = smem_u32(smem + s * args.slot_bytes) + row * 128;
+        const uint32_t tile = smem_u32(smem + s * args.slot_bytes + quad * 4096), mine = tile + lane * 128;
         const uint32_t acc = t_lane + D2 + b * BN + half * (BN / 2);
         uint32_t u[BN / 2];
 #pragma unroll
@@ -389,6 +391,13 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
         if constexpr (!BWD) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) y[q] = lds128(mine + (((half * 4 + q) ^ (lane & 7)) << 4));
+        } else {
+          // this room's last store has been read (at most NS - 1 younger ones are under way)
+          if (issuer && j >= NS) {
+            if (NS == 3) bulk_wait_read<2>();
+            else bulk_wait_read<3>();
+          }
+          quarter_sync(quad);
         }
         tmem_wait_ld();
         tc_fence_before();
@@ -397,7 +406,6 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
           mbar_arrive(smem_u32(d_empty + b));
           if (!BWD) mbar_arrive(smem_u32(empty3 + s));
         }
-        const int c = (t0 + j) * BN + half * (BN / 2);
         uint32_t w[16];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {                // 16-byte chunks
@@ -417,16 +425,46 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
             else w[4 * q + k] = __float_as_uint(o[k]);
           }
         }
-        if (lane < rows) {
-          // the columns come in multiples of 16
-          if (c < E) store_u32x8(out + c, *reinterpret_cast<const uint32_t(*)[8]>(w), args.wide != 0);
-          if (c + 32 / ES < E) store_u32x8(out + c + 32 / ES, *reinterpret_cast<const uint32_t(*)[8]>(w + 8), args.wide != 0);
+        const int c0t = (t0 + j) * BN;
+        if constexpr (!BWD) {
+          const int c = c0t + half * (BN / 2);
+          if (lane < rows) {
+            // the columns come in multiples of 16
+            if (c < E) store_u32x8(out + c, *reinterpret_cast<const uint32_t(*)[8]>(w), args.wide != 0);
+            if (c + 32 / ES < E)
+              store_u32x8(out + c + 32 / ES, *reinterpret_cast<const uint32_t(*)[8]>(w + 8), args.wide != 0);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            sts128(mine + (((half * 4 + q) ^ (lane & 7)) << 4), *reinterpret_cast<const uint32_t(*)[4]>(w + 4 * q));
+          if (rows == 32) {
+            fence_proxy_async_smem();
+            quarter_sync(quad);
+            if (issuer) {
+              tma_store_2d(&ty, tile, c0t, it.row + quad * 32);
+              bulk_commit_group();
+            }
+          } else {
+            quarter_sync(quad);
+            const int c = c0t + half * (BN / 2) + (lane & 3) * (16 / ES);
+            if (c < E) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int r = k * 8 + (lane >> 2);
+                if (r < rows)
+                  *reinterpret_cast<uint4*>(static_cast<YT*>(p.y) + (int64_t)(it.row + quad * 32 + r) * p.ldy + c) =
+                      lds128(tile + r * 128 + (((half * 4 + (lane & 3)) ^ (r & 7)) << 4));
+              }
+            }
+          }
         }
       } else if (lane == 0) {
         mbar_arrive(smem_u32(d_empty + b));
         if (!BWD) mbar_arrive(smem_u32(empty3 + s));
       }
     }
+    if (BWD && issuer) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -516,6 +554,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  grid_dep_wait();
   GradPieces pieces{p.bounds, p.index, p.M, p.Q, l, rank, cs};
   int m0, n, i = 0;
   bool ok = true;

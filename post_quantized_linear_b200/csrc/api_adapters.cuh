@@ -55,11 +55,11 @@ sq_status launch_few_rows_t(const sq::AdapterArgs& a, sq_dtype xt, sq_dtype yt, 
   const dim3 grid((unsigned)(slots * cs));
   if (xt == SQ_BF16)
     return yt == SQ_BF16
-               ? launch_grid<sq::adapter_few_rows_kernel<T, __nv_bfloat16, __nv_bfloat16, BWD>>(grid, sq::kFewThreads, 0, cs, false, s, a, cs)
-               : launch_grid<sq::adapter_few_rows_kernel<T, __nv_bfloat16, float, BWD>>(grid, sq::kFewThreads, 0, cs, false, s, a, cs);
+               ? launch_grid<sq::adapter_few_rows_kernel<T, __nv_bfloat16, __nv_bfloat16, BWD>>(grid, sq::kFewThreads, 0, cs, true, s, a, cs)
+               : launch_grid<sq::adapter_few_rows_kernel<T, __nv_bfloat16, float, BWD>>(grid, sq::kFewThreads, 0, cs, true, s, a, cs);
   return yt == SQ_BF16
-             ? launch_grid<sq::adapter_few_rows_kernel<T, float, __nv_bfloat16, BWD>>(grid, sq::kFewThreads, 0, cs, false, s, a, cs)
-             : launch_grid<sq::adapter_few_rows_kernel<T, float, float, BWD>>(grid, sq::kFewThreads, 0, cs, false, s, a, cs);
+             ? launch_grid<sq::adapter_few_rows_kernel<T, float, __nv_bfloat16, BWD>>(grid, sq::kFewThreads, 0, cs, true, s, a, cs)
+             : launch_grid<sq::adapter_few_rows_kernel<T, float, float, BWD>>(grid, sq::kFewThreads, 0, cs, true, s, a, cs);
 }
 
 // Pieces of one row where requests have one on average, of eight elsewhere.
@@ -80,8 +80,8 @@ sq_status launch_adapter_grad(sq::AdapterGradArgs g, sq_dtype gt, cudaStream_t s
   g.cs = cs;
   const dim3 grid((unsigned)(tiles * cs), (unsigned)g.L);
   if (gt == SQ_BF16)
-    return launch_grid<sq::adapter_grad_kernel<__nv_bfloat16, TRANS>>(grid, sq::kGradThreads, 0, cs, false, s, g);
-  return launch_grid<sq::adapter_grad_kernel<float, TRANS>>(grid, sq::kGradThreads, 0, cs, false, s, g);
+    return launch_grid<sq::adapter_grad_kernel<__nv_bfloat16, TRANS>>(grid, sq::kGradThreads, 0, cs, true, s, g);
+  return launch_grid<sq::adapter_grad_kernel<float, TRANS>>(grid, sq::kGradThreads, 0, cs, true, s, g);
 }
 
 // A tiled map of rank 2 or 3, boxes with 128-byte swizzled rows; strides in bytes
@@ -167,13 +167,15 @@ sq_status launch_tile_rb(sq::AdapterTileArgs t, const CUtensorMap& tx, const CUt
   cfg.blockDim = dim3(sq::kTileThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cs;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cuda_status(cudaLaunchKernelEx(&cfg, kern, tx, tw1, tw2, ty, t));
 }
 
@@ -188,7 +190,7 @@ sq_status launch_tile(const sq::AdapterTileArgs& t, sq_dtype yt, cudaStream_t s)
   if (BWD) {
     if ((st = make_adapter_map(&tw1, SQ_BF16, a.b, 3, R, N, L, R * 2, N * R * 2, 64, 64)) != SQ_OK) return st;
     if ((st = make_adapter_map(&tw2, SQ_BF16, a.a, 3, K, R, L, K * 2, K * R * 2, 64, rp)) != SQ_OK) return st;
-    ty = tx;
+    if ((st = make_adapter_map(&ty, yt, a.y, 2, K, M, 1, a.ldy * elt_size(yt), 0, bn, 32)) != SQ_OK) return st;
   } else {
     if ((st = make_adapter_map(&tw1, SQ_BF16, a.a, 3, K, R, L, K * 2, K * R * 2, 64, (uint32_t)R)) != SQ_OK) return st;
     if ((st = make_adapter_map(&tw2, SQ_BF16, a.b, 3, R, N, L, R * 2, N * R * 2, 64, bn)) != SQ_OK) return st;
@@ -234,13 +236,15 @@ sq_status launch_grad_tile_rb(sq::AdapterGradTileArgs g, const CUtensorMap (&t)[
   cfg.blockDim = dim3(sq::kTileThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cs;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cuda_status(cudaLaunchKernelEx(&cfg, kern, t[0], t[1], t[2], t[3], g));
 }
 

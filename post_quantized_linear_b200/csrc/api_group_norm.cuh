@@ -169,7 +169,7 @@ sq_status norm_forward_two(const NormPlan& pl, int64_t B, const sq::NormArgs& a,
   const int ring = sq::norm_ring_bytes(NT, sq::kNormU1, 1);
   const int smem = ring + 4 * sq::norm_smem_floats(NT, pl.t.vx, sq::Vec<XT>::n, pl.t.nb);
   const dim3 grid((unsigned)pl.tiles, (unsigned)(pl.t.G / pl.t.nb), (unsigned)B);
-  sq_status st = launch_grid<sq::group_norm_stats_kernel<XT, NT>>(grid, NT, smem, 1, false, s, a);
+  sq_status st = launch_grid<sq::group_norm_stats_kernel<XT, NT>>(grid, NT, smem, 1, true, s, a);
   if (st != SQ_OK) return st;
   return launch_grid<sq::group_norm_apply_kernel<XT, NT>>(grid, NT, ring + 8 * pl.t.nb, 1, true, s, a);
 }
@@ -184,41 +184,39 @@ sq_status norm_forward(const NormPlan& pl, int64_t B, sq::NormArgs& a, cudaStrea
   const dim3 grid((unsigned)(pl.t.G / pl.t.nb * pl.cs), (unsigned)B);
   return launch_grid<sq::group_norm_cluster_kernel<XT>>(grid, sq::kNormThreads,
                                                         norm_cluster_smem(pl.t, pl.nv, sq::Vec<XT>::n, 1), pl.cs,
-                                                        false, s, a, pl.cs, pl.nv);
-}
-
-sq_status norm_params(const sq::NormBwdArgs& a, int64_t B, float* dgamma, float* dbeta, cudaStream_t s) {
-  return launch_grid<sq::group_norm_bwd_params_kernel>(dim3((unsigned)((a.t.C + 31) / 32)), 32 * sq::kParamWarps, 0, 1,
-                                                       true, s, a, (int32_t)B, dgamma, dbeta);
+                                                        true, s, a, pl.cs, pl.nv);
 }
 
 template <typename XT, int NT>
-sq_status norm_backward_two(const NormPlan& pl, int64_t B, const sq::NormBwdArgs& a, float* dgamma, float* dbeta,
-                            cudaStream_t s) {
+sq_status norm_backward_two(const NormPlan& pl, int64_t B, const sq::NormBwdArgs& a, cudaStream_t s) {
   constexpr int vn = sq::Vec<XT>::n;
   const dim3 grid((unsigned)pl.tiles, (unsigned)(pl.t.G / pl.t.nb), (unsigned)B);
   const int ring = sq::norm_ring_bytes(NT, sq::kNormU2, 2);
   const int smem = ring + 4 * sq::norm_smem_floats(NT, pl.t.vx, vn, pl.t.nb);
-  sq_status st = launch_grid<sq::group_norm_bwd_sums_kernel<XT, NT>>(grid, NT, smem, 1, false, s, a);
-  if (st != SQ_OK || (st = norm_params(a, B, dgamma, dbeta, s)) != SQ_OK) return st;
+  sq_status st = launch_grid<sq::group_norm_bwd_sums_kernel<XT, NT>>(grid, NT, smem, 1, true, s, a);
+  if (st != SQ_OK) return st;
+  st = launch_grid<sq::group_norm_bwd_totals_kernel>(dim3((unsigned)((a.t.C + 31) / 32), (unsigned)B),
+                                                     32 * sq::kParamWarps, 0, 1, true, s, a);
+  if (st != SQ_OK) return st;
   return launch_grid<sq::group_norm_bwd_apply_kernel<XT, NT>>(grid, NT, ring + 8 * (pl.t.vx * vn + pl.t.nb), 1, true, s,
                                                               a);
 }
 
 template <typename XT>
-sq_status norm_backward(const NormPlan& pl, int64_t B, sq::NormBwdArgs& a, float* dgamma, float* dbeta,
-                        cudaStream_t s) {
+sq_status norm_backward(const NormPlan& pl, int64_t B, sq::NormBwdArgs& a, cudaStream_t s) {
   a.t = pl.t;
-  a.tiles = pl.cluster ? 0 : pl.tiles;
+  a.tiles = pl.tiles;
+  a.B = (int32_t)B;
   if (!pl.cluster)
     return pl.threads == sq::kNormThreads
-               ? norm_backward_two<XT, sq::kNormThreads>(pl, B, a, dgamma, dbeta, s)
-               : norm_backward_two<XT, sq::kNormThreadsMax>(pl, B, a, dgamma, dbeta, s);
+               ? norm_backward_two<XT, sq::kNormThreads>(pl, B, a, s)
+               : norm_backward_two<XT, sq::kNormThreadsMax>(pl, B, a, s);
   const dim3 grid((unsigned)(pl.t.G / pl.t.nb * pl.cs), (unsigned)B);
   sq_status st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT>>(
-      grid, sq::kNormThreads, norm_cluster_smem(pl.t, pl.nv, sq::Vec<XT>::n, 2), pl.cs, false, s, a, pl.cs, pl.nv);
-  if (st != SQ_OK || (dgamma == nullptr && dbeta == nullptr)) return st;
-  return norm_params(a, B, dgamma, dbeta, s);
+      grid, sq::kNormThreads, norm_cluster_smem(pl.t, pl.nv, sq::Vec<XT>::n, 2), pl.cs, true, s, a, pl.cs, pl.nv);
+  if (st != SQ_OK || (a.dgamma == nullptr && a.dbeta == nullptr)) return st;
+  return launch_grid<sq::group_norm_bwd_params_kernel>(dim3((unsigned)((a.t.C + 31) / 32)), 32 * sq::kParamWarps, 0, 1,
+                                                       true, s, a);
 }
 
 // Bytes of a backward call's workspace: the images' sums, then the tiles' (none when
@@ -338,10 +336,11 @@ sq_status sq_group_norm_act_backward(const void* dy, int64_t lddy, int64_t dybs,
   a.dy = dy; a.lddy = lddy; a.dybs = B > 1 ? dybs : 0;
   a.dx = dx; a.lddx = lddx; a.dxbs = B > 1 ? dxbs : 0;
   a.gamma = gamma; a.beta = beta; a.stats = stats; a.act = act;
+  a.dgamma = dgamma; a.dbeta = dbeta;
   a.total = static_cast<float*>(workspace);
   a.part = a.total + 2 * (size_t)B * (size_t)C;
-  return xt == SQ_BF16 ? norm_backward<__nv_bfloat16>(pl, B, a, dgamma, dbeta, s)
-                       : norm_backward<float>(pl, B, a, dgamma, dbeta, s);
+  return xt == SQ_BF16 ? norm_backward<__nv_bfloat16>(pl, B, a, s)
+                       : norm_backward<float>(pl, B, a, s);
 }
 
 }  // extern "C"

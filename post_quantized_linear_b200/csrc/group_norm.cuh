@@ -79,8 +79,11 @@ struct NormBwdArgs {
   const float* stats;            // [B][G][2] mean, rstd of the forward pass
   float* part;                   // [B][tiles][2][C]: sums of dz and of dz * (x - mean)
   float* total;                  // [B][2][C]: the same over all positions of an image
+  float* dgamma;                 // [C] or null
+  float* dbeta;
+  int32_t B;
   NormTile t;
-  int32_t tiles;                 // per image; 0: total is written by the clusters
+  int32_t tiles;                 // two passes: per image
   int32_t act;
 };
 
@@ -326,21 +329,26 @@ __device__ __forceinline__ void reduce_groups(const float (&v)[VN], bool active,
   __syncthreads();
 }
 
-// (n, mean, M2) of a union of two sets (Chan et al., "Updating Formulae and a
-// Pairwise Algorithm for Computing Sample Variances").
-__device__ __forceinline__ void chan_merge(float& n, float& mean, float& m2, float nb, float meanb,
-                                           float m2b) {
-  if (nb == 0.0f) return;
-  const float nn = n + nb, d = meanb - mean, f = nb / nn;
-  mean = fmaf(d, f, mean);
-  m2 += m2b + d * d * n * f;
-  n = nn;
-}
-
 __device__ __forceinline__ float dsmem_f32(const float* p, uint32_t rank) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(p), rank)));
   return v;
+}
+// The values at p of the cluster's CTAs 0 .. cs - 1 (cs <= 8), all reads in flight together.
+__device__ __forceinline__ void dsmem_gather(const float* p, int cs, float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v[k] = 0.0f;
+    if (k < cs) v[k] = dsmem_f32(p, k);
+  }
+}
+// Their sum, in rank order.
+__device__ __forceinline__ float dsmem_sum(const float* p, int cs) {
+  float v[8], a = 0.0f;
+  dsmem_gather(p, cs, v);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) a += v[k];
+  return a;
 }
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -397,26 +405,45 @@ struct NormOut {
     float v[VN];
     unpack_pairs<VN>(x, v);
     if constexpr (OUT == OUT_CODES || OUT == OUT_CODES_BF16) {
-      // the codes are those of the bf16 values that y holds
-      uint32_t q[VN], n[VN];
+      // The codes are those of the bf16 values that y holds: of either sign in one byte
+      // (the scale picked by the sign, one fma that rounds, one clamp), parted into q+ and
+      // q- by the bytes' sign bits.
+      uint32_t w[VN / 2], c4[VN / 4];
 #pragma unroll
-      for (int i = 0; i < VN; ++i) {
-        v[i] = __bfloat162float(__float2bfloat16_rn(v[i]));
-        q[i] = code_pos(v[i], rp);
-        n[i] = code_neg(v[i], rn);
+      for (int i = 0; i < VN / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+      for (int i = 0; i < VN / 4; ++i) {
+        uint32_t q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t h = w[2 * i + k / 2];
+          const float x1 = __uint_as_float(k & 1 ? h & 0xFFFF0000u : h << 16);
+          const float t = fmaf(x1, x1 >= 0.0f ? rp : rn, kMagic);
+          q[k] = __float_as_uint(fminf(fmaxf(t, kMagic - 127.0f), kMagic + 127.0f));
+        }
+        c4[i] = pack4_low(q[0], q[1], q[2], q[3]);
+      }
+      uint32_t qp[VN / 4], qn[VN / 4];
+#pragma unroll
+      for (int i = 0; i < VN / 4; ++i) {
+        const uint32_t neg = ((c4[i] >> 7) & 0x01010101u) * 0xFFu;
+        qn[i] = c4[i] & neg;
+        qp[i] = c4[i] & ~neg;
       }
       if constexpr (VN == 8) {
-        *reinterpret_cast<uint2*>(p.q_pos + q_at) =
-            make_uint2(pack4_low(q[0], q[1], q[2], q[3]), pack4_low(q[4], q[5], q[6], q[7]));
-        *reinterpret_cast<uint2*>(p.q_neg + q_at) =
-            make_uint2(pack4_low(n[0], n[1], n[2], n[3]), pack4_low(n[4], n[5], n[6], n[7]));
+        *reinterpret_cast<uint2*>(p.q_pos + q_at) = make_uint2(qp[0], qp[1]);
+        *reinterpret_cast<uint2*>(p.q_neg + q_at) = make_uint2(qn[0], qn[1]);
       } else {
-        *reinterpret_cast<uint32_t*>(p.q_pos + q_at) = pack4_low(q[0], q[1], q[2], q[3]);
-        *reinterpret_cast<uint32_t*>(p.q_neg + q_at) = pack4_low(n[0], n[1], n[2], n[3]);
+        *reinterpret_cast<uint32_t*>(p.q_pos + q_at) = qp[0];
+        *reinterpret_cast<uint32_t*>(p.q_neg + q_at) = qn[0];
       }
       q_at += q_step;
-    }
-    if constexpr (OUT != OUT_CODES) {
+      if constexpr (OUT == OUT_CODES_BF16) {
+        if constexpr (VN == 8) *reinterpret_cast<uint4*>(y) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2*>(y) = make_uint2(w[0], w[1]);
+        y += y_step;
+      }
+    } else {
       store_vec<VN>(y, 0, OUT != OUT_F32, v);
       y += y_step;
     }
@@ -468,6 +495,7 @@ __global__ void __launch_bounds__(kNormThreads, 3) group_norm_cluster_kernel(con
   const int mine = active && r < n_rows ? (n_rows - r + t.ty - 1) / t.ty : 0;
   const int batch = (nv + kNormBatches - 1) / kNormBatches;
   const uint32_t slab = smem_u32(smem) + threadIdx.x * 16;
+  grid_dep_wait();
   for (int b = 0; b < kNormBatches; ++b) {
     for (int i = b * batch; i < min(mine, (b + 1) * batch); ++i) {
       cp_async16(slab + i * NT * 16, base, 16);
@@ -516,9 +544,19 @@ __global__ void __launch_bounds__(kNormThreads, 3) group_norm_cluster_kernel(con
   for (int g = threadIdx.x; g < t.nb; g += NT) {
     float n = 0.0f, mean = 0.0f, m2 = 0.0f;
     if (cs > 1) {
-      for (int k = 0; k < cs; ++k) {
-        const float nk = (float)max(0, min(t.S, (k + 1) * t.rows) - k * t.rows) * (float)t.cpg;
-        chan_merge(n, mean, m2, nk, dsmem_f32(pub_mean + g, k), dsmem_f32(pub_m2 + g, k));
+      float mk[8], qk[8];
+      dsmem_gather(pub_mean + g, cs, mk);
+      dsmem_gather(pub_m2 + g, cs, qk);
+      const float full = (float)t.rows * (float)t.cpg;
+      n = (float)t.S * (float)t.cpg;
+      const float last = n - full * (float)(cs - 1);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mean = fmaf(mk[k], k < cs - 1 ? full : k == cs - 1 ? last : 0.0f, mean);
+      mean /= n;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float d = mk[k] - mean;
+        m2 += fmaf(d * d, k < cs - 1 ? full : k == cs - 1 ? last : 0.0f, qk[k]);
       }
     } else {
       n = n_loc; mean = pub_mean[g]; m2 = pub_m2[g];
@@ -615,7 +653,6 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_stats_kernel
   float* ch = scratch + max(NT * VN, 2 * W);
   float* g_mean = ch + 2 * W;
   float* g_m2 = g_mean + t.nb;
-  grid_dep_launch();
   const int tile = blockIdx.x, cb = blockIdx.y, img = blockIdx.z;
   const int tx = threadIdx.x % t.vx, r = threadIdx.x / t.vx;
   const bool active = r < t.ty;
@@ -625,6 +662,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_stats_kernel
   NormStream<XT, NT, U, 1> in;
   in.at[0] = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + (int64_t)(r0 + r) * p.ldx + c0 + lc;
   in.step[0] = (int64_t)t.ty * p.ldx;
+  grid_dep_wait();
   in.begin(smem, mine);
   uint64_t mean[VN / 2], m2[VN / 2];
 #pragma unroll
@@ -899,9 +937,9 @@ __global__ void __launch_bounds__(kNormThreads, 2)
   const int mine = active && r < n_rows ? (n_rows - r + t.ty - 1) / t.ty : 0;
   const XT* xb = static_cast<const XT*>(p.x) + (int64_t)img * p.xbs + (int64_t)(r0 + r) * p.ldx + c0 + lc;
   const XT* gb = static_cast<const XT*>(p.dy) + (int64_t)img * p.dybs + (int64_t)(r0 + r) * p.lddy + c0 + lc;
-  grid_dep_launch();
   const int batch = (nv + kNormBatches - 1) / kNormBatches;
   const uint32_t slab = smem_u32(smem) + threadIdx.x * 16;
+  grid_dep_wait();
   for (int b = 0; b < kNormBatches; ++b) {
     for (int i = b * batch; i < min(mine, (b + 1) * batch); ++i) {
       cp_async16(slab + 2 * i * NT * 16, xb, 16);
@@ -936,7 +974,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
   for (int c = threadIdx.x; c < 2 * W; c += NT) {
     float a = 0.0f;
     if (cs > 1) {
-      for (int q = 0; q < cs; ++q) a += dsmem_f32(ch + c, q);
+      a = dsmem_sum(ch + c, cs);
     } else {
       a = ch[c];
     }
@@ -960,8 +998,8 @@ __global__ void __launch_bounds__(kNormThreads, 2)
   if (cs > 1) cluster_wait();
 }
 
-// Two passes: the tiles' per-channel sums, the images' (group_norm_bwd_params_kernel),
-// then dx.
+// Two passes: the tiles' per-channel sums, the images' (group_norm_bwd_totals_kernel),
+// then dx and the parameters' gradients.
 template <typename XT, int NT>
 __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_sums_kernel(const NormBwdArgs p) {
   constexpr int VN = Vec<XT>::n, U = kNormU2;
@@ -970,7 +1008,6 @@ __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_sums_kernel(const
   const int W = t.vx * VN;
   float* scratch = reinterpret_cast<float*>(smem + norm_ring_bytes(NT, U, 2));
   float* ch = scratch + max(NT * VN, 2 * W);
-  grid_dep_launch();
   const int tile = blockIdx.x, cb = blockIdx.y, img = blockIdx.z;
   const int tx = threadIdx.x % t.vx, r = threadIdx.x / t.vx;
   const bool active = r < t.ty;
@@ -982,6 +1019,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_sums_kernel(const
   in.at[1] = static_cast<const XT*>(p.dy) + (int64_t)img * p.dybs + (int64_t)(r0 + r) * p.lddy + c0 + lc;
   in.step[0] = (int64_t)t.ty * p.ldx;
   in.step[1] = (int64_t)t.ty * p.lddy;
+  grid_dep_wait();
   in.begin(smem, mine);
   uint64_t t1[VN / 2], t2[VN / 2];
 #pragma unroll
@@ -1043,6 +1081,18 @@ __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_apply_kernel(cons
   in.begin(smem, mine);
   for (int c = threadIdx.x; c < 2 * W; c += NT)
     tot[c] = p.total[(int64_t)img * 2 * t.C + (c < W ? c0 + c : t.C + c0 + c - W)];
+  if (tile == 0 && img == 0) {
+    // one CTA of each channel block adds the images for dbeta and dgamma, in order
+    for (int c = threadIdx.x; c < 2 * W; c += NT) {
+      const int ch = c < W ? c0 + c : c0 + c - W;
+      float* out = c < W ? p.dbeta : p.dgamma;
+      float a = 0.0f;
+      for (int b = 0; b < p.B; ++b)
+        a = fmaf(p.total[((int64_t)b * 2 + (c < W ? 0 : 1)) * t.C + ch],
+                 c < W ? 1.0f : p.stats[((int64_t)b * t.G + ch / t.cpg) * 2 + 1], a);
+      if (out != nullptr) out[ch] = a;
+    }
+  }
   __syncthreads();
   grad_group_means<NT>(p, img, c0, W, tot, g1, g2);
   if (mine > 0) {
@@ -1066,71 +1116,57 @@ __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_apply_kernel(cons
   cp_async_wait<0>();
 }
 
-// dbeta and dgamma, and (two passes) each image's sums over its tiles.  A block
-// has 32 channels; its warps share the tiles of an image and their sums are added in
-// order, so every result repeats bit for bit.
-constexpr int kParamWarps = 16, kParamImages = 8;
-__global__ void __launch_bounds__(32 * kParamWarps) group_norm_bwd_params_kernel(const NormBwdArgs p, int32_t B,
-                                                                                 float* __restrict__ dgamma,
-                                                                                 float* __restrict__ dbeta) {
-  __shared__ float sh[kParamImages][2][kParamWarps][32];
+// Two passes: each image's sums over its tiles.  A block has 32 channels of an image; its
+// warps share the tiles and their sums are added in order, so results repeat bit for bit.
+constexpr int kParamWarps = 16;
+__global__ void __launch_bounds__(32 * kParamWarps) group_norm_bwd_totals_kernel(const NormBwdArgs p) {
+  __shared__ float sh[2][kParamWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int C = p.t.C, c = blockIdx.x * 32 + lane;
-  grid_dep_launch();
+  const int C = p.t.C, c = blockIdx.x * 32 + lane, b = blockIdx.y;
   grid_dep_wait();
-  float sum1 = 0.0f, sum2 = 0.0f;                // this warp's images
-  const float* stat = p.stats + (int64_t)(min(c, C - 1) / p.t.cpg) * 2 + 1;
-  if (p.tiles > 0) {
-    // kParamImages images at a time, all their loads in flight together
-    for (int b0 = 0; b0 < B; b0 += kParamImages) {
-      const int nb = min(kParamImages, B - b0);
-#pragma unroll 1
-      for (int b = 0; b < nb; ++b) {
-        float a1 = 0.0f, a2 = 0.0f;
-        if (c < C) {
-          const float* d = p.part + (int64_t)(b0 + b) * p.tiles * 2 * C + c;
-#pragma unroll 8
-          for (int k = warp; k < p.tiles; k += kParamWarps) {
-            a1 += d[(int64_t)k * 2 * C];
-            a2 += d[(int64_t)k * 2 * C + C];
-          }
-        }
-        sh[b][0][warp][lane] = a1;
-        sh[b][1][warp][lane] = a2;
-      }
-      __syncthreads();
-      // warp w: image w / 2, sum w % 2
-      if (warp < 2 * nb && c < C) {
-        float a = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kParamWarps; ++k) a += sh[warp >> 1][warp & 1][k][lane];
-        p.total[((int64_t)(b0 + (warp >> 1)) * 2 + (warp & 1)) * C + c] = a;
-        sh[warp >> 1][warp & 1][0][lane] = warp & 1 ? a * stat[(int64_t)(b0 + (warp >> 1)) * p.t.G * 2] : a;
-      }
-      __syncthreads();
-      if (warp < 2)
-        for (int b = 0; b < nb; ++b) sum1 += sh[b][warp][0][lane];
-      __syncthreads();
-    }
-    float* out = warp == 0 ? dbeta : dgamma;
-    if (warp < 2 && c < C && out != nullptr) out[c] = sum1;
-    return;
-  }
+  float a1 = 0.0f, a2 = 0.0f;
   if (c < C) {
-#pragma unroll 2
-    for (int b = warp; b < B; b += kParamWarps) {
-      sum1 += p.total[(int64_t)b * 2 * C + c];
-      sum2 = fmaf(p.total[((int64_t)b * 2 + 1) * C + c], stat[(int64_t)b * p.t.G * 2], sum2);
+    const float* d = p.part + (int64_t)b * p.tiles * 2 * C + c;
+#pragma unroll 8
+    for (int k = warp; k < p.tiles; k += kParamWarps) {
+      a1 += d[(int64_t)k * 2 * C];
+      a2 += d[(int64_t)k * 2 * C + C];
     }
   }
-  sh[0][0][warp][lane] = sum1;
-  sh[0][1][warp][lane] = sum2;
+  sh[0][warp][lane] = a1;
+  sh[1][warp][lane] = a2;
   __syncthreads();
   if (warp < 2 && c < C) {
     float a = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kParamWarps; ++k) a += sh[0][warp][k][lane];
-    float* out = warp == 0 ? dbeta : dgamma;
+    for (int k = 0; k < kParamWarps; ++k) a += sh[warp][k][lane];
+    p.total[((int64_t)b * 2 + warp) * C + c] = a;
+  }
+}
+
+// dbeta and dgamma from the images' sums, in order.
+__global__ void __launch_bounds__(32 * kParamWarps) group_norm_bwd_params_kernel(const NormBwdArgs p) {
+  __shared__ float sh[2][kParamWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int C = p.t.C, c = blockIdx.x * 32 + lane;
+  grid_dep_wait();
+  float sum1 = 0.0f, sum2 = 0.0f;                // this warp's images
+  if (c < C) {
+    const float* stat = p.stats + (int64_t)(c / p.t.cpg) * 2 + 1;
+#pragma unroll 4
+    for (int b = warp; b < p.B; b += kParamWarps) {
+      sum1 += p.total[(int64_t)b * 2 * C + c];
+      sum2 = fmaf(p.total[((int64_t)b * 2 + 1) * C + c], stat[(int64_t)b * p.t.G * 2], sum2);
+    }
+  }
+  sh[0][warp][lane] = sum1;
+  sh[1][warp][lane] = sum2;
+  __syncthreads();
+  if (warp < 2 && c < C) {
+    float a = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kParamWarps; ++k) a += sh[warp][k][lane];
+    float* out = warp == 0 ? p.dbeta : p.dgamma;
     if (out != nullptr) out[c] = a;
   }
 }
