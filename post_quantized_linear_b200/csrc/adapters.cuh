@@ -165,31 +165,47 @@ __device__ __forceinline__ void long_slice(int n, int cs, int k, int& from, int&
   to = min(n, from + per);
 }
 
-// Sums of a vector of 8 ranks per thread over the threads that share it:
-// thread tid holds v[] for ranks 8 * (tid % rv) .., out[r * pitch] receives the total.
-// red: kFewThreads * 8 floats.
-__device__ __forceinline__ void reduce_rank_vectors(const float (&v)[8], bool active, int rv, float* red, float* out,
+// Sums over the threads that share a vector of 8 ranks, M rows at a time: thread
+// tid holds v[m][] for ranks 8 * (tid % rv) .., out[r * pitch + m] receives the totals.
+// red: kFewThreads * 8 * M floats.
+template <int M>
+__device__ __forceinline__ void reduce_rank_vectors(const float (&v)[M][8], bool active, int rv, float* red, float* out,
                                                     int pitch) {
-  const int tid = threadIdx.x, outs = 8 * rv, lanes = kFewThreads / rv;
+  const int tid = threadIdx.x, outs = 8 * M * rv, lanes = kFewThreads / rv;
   __syncthreads();
   if (active) {
-    *reinterpret_cast<float4*>(red + tid * 8) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(red + tid * 8 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      *reinterpret_cast<float4*>(red + (tid * M + m) * 8) = make_float4(v[m][0], v[m][1], v[m][2], v[m][3]);
+      *reinterpret_cast<float4*>(red + (tid * M + m) * 8 + 4) = make_float4(v[m][4], v[m][5], v[m][6], v[m][7]);
+    }
   }
   __syncthreads();
-  // `ways` threads share a total, then one adds theirs
-  const int ways = min(lanes, kFewThreads / outs);
+  // a total o = ((rank vector * M) + m) * 8 + i; `ways` threads share it, then one adds theirs
+  const int ways = max(1, min(lanes, kFewThreads / outs));
+  auto put = [&](int o, float t) { out[((o / (8 * M)) * 8 + o % 8) * pitch + o / 8 % M] = t; };
+  if (ways == 1) {
+    for (int o = tid; o < outs; o += kFewThreads) {
+      float t = 0.0f;
+#pragma unroll 4
+      for (int j = 0; j < lanes; ++j) t += red[j * outs + o];
+      put(o, t);
+    }
+    return;
+  }
   const int o = tid % outs, wy = tid / outs;
   float t = 0.0f;
-  if (wy < ways)
+  if (wy < ways) {
+#pragma unroll 4
     for (int j = wy; j < lanes; j += ways) t += red[j * outs + o];
+  }
   __syncthreads();
   if (wy < ways) red[wy * outs + o] = t;
   __syncthreads();
   if (tid < outs) {
     float a = 0.0f;
     for (int j = 0; j < ways; ++j) a += red[j * outs + tid];
-    out[tid * pitch] = a;
+    put(tid, a);
   }
 }
 
@@ -199,10 +215,13 @@ template <int T, typename XT, typename YT, bool BWD>
 __global__ void __launch_bounds__(kFewThreads, T == 1 ? 4 : 2)
     adapter_few_rows_kernel(const AdapterArgs p, int cs) {
   constexpr int XP = kFewChunk + 4;                                   // row pitch: shifts the banks
-  __shared__ __align__(16) float xs[T == 1 ? 4 : T * XP];             // [row][k]
+  constexpr int MR = T == 1 ? 1 : 4;                                  // rows reduced at a time
+  // rows [row][k] while they are contracted, then the threads' sums
+  __shared__ __align__(16) float xs[kFewThreads * 8 * MR];
+  static_assert(T == 1 || T * XP <= kFewThreads * 8 * MR, "");
   __shared__ __align__(16) float part[T * kAdapterMaxRank];           // [r][row], this CTA's share
   __shared__ __align__(16) float full[T * kAdapterMaxRank];           // [r][row], times scale
-  __shared__ __align__(16) float red[kFewThreads * 8];
+  __shared__ __align__(16) float red[BWD ? 4 : T * kAdapterMaxRank];  // forward: the warps' sums
   const int rank = blockIdx.x % cs;
   const int tid = threadIdx.x;
   grid_dep_wait();
@@ -278,18 +297,14 @@ __global__ void __launch_bounds__(kFewThreads, T == 1 ? 4 : 2)
         }
       }
     }
-#pragma unroll 1
-    for (int m = 0; m < T; ++m) {
-      float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    for (int m0 = 0; m0 < T; m0 += MR) {
+      float v[MR][8];
 #pragma unroll
-      for (int q = 0; q < T; ++q)
-        if (q == m) {
+      for (int m = 0; m < MR; ++m)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = acc[q][i];
-        }
-      if (m < it.n) reduce_rank_vectors(v, nl_i < nl, RV, red, part + m, T);
+        for (int i = 0; i < 8; ++i) v[m][i] = acc[m0 + m][i];
+      if (m0 < it.n) reduce_rank_vectors<MR>(v, nl_i < nl, RV, xs, part + m0, T);
     }
   } else {
     const int quads = (R + 3) / 4, kg = max(1, kFewWarps / quads);
@@ -531,8 +546,11 @@ __global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const Adapte
   float* fs = sh;                                   // [row][rank]
   float* gs = sh + kGradRows * kAdapterMaxRank;     // [row][column]
   const int tid = threadIdx.x, l = blockIdx.y, rank = blockIdx.x % p.cs, c0 = blockIdx.x / p.cs * kGradCols;
-  // thread: 8 columns (cx) and the ranks ry, ry + 32, ...
-  const int cx = (tid % 8) * 8, ry = tid / 8;
+  // a thread: four ranks (r0 ..), the columns cx .. cx + 3 and 32 + cx .. , and every
+  // `groups`-th row; the groups' sums are added at the end
+  const int quads = p.R / 4, cx = (tid % 8) * 4, r0 = tid / 8 % quads * 4, group = tid / 8 / quads;
+  const int groups = kGradThreads / 8 / quads;
+  const bool active = group < groups;
   float acc[4][8];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -562,50 +580,63 @@ __global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const Adapte
         *reinterpret_cast<float4*>(gs + m * kGradCols + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
       }
       __syncthreads();
-      for (int m = 0; m < n; ++m) {
-        const float4 v0 = *reinterpret_cast<const float4*>(gs + m * kGradCols + cx);
-        const float4 v1 = *reinterpret_cast<const float4*>(gs + m * kGradCols + cx + 4);
-        const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+      if (active) {
+#pragma unroll 2
+        for (int m = group; m < n; m += groups) {
+          const float4 w = *reinterpret_cast<const float4*>(fs + m * kAdapterMaxRank + r0);
+          const float4 v0 = *reinterpret_cast<const float4*>(gs + m * kGradCols + cx);
+          const float4 v1 = *reinterpret_cast<const float4*>(gs + m * kGradCols + cx + 32);
+          const float wv[4] = {w.x, w.y, w.z, w.w};
+          const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (ry + 32 * i < p.R) {
-            const float w = fs[m * kAdapterMaxRank + ry + 32 * i];
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(w, v[j], acc[i][j]);
-          }
+            for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(wv[i], v[j], acc[i][j]);
         }
       }
     }
   }
+  // the groups' sums [group][rank][column] (groups * R <= 128), then this CTA's in the first
+  const int outs = p.R * kGradCols;
+  __syncthreads();
+  if (active) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float* d = sh + group * outs + (r0 + i) * kGradCols + cx;
+      *reinterpret_cast<float4*>(d) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      *reinterpret_cast<float4*>(d + 32) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
+  }
+  __syncthreads();
+  for (int o = tid * 4; o < outs; o += kGradThreads * 4) {
+    float4 t = *reinterpret_cast<const float4*>(sh + o);
+    for (int k = 1; k < groups; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(sh + k * outs + o);
+      t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+    }
+    *reinterpret_cast<float4*>(sh + o) = t;
+  }
   if (p.cs > 1) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (ry + 32 * i < p.R) {
-#pragma unroll
-        for (int j = 0; j < 8; j += 4)
-          *reinterpret_cast<float4*>(sh + (ry + 32 * i) * kGradCols + cx + j) =
-              make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
-      }
     cluster_arrive();
     cluster_wait();
+  } else {
+    __syncthreads();
   }
   const float scale = p.scale != nullptr ? __ldg(p.scale + l) : 1.0f;
+  // the CTAs of the cluster write eight columns of a rank in turn
+  for (int u = tid; u < outs / 8; u += kGradThreads) {
+    if (p.cs > 1 && u % p.cs != rank) continue;
+    const int r = u / (kGradCols / 8), c = c0 + u % (kGradCols / 8) * 8;
+    if (c >= p.C) continue;
+    float v[8];
+    dsmem_sum8(sh + u * 8, p.cs, v);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = ry + 32 * i;
-    // the CTAs of the cluster write the ranks in turn
-    if (r < p.R && (p.cs == 1 || r % p.cs == rank)) {
-      float v[8];
+    for (int j = 0; j < 8; ++j) v[j] *= scale;
+    if (TRANS) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = acc[i][j];
-      if (p.cs > 1) dsmem_sum8(sh + r * kGradCols + cx, p.cs, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = c0 + cx + j;
-        if (c < p.C)
-          p.out[TRANS ? ((int64_t)l * p.C + c) * p.R + r : ((int64_t)l * p.R + r) * p.C + c] = v[j] * scale;
-      }
+      for (int j = 0; j < 8; ++j) p.out[((int64_t)l * p.C + c + j) * p.R + r] = v[j];
+    } else {
+      store_vec<8>(p.out, ((int64_t)l * p.R + r) * p.C + c, false, v);
     }
   }
   __syncwarp();
