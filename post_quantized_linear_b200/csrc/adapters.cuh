@@ -510,7 +510,8 @@ __device__ __forceinline__ float4 dsmem_f32x4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));
+               : "r"(addr)
+               : "memory");
   return v;
 }
 // Eight consecutive values at p summed over the cluster's CTAs in rank order, four

@@ -77,7 +77,8 @@ constexpr int kTileRows = 128;
 constexpr int kTileThreads = 320;          // TMA warp, MMA warp, eight epilogue warps
 constexpr int kTileEpiWarps = 8;
 constexpr int kTileX = kTileRows * 128;    // bytes of a 128-row, 128-byte-wide tile
-constexpr int kTileBars = 256;             // bytes of barriers and flags
+constexpr int kTileBars = 512;             // bytes of barriers and flags
+constexpr int kTileStages = 8;             // most slots of the ring
 
 struct AdapterTileArgs {
   AdapterArgs p;
@@ -146,10 +147,10 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
   const int RP = (R + 15) & ~15, rt = (RP + 63) / 64;
   uint8_t* hbuf = smem + NS * args.slot_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(hbuf + adapter_h_bytes(RP, args.parts));
-  uint64_t* full = bars;             // [4]
-  uint64_t* empty1 = full + 4;       // [4] slot free: its products are done
-  uint64_t* empty3 = empty1 + 4;     // [4] forward, second product: its tile of y is read
-  uint64_t* d_full = empty3 + 4;     // [3]
+  uint64_t* full = bars;                       // [kTileStages]
+  uint64_t* empty1 = full + kTileStages;       // [kTileStages] slot free: its products are done
+  uint64_t* empty3 = empty1 + kTileStages;     // [kTileStages] forward, second product: its tile of y is read
+  uint64_t* d_full = empty3 + kTileStages;     // [3]
   uint64_t* d_empty = d_full + 3;    // [3]
   uint64_t* h_full = d_empty + 3;
   uint64_t* h_ready = h_full + 1;
@@ -323,7 +324,18 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
         if (u < u1) {
-          dsmem_sum8(reinterpret_cast<const float*>(hbuf) + (u / octs) * (RP + 4) + (u % octs) * 8, cs, v[k]);
+          const float* at = reinterpret_cast<const float*>(hbuf) + (u / octs) * (RP + 4) + (u % octs) * 8;
+          dsmem_sum8(at, cs, v[k]);
+          // The values have to be here before this warp says so: a store of the sums (into the
+          // unit's own place, which no other thread reads) depends on them, and the arrival
+          // comes behind it.
+          const uint32_t a = smem_u32(at);
+          const uint32_t lo[4] = {__float_as_uint(v[k][0]), __float_as_uint(v[k][1]), __float_as_uint(v[k][2]),
+                                  __float_as_uint(v[k][3])};
+          const uint32_t hi[4] = {__float_as_uint(v[k][4]), __float_as_uint(v[k][5]), __float_as_uint(v[k][6]),
+                                  __float_as_uint(v[k][7])};
+          sts128(a, lo);
+          sts128(a + 16, hi);
         }
       }
       __syncwarp();
@@ -367,7 +379,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
       }
     }
     // Output tiles; a thread has 64 bytes of its row.  Forward: they are added to y's, read
-    // from the ring (the slot goes back at once), and stored in whole 32-byte sectors: that
+    // from the ring, and stored in whole 32-byte sectors: that
     // costs the load/store unit a line per row, but held the ring's slots shorter than TMA
     // stores from them (62 us instead of 67 on the ragged batch of 16384 x 2304 -> 3456).
     // Backward: no ring to hold up; tiles are put together in the first product's room (the
@@ -392,20 +404,14 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) y[q] = lds128(mine + (((half * 4 + q) ^ (lane & 7)) << 4));
         } else {
-          // this room's last store has been read (at most NS - 1 younger ones are under way)
-          if (issuer && j >= NS) {
-            if (NS == 3) bulk_wait_read<2>();
-            else bulk_wait_read<3>();
-          }
+          // this room's last store has been read: NS >= 3 rooms, two younger ones may be under way
+          if (issuer && j >= NS) bulk_wait_read<2>();
           quarter_sync(quad);
         }
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(d_empty + b));
-          if (!BWD) mbar_arrive(smem_u32(empty3 + s));
-        }
+        if (lane == 0) mbar_arrive(smem_u32(d_empty + b));
         uint32_t w[16];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {                // 16-byte chunks
@@ -434,6 +440,10 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
             if (c + 32 / ES < E)
               store_u32x8(out + c + 32 / ES, *reinterpret_cast<const uint32_t(*)[8]>(w + 8), args.wide != 0);
           }
+          // behind the stores, which depend on what was read of the slot: an arrival right after
+          // the loads let the ring overwrite rows that were still on their way to registers
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(empty3 + s));
         } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q)

@@ -148,16 +148,26 @@ sq_status launch_tile_rb(sq::AdapterTileArgs t, const CUtensorMap& tx, const CUt
   t.wait_budget = g_wait_budget;
   t.starve = g_debug_starve;
   const int rest = sq::adapter_h_bytes(rp, t.parts) + sq::kTileBars + 1024;
-  const bool two = RB == 64 && 3 * t.slot_bytes + rest <= kSmemPerSm / 2 - 1024;
-  t.stages = two ? 3 : 4 * t.slot_bytes + rest <= kSmemPerSm ? 4 : 3;
-  const int smem = t.stages * t.slot_bytes + rest;
   // Pieces expected: the batch cut into 128 rows, or one per request.  The largest
   // cluster whose pieces are all resident at once: a second wave of a few clusters
-  // costs a whole pass.
+  // costs a whole pass.  Two CTAs on an SM overlap one another's steps; where that would
+  // make clusters of more than four, one CTA with a deep ring and a smaller exchange is
+  // faster (32 pieces of 4608 -> 4608, rank 64: 41.5 us, not 44.9; 64 pieces of
+  // 8192 x 1152 -> 4608 backward: 75.6 us, not 68.9, so not below that).
   const int64_t pieces = std::max<int64_t>((a.M + sq::kTileRows - 1) / sq::kTileRows, std::min<int64_t>(a.Q, a.M));
-  const int most = std::min({8, (D + 63) / 64, (E + 128 / (int)sizeof(YT) - 1) / (128 / (int)sizeof(YT))});
-  int cs = std::max(1, most);
-  while (cs > 1 && pieces > (two ? 2 : 1) * resident_clusters<kern>(cs, sq::kTileThreads, smem)) --cs;
+  const int most = std::max(1, std::min({8, (D + 63) / 64, (E + 128 / (int)sizeof(YT) - 1) / (128 / (int)sizeof(YT))}));
+  auto choose = [&](bool two, int* stages) {
+    const int room = two ? kSmemPerSm / 2 - 1024 : kSmemPerSm;
+    *stages = std::min(sq::kTileStages, (room - rest) / t.slot_bytes);
+    const int smem = *stages * t.slot_bytes + rest;
+    int cs = most;
+    while (cs > 1 && pieces > (two ? 2 : 1) * resident_clusters<kern>(cs, sq::kTileThreads, smem)) --cs;
+    return cs;
+  };
+  bool two = RB == 64 && 3 * t.slot_bytes + rest <= kSmemPerSm / 2 - 1024;
+  int cs = choose(two, &t.stages);
+  if (two && cs > 4) cs = choose(two = false, &t.stages);
+  const int smem = t.stages * t.slot_bytes + rest;
   t.cs = cs;
   cudaError_t e = smem_limit<kern>(kSmemPerSm);
   if (e != cudaSuccess) return cuda_status(e);

@@ -276,3 +276,25 @@ def test_norm_codes_linear_adapters_run(B, S, C, N, act):
     (ref, _), (e2, _) = forward64(full, rows, ad, bounds, idx)
     mag = q.abs() @ (qw.codes.double().abs() * qw.scales[0].double()[:, None]).t() * max(sp.item(), sn.item())
     check(base, ref, e2 + e + half_step(BF) * full.abs() + 1e-6 * mag)
+
+
+@pytest.mark.parametrize("R", [16, 64, 128])
+def test_results_repeat_under_load(R):
+    """The same call over and over, other calls in flight around it, gives the same bits:
+    sums have a fixed order, and no step overtakes another in the kernels' rings (a slot
+    given back while its last rows were still being read showed here)."""
+    x, y, ad, g = make(8192, 1152, 768, 4, R, seed=R)
+    dy = torch.randn(8192, 768, generator=g, device="cuda").to(BF)
+    bounds, idx = requests([256] * 30 + [100, 412], [i % 4 for i in range(32)])
+    other = torch.randn_like(y)
+    base = y.clone()
+    want, hidden = pq.adapter_add(y.clone(), x, ad, bounds, idx, return_hidden=True)
+    grads = pq.adapter_backward(dy, x, hidden, ad, bounds, idx)
+    for _ in range(40):
+        pq.adapter_add(other, x, ad, bounds, idx)
+        y.copy_(base)
+        _, h = pq.adapter_add(y, x, ad, bounds, idx, return_hidden=True)
+        again = pq.adapter_backward(dy, x, h, ad, bounds, idx)
+        assert torch.equal(y, want) and torch.equal(h, hidden)
+        assert all(torch.equal(a, b) for a, b in zip(again, grads))
+    assert pq.stream_status() == 0
