@@ -47,18 +47,20 @@ sq_status norm_plan_for(int64_t B, int64_t S, int64_t C, int32_t groups, int es,
       const sq::NormTile t{(int32_t)S, (int32_t)C, groups, cpg, unit * m, (int32_t)vx, ty, (int32_t)rows};
       const int smem = norm_cluster_smem(t, (int)nv, vn, tensors) + 1024;
       if (smem > kNormSmem) continue;
-      // Estimated time: waves of resident CTAs, each the latency of its loads,
-      // reductions and stores and of the cluster barriers (measured at the smallest
-      // maps), plus its traffic at an SM's share of the copy rate (44 KB/us); narrow
-      // blocks waste part of the 32-byte sectors.
+      // Estimated time: waves of resident CTAs, each the latency of its loads, reductions
+      // and stores and of the cluster barriers, its arithmetic (an SM's 16 warps or more
+      // take 0.022 us a KB, fewer in proportion longer), and its traffic at an SM's share of
+      // the copy rate (44 KB/us); fitted to all choices at eight sizes.
       const int res = std::min(tensors == 1 ? 3 : 2, kNormSmem / smem);
       const int64_t ctas = B * (blocks_all / m) * cs;
       const int64_t waves = (ctas + (int64_t)sms * res - 1) / ((int64_t)sms * res);
       const double on_sm = (double)std::min<int64_t>(res, (ctas + sms - 1) / sms);
       const int chunk = (int)vx * 16;
       const double waste = chunk % 32 == 0 || chunk >= C * es ? 1.0 : (double)((chunk + 31) / 32 * 32 + 16) / chunk;
-      const double kb = (double)rows * chunk * (tensors + 1) / 1024.0 * waste;
-      const double us = (double)waves * (2.0 + (cs > 1 ? 1.0 : 0.0) + on_sm * kb / 44.0);
+      const double slab = (double)rows * chunk / 1024.0;
+      const double busy = std::max(1.0, 16.0 / (on_sm * sq::kNormThreads / 32.0));
+      const double us = (double)waves * (2.0 + 0.7 * (cs > 1) + 0.15 * (cs - 1) +
+                                         on_sm * slab * (0.022 * tensors * busy + waste * (tensors + 1) / 44.0));
       if (us < best_us) {
         best_us = us;
         best.t = t;
@@ -212,7 +214,7 @@ sq_status norm_backward(const NormPlan& pl, int64_t B, sq::NormBwdArgs& a, cudaS
                ? norm_backward_two<XT, sq::kNormThreads>(pl, B, a, s)
                : norm_backward_two<XT, sq::kNormThreadsMax>(pl, B, a, s);
   const dim3 grid((unsigned)(pl.t.G / pl.t.nb * pl.cs), (unsigned)B);
-  sq_status st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT>>(
+  const sq_status st = launch_grid<sq::group_norm_bwd_cluster_kernel<XT>>(
       grid, sq::kNormThreads, norm_cluster_smem(pl.t, pl.nv, sq::Vec<XT>::n, 2), pl.cs, true, s, a, pl.cs, pl.nv);
   if (st != SQ_OK || (a.dgamma == nullptr && a.dbeta == nullptr)) return st;
   return launch_grid<sq::group_norm_bwd_params_kernel>(dim3((unsigned)((a.t.C + 31) / 32)), 32 * sq::kParamWarps, 0, 1,

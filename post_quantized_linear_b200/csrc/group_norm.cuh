@@ -238,41 +238,46 @@ __device__ __forceinline__ void with_act_out(const NormArgs& p, F&& f) {
 }
 
 // --------------------------------------------------------------- reductions
-// Per-thread, per-channel values v[VN] of all rows of threads -> per-channel
-// totals ch[0 .. vx*VN) in shared memory.  `scratch` holds NT * VN
-// floats.  Begins and ends with every thread past a barrier.
-template <int NT, int VN>
-__device__ __forceinline__ void reduce_channels(const float (&v)[VN], bool active, int tx, int r,
+// Per-thread, per-channel values v[m][VN] (M arrays) of all rows of threads ->
+// per-channel totals ch[m * W + 0 .. W), W = vx * VN, in shared memory.  `scratch` holds
+// NT * VN * M floats.  Begins and ends with every thread past a barrier.
+template <int NT, int VN, int M>
+__device__ __forceinline__ void reduce_channels(const float (&v)[M][VN], bool active, int tx, int r,
                                                 const NormTile& t, float* scratch, float* ch) {
-  const int W = t.vx * VN;
+  const int W = t.vx * VN, W2 = M * W;
   __syncthreads();
   if (active) {
 #pragma unroll
-    for (int i = 0; i < VN; i += 4)
-      *reinterpret_cast<float4*>(scratch + r * W + tx * VN + i) =
-          make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int i = 0; i < VN; i += 4)
+        *reinterpret_cast<float4*>(scratch + r * W2 + m * W + tx * VN + i) =
+            make_float4(v[m][i], v[m][i + 1], v[m][i + 2], v[m][i + 3]);
   }
   __syncthreads();
-  const int nseg = W < NT ? NT / W : 1;
+  const int nseg = W2 < NT ? NT / W2 : 1;
   if (nseg == 1) {
-    for (int c = threadIdx.x; c < W; c += NT) {
+    for (int c = threadIdx.x; c < W2; c += NT) {
       float s = 0.0f;
-      for (int k = 0; k < t.ty; ++k) s += scratch[k * W + c];
+#pragma unroll 4
+      for (int k = 0; k < t.ty; ++k) s += scratch[k * W2 + c];
       ch[c] = s;
     }
     __syncthreads();
     return;
   }
-  const int c = threadIdx.x % W, sg = threadIdx.x / W;
+  const int c = threadIdx.x % W2, sg = threadIdx.x / W2;
   float s = 0.0f;
-  if (sg < nseg)
-    for (int k = sg; k < t.ty; k += nseg) s += scratch[k * W + c];
+  if (sg < nseg) {
+#pragma unroll 4
+    for (int k = sg; k < t.ty; k += nseg) s += scratch[k * W2 + c];
+  }
   __syncthreads();
-  if (sg < nseg) scratch[sg * W + c] = s;
+  if (sg < nseg) scratch[sg * W2 + c] = s;
   __syncthreads();
-  if (threadIdx.x < W) {
+  if (threadIdx.x < W2) {
     float a = 0.0f;
-    for (int k = 0; k < nseg; ++k) a += scratch[k * W + threadIdx.x];
+    for (int k = 0; k < nseg; ++k) a += scratch[k * W2 + threadIdx.x];
     ch[threadIdx.x] = a;
   }
   __syncthreads();
@@ -319,7 +324,39 @@ __device__ __forceinline__ void reduce_groups(const float (&v)[VN], bool active,
     __syncthreads();
     return;
   }
-  reduce_channels<NT, VN>(v, active, tx, r, t, scratch, ch);
+  if (t.cpg > VN) {
+    // a vector meets at most two groups: its first's share and the next one's, in two
+    // columns of ty values; a group's are those of the vectors that begin in it, and the
+    // second share of the one before them
+    const int lc = tx * VN, split = (lc / t.cpg + 1) * t.cpg - lc;
+    float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+      if (i < split) lo += v[i];
+      else hi += v[i];
+    }
+    __syncthreads();
+    if (active) {
+      scratch[tx * t.ty + r] = lo;
+      scratch[NT + tx * t.ty + r] = hi;
+    }
+    __syncthreads();
+    for (int g = warp; g < t.nb; g += NT / 32) {
+      const int first = (g * t.cpg + VN - 1) / VN, last = ((g + 1) * t.cpg - 1) / VN;
+      float a = 0.0f;
+      for (int k = first * t.ty + lane; k < (last + 1) * t.ty; k += 32) a += scratch[k];
+      if (first * VN != g * t.cpg)
+        for (int k = lane; k < t.ty; k += 32) a += scratch[NT + (first - 1) * t.ty + k];
+      a = warp_sum(a);
+      if (lane == 0) grp[g] = a;
+    }
+    __syncthreads();
+    return;
+  }
+  float one[1][VN];
+#pragma unroll
+  for (int i = 0; i < VN; ++i) one[0][i] = v[i];
+  reduce_channels<NT, VN, 1>(one, active, tx, r, t, scratch, ch);
   for (int g = warp; g < t.nb; g += (NT / 32)) {
     float a = 0.0f;
     for (int k = lane; k < t.cpg; k += 32) a += ch[g * t.cpg + k];
@@ -452,9 +489,9 @@ struct NormOut {
 
 // Shared memory of the norm kernels behind the slab, in floats: scratch (reductions,
 // then the cluster's totals), two totals per channel and four values per group.
+__host__ __device__ inline int norm_scratch_floats(int threads, int vn) { return 2 * threads * vn; }
 __host__ __device__ inline int norm_smem_floats(int threads, int vx, int vn, int nb) {
-  const int w2 = 2 * vx * vn;
-  return (threads * vn > w2 ? threads * vn : w2) + w2 + 4 * nb;
+  return norm_scratch_floats(threads, vn) + 2 * vx * vn + 4 * nb;
 }
 constexpr int kNormBatches = 4;   // groups of copies that a slab's sums wait for one after the other
 
@@ -466,10 +503,49 @@ __device__ __forceinline__ void slab_wait(int b) {
   else cp_async_wait<0>();
 }
 
+// Running mean and squared deviations of a thread's rows, per channel: four rows at a
+// time (their mean, the deviations from it, merged by the formula of Chan, Golub and
+// LeVeque, "Updating Formulae and a Pairwise Algorithm for Computing Sample Variances"),
+// so nothing is lost to a large mean or to rows far off the rest.
+template <int VN>
+struct RowStats {
+  uint64_t mean[VN / 2], m2[VN / 2];
+  float n;
+  __device__ __forceinline__ void clear() {
+    n = 0.0f;
+#pragma unroll
+    for (int k = 0; k < VN / 2; ++k) mean[k] = m2[k] = 0;
+  }
+  template <int U>
+  __device__ __forceinline__ void add(const uint64_t (&v)[U][VN / 2]) {
+    const float f = __fdividef((float)U, n + (float)U);   // the new rows' share of all
+    const uint64_t inv = f2_both(-1.0f / (float)U), f2 = f2_both(-f), nf = f2_both(n * f);
+#pragma unroll
+    for (int c = 0; c < VN / 2; ++c) {
+      uint64_t sum = v[0][c], q = 0;
+#pragma unroll
+      for (int i = 1; i < U; ++i) sum = f2_add(sum, v[i][c]);
+      sum = f2_mul(sum, inv);                       // minus the rows' mean
+      if (U > 1) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const uint64_t d = f2_add(v[i][c], sum);
+          q = f2_fma(d, d, q);
+        }
+      }
+      const uint64_t d = f2_add(sum, mean[c]);      // running mean minus the rows' mean
+      mean[c] = f2_fma(d, f2, mean[c]);
+      m2[c] = f2_add(m2[c], f2_fma(f2_mul(d, d), nf, q));
+    }
+    n += (float)U;
+  }
+};
+
 // ------------------------------------------------------ forward, slab on chip
 // Cluster of `cs` CTAs per (image, channel block); CTA rank k holds positions
-// k*rows .. of it, nv 16-byte vectors per thread.  The group's mean first, then the
-// squared deviations from it: as exact as two passes over memory.
+// k*rows .. of it, nv 16-byte vectors per thread.  The statistics are taken as the rows
+// arrive.  (512 threads per CTA, for slabs that have an SM to themselves, gained nothing:
+// 11.9 us, not 11.2, on 8 x 1024 x 640 bf16.)
 template <typename XT>
 __global__ void __launch_bounds__(kNormThreads, 3) group_norm_cluster_kernel(const NormArgs p, int cs, int nv) {
   constexpr int VN = Vec<XT>::n, NT = kNormThreads;
@@ -477,7 +553,7 @@ __global__ void __launch_bounds__(kNormThreads, 3) group_norm_cluster_kernel(con
   const NormTile& t = p.t;
   const int W = t.vx * VN;
   float* scratch = reinterpret_cast<float*>(smem + (size_t)nv * NT * 16);
-  float* ch = scratch + max(NT * VN, 2 * W);
+  float* ch = scratch + norm_scratch_floats(NT, VN);
   float* pub_mean = ch + 2 * W;
   float* pub_m2 = pub_mean + t.nb;
   float* fin_mean = pub_m2 + t.nb;
@@ -503,42 +579,42 @@ __global__ void __launch_bounds__(kNormThreads, 3) group_norm_cluster_kernel(con
     }
     cp_async_commit();
   }
-  uint64_t s2[VN / 2];
-#pragma unroll
-  for (int k = 0; k < VN / 2; ++k) s2[k] = 0;
+  RowStats<VN> st;
+  st.clear();
   for (int b = 0; b < kNormBatches; ++b) {
     slab_wait(b);
-#pragma unroll 2
-    for (int i = b * batch; i < min(mine, (b + 1) * batch); ++i) {
-      uint64_t v[VN / 2];
-      load_pairs<XT>(lds128(slab + i * NT * 16), v);
+    int i = b * batch;
+    const int end = min(mine, (b + 1) * batch);
+#pragma unroll 1
+    for (; i + 4 <= end; i += 4) {
+      uint64_t v[4][VN / 2];
 #pragma unroll
-      for (int k = 0; k < VN / 2; ++k) s2[k] = f2_add(s2[k], v[k]);
+      for (int j = 0; j < 4; ++j) load_pairs<XT>(lds128(slab + (i + j) * NT * 16), v[j]);
+      st.add(v);
+    }
+#pragma unroll 1
+    for (; i < end; ++i) {
+      uint64_t v[1][VN / 2];
+      load_pairs<XT>(lds128(slab + i * NT * 16), v[0]);
+      st.add(v);
     }
   }
-  float s[VN];
-  unpack_pairs<VN>(s2, s);
+  // the CTA's means and deviations: of the threads' means, then their own and those from
+  // the CTA's mean
+  float mv[VN], qv[VN], s[VN];
+  unpack_pairs<VN>(st.mean, mv);
+  unpack_pairs<VN>(st.m2, qv);
+#pragma unroll
+  for (int k = 0; k < VN; ++k) s[k] = st.n * mv[k];
   reduce_groups<NT, VN>(s, active, tx, r, t, scratch, ch, pub_mean);
   const float n_loc = (float)n_rows * (float)t.cpg;
   for (int g = threadIdx.x; g < t.nb; g += NT) pub_mean[g] = n_loc > 0.0f ? pub_mean[g] / n_loc : 0.0f;
   __syncthreads();
-  uint64_t m[VN / 2];
 #pragma unroll
-  for (int k = 0; k < VN / 2; ++k) {
-    m[k] = active ? f2_pack(-pub_mean[(lc + 2 * k) / t.cpg], -pub_mean[(lc + 2 * k + 1) / t.cpg]) : 0;
-    s2[k] = 0;
+  for (int k = 0; k < VN; ++k) {
+    const float d = active ? mv[k] - pub_mean[(lc + k) / t.cpg] : 0.0f;
+    s[k] = fmaf(st.n * d, d, qv[k]);
   }
-#pragma unroll 2
-  for (int i = 0; i < mine; ++i) {
-    uint64_t v[VN / 2];
-    load_pairs<XT>(lds128(slab + i * NT * 16), v);
-#pragma unroll
-    for (int k = 0; k < VN / 2; ++k) {
-      const uint64_t d = f2_add(v[k], m[k]);
-      s2[k] = f2_fma(d, d, s2[k]);
-    }
-  }
-  unpack_pairs<VN>(s2, s);
   reduce_groups<NT, VN>(s, active, tx, r, t, scratch, ch, pub_m2);
   if (cs > 1) { cluster_arrive(); cluster_wait(); }
   for (int g = threadIdx.x; g < t.nb; g += NT) {
@@ -650,7 +726,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_stats_kernel
   const NormTile& t = p.t;
   const int W = t.vx * VN;
   float* scratch = reinterpret_cast<float*>(smem + norm_ring_bytes(NT, U, 1));
-  float* ch = scratch + max(NT * VN, 2 * W);
+  float* ch = scratch + norm_scratch_floats(NT, VN);
   float* g_mean = ch + 2 * W;
   float* g_m2 = g_mean + t.nb;
   const int tile = blockIdx.x, cb = blockIdx.y, img = blockIdx.z;
@@ -664,54 +740,30 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_stats_kernel
   in.step[0] = (int64_t)t.ty * p.ldx;
   grid_dep_wait();
   in.begin(smem, mine);
-  uint64_t mean[VN / 2], m2[VN / 2];
-#pragma unroll
-  for (int k = 0; k < VN / 2; ++k) mean[k] = m2[k] = 0;
-  // whole steps of U rows, then the rest row by row; f: the new rows' share of all so far
+  RowStats<VN> st;
+  st.clear();
   int k = 0;
   for (; (k + 1) * U <= mine; ++k) {
     const uint32_t at = in.wait(k);
-    const float n0 = (float)(k * U), f = __fdividef((float)U, n0 + (float)U);
     uint64_t v[U][VN / 2];
 #pragma unroll
     for (int i = 0; i < U; ++i) load_pairs<XT>(in.get(at, i, 0), v[i]);
-    const uint64_t inv = f2_both(-1.0f / (float)U), f2 = f2_both(-f), nf = f2_both(n0 * f);
-#pragma unroll
-    for (int c = 0; c < VN / 2; ++c) {
-      uint64_t sum = v[0][c], q = 0;
-#pragma unroll
-      for (int i = 1; i < U; ++i) sum = f2_add(sum, v[i][c]);
-      sum = f2_mul(sum, inv);                       // minus the rows' mean
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const uint64_t d = f2_add(v[i][c], sum);
-        q = f2_fma(d, d, q);
-      }
-      const uint64_t d = f2_add(sum, mean[c]);      // running mean minus the rows' mean
-      mean[c] = f2_fma(d, f2, mean[c]);
-      m2[c] = f2_add(m2[c], f2_fma(f2_mul(d, d), nf, q));
-    }
+    st.add(v);
   }
   if (k * U < mine) {
     const uint32_t at = in.wait(k);
 #pragma unroll 1
     for (int i = 0; k * U + i < mine; ++i) {
-      const float n0 = (float)(k * U + i), f = __fdividef(1.0f, n0 + 1.0f);
-      uint64_t v[VN / 2];
-      load_pairs<XT>(in.get(at, i, 0), v);
-#pragma unroll
-      for (int c = 0; c < VN / 2; ++c) {
-        const uint64_t d = f2_fma(mean[c], f2_both(-1.0f), v[c]);
-        mean[c] = f2_fma(d, f2_both(f), mean[c]);
-        m2[c] = f2_fma(f2_mul(d, d), f2_both(n0 * f), m2[c]);
-      }
+      uint64_t v[1][VN / 2];
+      load_pairs<XT>(in.get(at, i, 0), v[0]);
+      st.add(v);
     }
   }
   cp_async_wait<0>();
   float mv[VN], qv[VN], s[VN];
-  unpack_pairs<VN>(mean, mv);
-  unpack_pairs<VN>(m2, qv);
-  const float n = (float)mine;
+  unpack_pairs<VN>(st.mean, mv);
+  unpack_pairs<VN>(st.m2, qv);
+  const float n = st.n;
 #pragma unroll
   for (int k = 0; k < VN; ++k) s[k] = n * mv[k];
   reduce_groups<NT, VN>(s, active, tx, r, t, scratch, ch, g_mean);
@@ -926,7 +978,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
   const NormTile& t = p.t;
   const int W = t.vx * VN;
   float* scratch = reinterpret_cast<float*>(smem + (size_t)nv * NT * 32);   // later the cluster's totals [2][W]
-  float* ch = scratch + max(NT * VN, 2 * W);                               // this CTA's totals [2][W]
+  float* ch = scratch + norm_scratch_floats(NT, VN);                               // this CTA's totals [2][W]
   float* g1 = ch + 2 * W;
   float* g2 = g1 + t.nb;
   const int rank = blockIdx.x % cs, cb = blockIdx.x / cs, img = blockIdx.y;
@@ -965,11 +1017,10 @@ __global__ void __launch_bounds__(kNormThreads, 2)
       }
     });
   }
-  float s1[VN], s2[VN];
-  unpack_pairs<VN>(t1, s1);
-  unpack_pairs<VN>(t2, s2);
-  reduce_channels<NT, VN>(s1, active, tx, r, t, scratch, ch);
-  reduce_channels<NT, VN>(s2, active, tx, r, t, scratch, ch + W);
+  float both[2][VN];
+  unpack_pairs<VN>(t1, both[0]);
+  unpack_pairs<VN>(t2, both[1]);
+  reduce_channels<NT, VN, 2>(both, active, tx, r, t, scratch, ch);
   if (cs > 1) { cluster_arrive(); cluster_wait(); }
   for (int c = threadIdx.x; c < 2 * W; c += NT) {
     float a = 0.0f;
@@ -1007,7 +1058,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_sums_kernel(const
   const NormTile& t = p.t;
   const int W = t.vx * VN;
   float* scratch = reinterpret_cast<float*>(smem + norm_ring_bytes(NT, U, 2));
-  float* ch = scratch + max(NT * VN, 2 * W);
+  float* ch = scratch + norm_scratch_floats(NT, VN);
   const int tile = blockIdx.x, cb = blockIdx.y, img = blockIdx.z;
   const int tx = threadIdx.x % t.vx, r = threadIdx.x / t.vx;
   const bool active = r < t.ty;
@@ -1044,11 +1095,10 @@ __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_sums_kernel(const
     });
   }
   cp_async_wait<0>();
-  float s1[VN], s2[VN];
-  unpack_pairs<VN>(t1, s1);
-  unpack_pairs<VN>(t2, s2);
-  reduce_channels<NT, VN>(s1, active, tx, r, t, scratch, ch);
-  reduce_channels<NT, VN>(s2, active, tx, r, t, scratch, ch + W);
+  float both[2][VN];
+  unpack_pairs<VN>(t1, both[0]);
+  unpack_pairs<VN>(t2, both[1]);
+  reduce_channels<NT, VN, 2>(both, active, tx, r, t, scratch, ch);
   float* d = p.part + ((int64_t)img * p.tiles + tile) * 2 * t.C + c0;
   for (int c = threadIdx.x; c < W; c += NT) {
     d[c] = ch[c];
