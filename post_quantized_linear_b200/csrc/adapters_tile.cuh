@@ -511,14 +511,17 @@ struct AdapterGradTileArgs {
 constexpr int kGradChain = 8;
 __host__ __device__ inline int adapter_grad_atoms(int rp) { return (3 * rp + 63) / 64; }   // 64 ranks wide
 
+// RB: the largest rank (32, 64, 128); CTAs per SM 3, 2, 1, by their sums' registers and
+// TMEM columns (one MMA thread takes 0.7 us a piece, so an SM needs several).
+__host__ __device__ constexpr int adapter_grad_ctas(int rb) { return rb == 32 ? 3 : rb == 64 ? 2 : 1; }
 template <int RB>
-__global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
+__global__ void __launch_bounds__(kTileThreads, adapter_grad_ctas(RB))
     adapter_grad_tile_kernel(const __grid_constant__ CUtensorMap tg0, const __grid_constant__ CUtensorMap tg1,
                              const __grid_constant__ CUtensorMap tf0, const __grid_constant__ CUtensorMap tf1,
                              const __grid_constant__ AdapterGradTileArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int TM = RB == 64 ? 256 : 512;
+  constexpr int TM = RB == 32 ? 128 : RB == 64 ? 256 : 512;
   const int cs = p.cs, NS = p.stages, R = p.R, RP = (R + 15) & ~15;
   const int rank = blockIdx.x % cs, l = blockIdx.y;
   int tile = blockIdx.x / cs;
@@ -538,6 +541,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
   uint64_t* p_full = ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(p_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* note = abort_flag + 1;   // [4] what the slot holds: 1 the last piece, 2 a short one, 4 nothing
   const long long budget = p.wait_budget;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -577,15 +581,22 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
       tma_prefetch_desc(tf);
     }
     ok = p.starve == 0;
-    while (ok && pieces.mine(m0, n)) {
-      const int s = i % NS;
+    bool more = pieces.mine(m0, n);
+    if (!more && lane == 0) {      // no rows: the MMA thread hears of it through the first slot
+      note[0] = 4;
+      mbar_arrive(smem_u32(full));
+    }
+    while (ok && more) {
+      const int s = i % NS, at = m0, cnt = n;
+      more = pieces.mine(m0, n);
       if (i >= NS && !(ok = wait_warp(smem_u32(empty + s), (i / NS - 1) & 1, abort_flag, budget))) break;
       if (lane == 0) {
         const uint32_t st = smem_u32(smem + s * slot_bytes), bar = smem_u32(full + s);
+        note[s] = (more ? 0 : 1) | (cnt < kGradPiece ? 2 : 0);
         mbar_arrive_expect_tx(bar, slot_bytes);
-        tma_load_2d(st, tg, bar, c0, m0);
-        tma_load_2d(st + 8192, tg, bar, c0 + 64, m0);
-        for (int a = 0; a < atoms; ++a) tma_load_2d(st + kTileX + a * 8192, tf, bar, a * 64, m0);
+        tma_load_2d(st, tg, bar, c0, at);
+        tma_load_2d(st + 8192, tg, bar, c0 + 64, at);
+        for (int a = 0; a < atoms; ++a) tma_load_2d(st + kTileX + a * 8192, tf, bar, a * 64, at);
       }
       ++i;
     }
@@ -593,43 +604,45 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    const int n1 = cols > 256 ? 192 : cols, n2 = cols - n1;
-    int chain = 0, shorts = 0;
-    bool more = pieces.mine(m0, n);
-    while (more) {
-      const int s = i % NS, b = chain % NB;
-      const bool first = i % kGradChain == 0;
-      if (first && chain >= NB &&
-          !(ok = wait_warp(smem_u32(d_empty + b), (chain / NB - 1) & 1, abort_flag, budget)))
-        break;
-      if (!(ok = wait_warp(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
-      if (n < kGradPiece) {
-        if (lane == 0) mbar_arrive(smem_u32(brief));
-        if (!(ok = wait_warp(smem_u32(ready), shorts & 1, abort_flag, budget))) break;
-        ++shorts;
-      }
-      tc_fence_after();
-      more = pieces.mine(m0, n);
-      if (lane == 0) {
-        const uint32_t st = smem_u32(smem + s * slot_bytes), ft = st + kTileX, d = tmem + b * buf;
+    // One thread, kept lean: the producer leaves a note with each slot.
+    if (lane == 0) {
+      const int n1 = cols > 256 ? 192 : cols, n2 = cols - n1;
+      const uint32_t id1 = idesc_bf16(128, n1) | kIdescAMn | kIdescBMn;
+      const uint32_t id2 = idesc_bf16(128, n2 > 0 ? n2 : 16) | kIdescAMn | kIdescBMn;
+      int chain = 0, shorts = 0, s = 0, b = 0;
+      uint32_t phase = 0;
+      bool last = false;
+      while (!last) {
+        const bool first = i % kGradChain == 0;
+        if (first && chain >= NB && !(ok = wait1(smem_u32(d_empty + b), (chain / NB - 1) & 1, abort_flag, budget))) break;
+        if (!(ok = wait1(smem_u32(full + s), phase, abort_flag, budget))) break;
+        const int what = note[s];
+        if (what == 4) break;
+        last = what & 1;
+        if (what & 2) {
+          mbar_arrive(smem_u32(brief));
+          if (!(ok = wait1(smem_u32(ready), shorts & 1, abort_flag, budget))) break;
+          ++shorts;
+        }
+        tc_fence_after();
+        const uint32_t st = smem_u32(smem + s * slot_bytes), d = tmem + b * buf;
+        const uint64_t da = smem_desc_mn_sw128(st, 8192), df = smem_desc_mn_sw128(st + kTileX, 8192);
+        // 16 rows on: 2048 bytes, 128 units of a descriptor's address
 #pragma unroll
         for (int ks = 0; ks < kGradPiece / 16; ++ks) {
-          const uint64_t a = smem_desc_mn_sw128(st + ks * 2048, 8192);
           const uint32_t acc = !first || ks > 0 ? 1u : 0u;
-          umma_bf16(d, a, smem_desc_mn_sw128(ft + ks * 2048, 8192), idesc_bf16(128, n1) | kIdescAMn | kIdescBMn, acc);
-          if (n2 > 0)
-            umma_bf16(d + n1, a, smem_desc_mn_sw128(ft + 3 * 8192 + ks * 2048, 8192),
-                      idesc_bf16(128, n2) | kIdescAMn | kIdescBMn, acc);
+          umma_bf16(d, da + ks * 128, df + ks * 128, id1, acc);
+          if (n2 > 0) umma_bf16(d + n1, da + ks * 128, df + 3 * 512 + ks * 128, id2, acc);
         }
+        ++i;
         umma_commit(smem_u32(empty + s));
-        if (!more || (i + 1) % kGradChain == 0) umma_commit(smem_u32(d_full + b));
+        if (last || i % kGradChain == 0) umma_commit(smem_u32(d_full + b));
+        if (++s == NS) { s = 0; phase ^= 1; }
+        if (i % kGradChain == 0) { ++chain; b = chain % NB; }
       }
-      __syncwarp();
-      ++i;
-      if (i % kGradChain == 0) ++chain;
+      if (i > 0)                   // every product has landed when the last commit has
+        wait_drain(smem_u32(empty + (i - 1) % NS), ((i - 1) / NS) & 1, kDrainBudget);
     }
-    if (lane == 0 && i > 0)        // every product has landed when the last commit has
-      wait_drain(smem_u32(empty + (i - 1) % NS), ((i - 1) / NS) & 1, kDrainBudget);
     __syncwarp();
   } else {
     // ----------------------- short pieces cleared, the chains' sums added up

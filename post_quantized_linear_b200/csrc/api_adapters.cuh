@@ -227,18 +227,25 @@ sq_status launch_grad_tile_rb(sq::AdapterGradTileArgs g, const CUtensorMap (&t)[
   constexpr auto kern = sq::adapter_grad_tile_kernel<RB>;
   const int rp = (g.R + 15) / 16 * 16;
   const int slot = sq::kTileX + sq::adapter_grad_atoms(rp) * 8192;
-  const int room = (RB == 64 ? kSmemPerSm / 2 - 1024 : kSmemPerSm) - sq::kTileBars - 1024;
+  constexpr int on_sm = sq::adapter_grad_ctas(RB);
+  const int room = kSmemPerSm / on_sm - 1024 - sq::kTileBars - 1024;
   g.stages = std::min(4, room / slot);
-  // the cluster shares an adapter's pieces: as many CTAs as are resident at once
+  // The cluster shares an adapter's pieces: the number of CTAs that takes the least time by
+  // waves of resident CTAs, each about ten pieces' time to begin and end.
   const int64_t per = std::max<int64_t>(1, (int64_t)g.M / sq::kGradPiece / std::max(1, std::min(g.L, g.Q)));
   const int64_t ctas = (int64_t)tiles * std::max(1, std::min(g.L, g.Q));
+  const int64_t resident = (int64_t)num_sms() * on_sm;
   int cs = 1;
-  while (cs < 8 && cs < per && ctas * (cs + 1) <= (int64_t)num_sms() * (RB == 64 ? 2 : 1)) ++cs;
+  int64_t least = INT64_MAX;
+  for (int k = 1; k <= 8 && k <= per; ++k) {
+    const int64_t t = (ctas * k + resident - 1) / resident * (10 + (per + k - 1) / k);
+    if (t < least) { least = t; cs = k; }
+  }
   g.cs = cs;
-  // At least the share of shared memory that the CTA has of TMEM (half, or all): a CTA
-  // that is resident never waits for TMEM of another cluster's.
+  // At least the share of shared memory that the CTA has of TMEM (a quarter, half, or
+  // all): a CTA that is resident never waits for TMEM of another cluster's.
   const int smem = std::max(std::max(g.stages * slot, cs > 1 ? 128 * rp * 4 : 0) + sq::kTileBars + 1024,
-                            (RB == 64 ? kSmemPerSm / 2 : kSmemPerSm) - 4096);
+                            kSmemPerSm / (RB == 32 ? 4 : on_sm) - 4096);
   cudaError_t e = smem_limit<kern>(kSmemPerSm);
   if (e != cudaSuccess) return cuda_status(e);
   cudaLaunchConfig_t cfg = {};
@@ -278,7 +285,9 @@ sq_status launch_grad_tiles(const sq::AdapterTileArgs& t, const void* x, int64_t
   g.wait_budget = g_wait_budget;
   g.starve = g_debug_starve;
   const int tiles = g.tiles0 + (a.N + 127) / 128;
-  return a.R <= 64 ? launch_grad_tile_rb<64>(g, maps, tiles, s) : launch_grad_tile_rb<128>(g, maps, tiles, s);
+  return a.R <= 32   ? launch_grad_tile_rb<32>(g, maps, tiles, s)
+         : a.R <= 64 ? launch_grad_tile_rb<64>(g, maps, tiles, s)
+                     : launch_grad_tile_rb<128>(g, maps, tiles, s);
 }
 
 // Bytes of a backward call's workspace: u in fp32, or u and h as three bf16 parts.
