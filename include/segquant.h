@@ -371,7 +371,8 @@ sq_status sq_group_norm_act_backward(const void* dy, int64_t lddy, int64_t dybs,
  * projection.  The struct is host memory; a, b and scale are device buffers:
  * a bf16 [L, R, K], b bf16 [L, N, R], contiguous, scale fp32 [L] (NULL: 1).
  * Adapters of smaller rank are padded with zeros.  R % 8 == 0 and R <= 128 (a
- * higher rank is the sum of two calls); K % 16 == 0, N % 16 == 0. */
+ * higher rank is the sum of two calls); K % 16 == 0, N % 16 == 0 (SQ_ERR_UNSUPPORTED);
+ * L <= 65535, K and N <= SQ_MAX_K (SQ_ERR_RANGE). */
 typedef struct {
   int32_t L;
   int32_t R;
@@ -392,7 +393,7 @@ typedef struct {
  * all other rows of y are neither read nor written.  x: [M, K], y: [M, N]; products
  * are exact, sums in fp32, one rounding to y's type.  hidden: fp32 [M, R] or NULL,
  * receives A_l x (zeros in rows without an adapter) for the backward call.
- * M = 0 is a no-op.  y must not overlap x. */
+ * M = 0 is a no-op; M <= 2^30, requests <= 2^24 (SQ_ERR_RANGE).  y must not overlap x. */
 sq_status sq_adapter_add(const void* x, sq_dtype xt, int64_t M, int64_t ldx,
                          const sq_adapters* adapters, const int32_t* bounds, const int32_t* index,
                          int32_t requests, void* y, sq_dtype yt, int64_t ldy, float* hidden,

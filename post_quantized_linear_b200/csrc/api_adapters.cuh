@@ -10,8 +10,7 @@ sq_status check_adapters(const sq_adapters* ad, const int32_t* bounds, const int
   if (M < 0 || requests < 0) return SQ_ERR_INVALID_ARG;
   if (ad->a == nullptr || ad->b == nullptr) return SQ_ERR_INVALID_ARG;
   if (ad->R % 8 != 0 || ad->R > sq::kAdapterMaxRank || ad->K % 16 != 0 || ad->N % 16 != 0) return SQ_ERR_UNSUPPORTED;
-  if (ad->K > SQ_MAX_K || ad->N > SQ_MAX_K || M > (1 << 30) || requests > (1 << 24) ||
-      (int64_t)ad->L * std::max(ad->K, ad->N) > (int64_t)INT32_MAX - 256)
+  if (ad->K > SQ_MAX_K || ad->N > SQ_MAX_K || M > (1 << 30) || requests > (1 << 24) || ad->L > 65535)
     return SQ_ERR_RANGE;
   if (!aligned16(ad->a) || !aligned16(ad->b)) return SQ_ERR_ALIGNMENT;
   if (bounds == nullptr || (requests > 0 && index == nullptr)) return SQ_ERR_INVALID_ARG;

@@ -98,6 +98,9 @@ CASES = {
     "many_requests": (1500, 256, 128, 7, 32, [1, 2] * 500, [i % 8 - 1 for i in range(1000)], 0),
     "long": (2500, 640, 1920, 2, 16, [2300, 7], [1, 0], 33),
     "none": (40, 128, 64, 2, 8, [20, 20], [-1, -3], 0),
+    "single_rows_many": (613, 128, 96, 4, 8, [1] * 600, [i % 5 - 1 for i in range(600)], 7),
+    "tiles_of_many_requests": (2700, 192, 208, 3, 24, [9, 0, 17] * 100, [i % 4 - 1 for i in range(300)], 3),
+    "middle_rank": (900, 320, 336, 2, 72, [513, 130, 64], [1, 0, 1], 11),
 }
 
 
@@ -199,6 +202,75 @@ def test_non_finite_rows_of_other_requests():
         assert torch.equal(dx[~bad], want_g[0][~bad])
         for l in (0, 2):
             assert torch.equal(da[l], want_g[1][l]) and torch.equal(db[l], want_g[2][l])
+
+
+@pytest.mark.parametrize("rows", [1, 90])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_non_finite_adapters_of_other_requests(rows, dtype):
+    """Infinities and NaN in another adapter reach nothing else: ranks, columns and rows of
+    this one that do not fill the kernels' tiles meet zeros, not their neighbours."""
+    x, y, ad, g = make(3 * rows, 272, 400, 3, 24, dtype, seed=5)
+    dy = torch.randn(3 * rows, 400, generator=g, device="cuda").to(dtype)
+    bounds, idx = requests([rows] * 3, [0, 1, 2])
+    want, h = pq.adapter_add(y.clone(), x, ad, bounds, idx, return_hidden=True)
+    grads = pq.adapter_backward(dy, x, h, ad, bounds, idx)
+    a, b = ad.a.clone(), ad.b.clone()
+    a[1], b[1] = float("nan"), float("inf")
+    bad = pq.Adapters(a, b, ad.scale)
+    got, h2 = pq.adapter_add(y.clone(), x, bad, bounds, idx, return_hidden=True)
+    again = pq.adapter_backward(dy, x, h2, bad, bounds, idx)
+    keep = torch.ones(3 * rows, dtype=torch.bool, device="cuda")
+    keep[rows:2 * rows] = False
+    assert torch.equal(got[keep], want[keep]) and torch.equal(again[0][keep], grads[0][keep])
+    for l in (0, 2):
+        assert torch.equal(again[1][l], grads[1][l]) and torch.equal(again[2][l], grads[2][l])
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams share nothing."""
+    sets = []
+    for k in range(2):
+        x, y, ad, g = make(3000, 768, 512, 3, 32, seed=20 + k)
+        dy = torch.randn(3000, 512, generator=g, device="cuda").to(BF)
+        bounds, idx = requests([1000, 900, 1100], [k, 1, 2])
+        want, h = pq.adapter_add(y.clone(), x, ad, bounds, idx, return_hidden=True)
+        sets.append((x, y, ad, dy, bounds, idx, want, h, pq.adapter_backward(dy, x, h, ad, bounds, idx)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for k, (x, y, ad, dy, bounds, idx, _, h, _) in enumerate(sets):
+            with torch.cuda.stream(streams[k]):
+                got[k].append((pq.adapter_add(y.clone(), x, ad, bounds, idx), pq.adapter_backward(dy, x, h, ad, bounds, idx)))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for out, grads in got[k]:
+            assert torch.equal(out, sets[k][6])
+            assert all(torch.equal(a, b) for a, b in zip(grads, sets[k][8]))
+    assert pq.stream_status() == 0
+
+
+def test_starved_rings_time_out_and_the_context_recovers(dev_lib):
+    """No copy arrives (a host switch of the development library): every wait of the two
+    kernels runs out, the status says so, and the next calls are right."""
+    x, y, ad, g = make(700, 512, 320, 2, 16, seed=30)
+    bounds, idx = requests([300, 400], [0, 1])
+    want, h = pq.adapter_add(y.clone(), x, ad, bounds, idx, return_hidden=True)
+    grads = pq.adapter_backward(y, x, h, ad, bounds, idx)
+    assert pq.stream_status() == 0
+    pq.set_wait_budget(2_000_000)
+    pq.debug_starve_pipeline(True)
+    try:
+        pq.adapter_add(y.clone(), x, ad, bounds, idx)
+        assert pq.stream_status() == pq._lib.SQ_ERR_TIMEOUT
+        pq.adapter_backward(y, x, h, ad, bounds, idx)
+        assert pq.stream_status() == pq._lib.SQ_ERR_TIMEOUT
+    finally:
+        pq.debug_starve_pipeline(False)
+        pq.set_wait_budget(0)
+    assert torch.equal(pq.adapter_add(y.clone(), x, ad, bounds, idx), want)
+    assert all(torch.equal(a, b) for a, b in zip(pq.adapter_backward(y, x, h, ad, bounds, idx), grads))
+    assert pq.stream_status() == 0
 
 
 def test_bad_requests_are_left_out_and_reported():

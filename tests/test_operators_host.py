@@ -121,7 +121,8 @@ def test_adapter_refusals():
     assert add(N=72, ldy=72) == L.SQ_ERR_UNSUPPORTED
     assert add(M=(1 << 30) + 1) == L.SQ_ERR_RANGE
     assert add(K=L.SQ_MAX_K + 16, ldx=L.SQ_MAX_K + 16) == L.SQ_ERR_RANGE
-    assert add(A=1 << 25) == L.SQ_ERR_RANGE
+    assert add(A=65536) == L.SQ_ERR_RANGE
+    assert add(Q=(1 << 24) + 1) == L.SQ_ERR_RANGE
     assert add(a=FAKE + 8) == L.SQ_ERR_ALIGNMENT
     assert add(x=FAKE + 8) == L.SQ_ERR_ALIGNMENT
     assert add(ldy=68) == L.SQ_ERR_ALIGNMENT
