@@ -535,6 +535,9 @@ def _norm_workspace_size(device: int, B: int, S: int, C: int, groups: int, xt: i
     return n.value
 
 
+_segments_of = functools.lru_cache(maxsize=256)(_lib.segments)   # of a tuple of ints, never changed
+
+
 def _workspace(n: int, device, stream):
     """A workspace of n bytes that lives until the call on ``stream`` has run."""
     ws = torch.empty(n, dtype=torch.uint8, device=device)
@@ -605,7 +608,7 @@ def quantize_activations_norm(x: torch.Tensor, groups: int, gamma: Optional[torc
         if B * S > 1:
             ldq = qp.stride(0)
     y = x.new_empty((B * S, C), dtype=torch.bfloat16) if return_y else None
-    seg, keep = _lib.segments(kseg)
+    seg, keep = _segments_of(tuple(kseg))
     xt = _dtype_code(x.dtype)
     wn = _norm_workspace_size(dev, B, S, C, groups, xt, 0)
     ws = _workspace(wn, x.device, stream) if wn else None
