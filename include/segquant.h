@@ -322,7 +322,8 @@ sq_status sq_linear_forward_codes_hadamard(const int8_t* q_pos, const int8_t* q_
  * pointers of maps and codes 16-byte aligned, their strides multiples of 16 bytes.
  * B = 0 or S = 0 is a no-op (gradients of gamma and beta: zeros).  Infinities and
  * NaN stay in their group.  Outputs must not overlap inputs, except that y may be
- * x itself (same type and strides) and dx may be x or dy. */
+ * x itself (same type and strides) and dx may be x or dy; x and dy may repeat an image
+ * (image stride 0), the images of an output lie at least C elements apart. */
 
 /* Host only: workspace bytes (0: none needed, NULL may be passed) of the forward
  * calls (backward = 0) or the backward call (backward = 1) on the current device.
@@ -355,7 +356,7 @@ sq_status sq_quantize_activations_norm(const void* x, sq_dtype xt, int64_t B, in
                                        size_t workspace_bytes, sq_stream_t stream);
 
 /* Gradients: dy, x and dx [B, S, C] of type xt; stats as written by the forward
- * call; with xhat = (x - mean) * rstd and dz = dy * act'(z):
+ * call, 8-byte aligned; with xhat = (x - mean) * rstd and dz = dy * act'(z):
  * dgamma[c] = sum dz * xhat, dbeta[c] = sum dz over positions and images (fp32 [C],
  * overwritten; either may be NULL), dx = rstd * (dz * gamma - m1 - xhat * m2) with
  * m1, m2 the group's means of dz * gamma and dz * gamma * xhat.  Sums run in a fixed

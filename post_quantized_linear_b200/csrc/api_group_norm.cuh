@@ -127,12 +127,18 @@ sq_status norm_sizes(int64_t B, int64_t S, int64_t C, int32_t groups, sq_dtype x
   return SQ_OK;
 }
 
-// A channels-last map: positions ld apart, images bs apart, 16-byte vectors.
-sq_status norm_map(const void* p, int es, int64_t B, int64_t S, int64_t C, int64_t ld, int64_t bs) {
-  if (p == nullptr || ld < C || (B > 1 && bs < 0)) return SQ_ERR_INVALID_ARG;
-  (void)S;
+// A channels-last map: positions ld apart, images bs apart (read maps may repeat an image),
+// 16-byte vectors.
+sq_status norm_map(const void* p, int es, int64_t B, int64_t C, int64_t ld, int64_t bs, bool written) {
+  if (p == nullptr || ld < C || (B > 1 && bs < (written ? C : 0))) return SQ_ERR_INVALID_ARG;
   if (!aligned16(p) || (ld * es) % 16 != 0 || (B > 1 && (bs * es) % 16 != 0)) return SQ_ERR_ALIGNMENT;
   return SQ_OK;
+}
+
+// Whether fp32 arrays (or null) lie on multiples of `bytes`.
+template <typename... P>
+bool aligned_f32(uintptr_t bytes, P... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & (bytes - 1)) == 0;
 }
 
 template <auto KERN, typename... Args>
@@ -248,10 +254,11 @@ sq_status group_norm_forward(const void* x, sq_dtype xt, int64_t B, int64_t S, i
   st = norm_plan(std::max<int64_t>(B, 1), std::max<int64_t>(S, 1), C, groups, elt_size(xt), 1, &pl);
   if (st != SQ_OK) return st;
   if (B == 0 || S == 0) return SQ_OK;
-  st = norm_map(x, elt_size(xt), B, S, C, ldx, xbs);
+  if (!aligned_f32(4, gamma, beta, s_pos, s_neg, stats)) return SQ_ERR_ALIGNMENT;
+  st = norm_map(x, elt_size(xt), B, C, ldx, xbs, false);
   if (st != SQ_OK) return st;
   if (y != nullptr) {
-    st = norm_map(y, elt_size(yt), B, S, C, ldy, ybs);
+    st = norm_map(y, elt_size(yt), B, C, ldy, ybs, true);
     if (st != SQ_OK) return st;
   }
   if (!pl.cluster) {
@@ -316,6 +323,8 @@ sq_status sq_group_norm_act_backward(const void* dy, int64_t lddy, int64_t dybs,
   sq_status st = norm_sizes(B, S, C, groups, xt);
   if (st != SQ_OK) return st;
   if (act < 0 || act > 2) return SQ_ERR_INVALID_ARG;
+  // the statistics are read in pairs
+  if (!aligned_f32(8, stats) || !aligned_f32(4, gamma, beta, dgamma, dbeta)) return SQ_ERR_ALIGNMENT;
   NormPlan pl;
   const int es = elt_size(xt);
   st = norm_plan(std::max<int64_t>(B, 1), std::max<int64_t>(S, 1), C, groups, es, 2, &pl);
@@ -327,9 +336,9 @@ sq_status sq_group_norm_act_backward(const void* dy, int64_t lddy, int64_t dybs,
     return dbeta == nullptr ? SQ_OK : cuda_status(cudaMemsetAsync(dbeta, 0, sizeof(float) * (size_t)C, s));
   }
   if (stats == nullptr) return SQ_ERR_INVALID_ARG;
-  if ((st = norm_map(x, es, B, S, C, ldx, xbs)) != SQ_OK) return st;
-  if ((st = norm_map(dy, es, B, S, C, lddy, dybs)) != SQ_OK) return st;
-  if ((st = norm_map(dx, es, B, S, C, lddx, dxbs)) != SQ_OK) return st;
+  if ((st = norm_map(x, es, B, C, ldx, xbs, false)) != SQ_OK) return st;
+  if ((st = norm_map(dy, es, B, C, lddy, dybs, false)) != SQ_OK) return st;
+  if ((st = norm_map(dx, es, B, C, lddx, dxbs, true)) != SQ_OK) return st;
   if (workspace == nullptr || workspace_bytes < norm_bwd_bytes(pl, B, C))
     return SQ_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return SQ_ERR_ALIGNMENT;

@@ -16,9 +16,9 @@ def _seg(bounds):
 
 
 def norm(x=FAKE, xt=L.SQ_BF16, B=2, S=9, C=64, ldx=64, xbs=576, groups=8, gamma=FAKE, beta=FAKE, eps=1e-5,
-         act=1, y=FAKE, yt=L.SQ_BF16, ldy=64, ybs=576, ws=None, wn=0):
+         act=1, y=FAKE, yt=L.SQ_BF16, ldy=64, ybs=576, ws=None, wn=0, stats=None):
     return L.load().sq_group_norm_act(x, xt, B, S, C, ldx, xbs, groups, gamma, beta, eps, act, y, yt, ldy, ybs,
-                                      None, ws, wn, None)
+                                      stats, ws, wn, None)
 
 
 def test_norm_refusals():
@@ -98,6 +98,16 @@ def test_norm_backward_refusals():
     assert norm_bwd(ws=FAKE + 4) == L.SQ_ERR_ALIGNMENT
     assert norm_bwd(dy=FAKE + 8) == L.SQ_ERR_ALIGNMENT
     assert norm_bwd(groups=5) == L.SQ_ERR_INVALID_ARG
+
+
+def test_misaligned_and_overlapping_norm_arguments():
+    # the backward reads the statistics in pairs: eight bytes; every other fp32 array takes four
+    assert norm_bwd(stats=FAKE + 4) == L.SQ_ERR_ALIGNMENT
+    assert norm(stats=FAKE + 2) == L.SQ_ERR_ALIGNMENT
+    assert codes(sp=FAKE + 2) == L.SQ_ERR_ALIGNMENT
+    # an input may repeat its image, an output not
+    assert norm(ybs=0) == L.SQ_ERR_INVALID_ARG
+    assert norm(ybs=32) == L.SQ_ERR_INVALID_ARG
 
 
 def add(x=FAKE, xt=L.SQ_BF16, M=100, ldx=128, A=2, R=16, K=128, N=64, a=FAKE, b=FAKE, scale=None, bounds=FAKE,
