@@ -109,9 +109,10 @@ __device__ __forceinline__ AdapterItem adapter_item(const AdapterArgs& p, int sl
   if (lo >= count) return it;
   const int s = start(lo), e = start(lo + 1);
   it.l = lo == 0 || lo == p.Q + 1 ? -1 : __ldg(p.index + lo - 1);
+  // (of falling bounds the search may bring any piece)
+  if (s < 0 || e > p.M || e < s || it.l >= p.L || piece < 0 || piece > (e - s) / T) return it;
   it.row = s + piece * T;
   it.n = min(T, e - it.row);
-  if (s < 0 || e > p.M || it.l >= p.L || piece < 0 || it.n < 0) it.n = 0;
   return it;
 }
 
