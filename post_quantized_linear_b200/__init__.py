@@ -539,11 +539,11 @@ _segments_of = functools.lru_cache(maxsize=256)(_lib.segments)   # of a tuple of
 
 
 def _workspace(n: int, device, stream):
-    """A workspace of n bytes that lives until the call on ``stream`` has run."""
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+    """A workspace of n bytes in ``stream``'s order (None: the current stream's)."""
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def group_norm_act(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = None,
@@ -608,7 +608,7 @@ def quantize_activations_norm(x: torch.Tensor, groups: int, gamma: Optional[torc
         if B * S > 1:
             ldq = qp.stride(0)
     y = x.new_empty((B * S, C), dtype=torch.bfloat16) if return_y else None
-    seg, keep = _segments_of(tuple(kseg))
+    seg, keep = _segments_of(tuple(map(int, kseg)))
     xt = _dtype_code(x.dtype)
     wn = _norm_workspace_size(dev, B, S, C, groups, xt, 0)
     ws = _workspace(wn, x.device, stream) if wn else None
