@@ -491,21 +491,24 @@ struct GradPieces {
   }
 };
 
-// fp32 rows: out[l][r][c] = sum over the rows of requests that use l of f[m][r] * g[m][c]
-// (TRANS: written as out[l][c][r]), times scale_l when asked.  One cluster per
-// (64 columns, adapter): its CTAs share the pieces and add their sums in rank order,
-// so they repeat bit for bit.
+// fp32 rows, and requests of few: both gradients in one launch,
+//   out[0][l][r][c] = sum over the rows of requests that use l of f[0][m][r] * g[0][m][c] (dA: u, x),
+//   out[1][l][c][r] = scale_l times the same of f[1] and g[1]                              (dB: h, dy).
+// One cluster per (64 columns, adapter): its CTAs share the pieces and add their sums in
+// rank order, so they repeat bit for bit.
 struct AdapterGradArgs {
-  const float* f;                // [M, R]
-  const void* g;                 // [M, C]
-  int64_t ldg;
-  const float* scale;            // or null
+  const float* f[2];             // [M, R]
+  const void* g[2];              // [M, C]
+  int64_t ldg[2];
+  float* out[2];
+  const float* scale;            // of the second, or null
   const int32_t* bounds;
   const int32_t* index;
-  float* out;
-  int32_t M, C, R, L, Q, cs;
+  int32_t C[2];
+  int32_t tiles0;                // column tiles of the first
+  int32_t M, R, L, Q, cs;
 };
-constexpr int kGradCols = 64, kGradRows = 32, kGradThreads = 256;
+constexpr int kGradCols = 64, kGradThreads = 256;
 
 __device__ __forceinline__ float4 dsmem_f32x4(uint32_t addr) {
   float4 v;
@@ -540,14 +543,16 @@ __device__ __forceinline__ void dsmem_sum8(const float* p, int cs, float (&v)[8]
   }
 }
 
-template <typename GT, bool TRANS>
-__global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const AdapterGradArgs p) {
-  // rows of f and g, then the sums [rank][column]
-  __shared__ __align__(16) float sh[kAdapterMaxRank * kGradCols];
-  static_assert(kGradRows * (kAdapterMaxRank + kGradCols) <= kAdapterMaxRank * kGradCols, "");
-  float* fs = sh;                                   // [row][rank]
-  float* gs = sh + kGradRows * kAdapterMaxRank;     // [row][column]
-  const int tid = threadIdx.x, l = blockIdx.y, rank = blockIdx.x % p.cs, c0 = blockIdx.x / p.cs * kGradCols;
+template <typename GT, int WHICH>
+__device__ __forceinline__ void adapter_grad_tile(const AdapterGradArgs& p, int tile, float* sh) {
+  constexpr bool TRANS = WHICH == 1;
+  const int C = p.C[WHICH];
+  // rows of f and g, a whole piece of them where the ranks leave room; then the sums
+  // [rank][column]
+  const int step = p.R <= 64 ? kGradPiece : kGradPiece / 2;
+  float* fs = sh;                                           // [row][rank]
+  float* gs = sh + kAdapterMaxRank * kGradCols / 2;         // [row][column]
+  const int tid = threadIdx.x, l = blockIdx.y, rank = blockIdx.x % p.cs, c0 = tile * kGradCols;
   // a thread: four ranks (r0 ..), the columns cx .. cx + 3 and 32 + cx .. , and every
   // `groups`-th row; the groups' sums are added at the end
   const int quads = p.R / 4, cx = (tid % 8) * 4, r0 = tid / 8 % quads * 4, group = tid / 8 / quads;
@@ -558,18 +563,17 @@ __global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const Adapte
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
-  grid_dep_wait();
   GradPieces pieces{p.bounds, p.index, p.M, p.Q, l, rank, p.cs};
   const int R4 = p.R / 4;
   int first, count;
   while (pieces.mine(first, count)) {
-    for (int m0 = first; m0 < first + count; m0 += kGradRows) {
-      const int n = min(kGradRows, first + count - m0);
+    for (int m0 = first; m0 < first + count; m0 += step) {
+      const int n = min(step, first + count - m0);
       __syncthreads();
       for (int i = tid; i < n * R4; i += kGradThreads) {
         const int m = i / R4, r = i % R4 * 4;
-        *reinterpret_cast<float4*>(fs + m * kAdapterMaxRank + r) =
-            __ldg(reinterpret_cast<const float4*>(p.f + (int64_t)(m0 + m) * p.R + r));
+        *reinterpret_cast<float4*>(fs + m * p.R + r) =
+            __ldg(reinterpret_cast<const float4*>(p.f[WHICH] + (int64_t)(m0 + m) * p.R + r));
       }
       // C is a multiple of 16
       for (int i = tid; i < n * (kGradCols / 8); i += kGradThreads) {
@@ -577,7 +581,7 @@ __global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const Adapte
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        if (c0 + c < p.C) load8(static_cast<const GT*>(p.g) + (int64_t)(m0 + m) * p.ldg + c0 + c, v);
+        if (c0 + c < C) load8(static_cast<const GT*>(p.g[WHICH]) + (int64_t)(m0 + m) * p.ldg[WHICH] + c0 + c, v);
         *reinterpret_cast<float4*>(gs + m * kGradCols + c) = make_float4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<float4*>(gs + m * kGradCols + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
       }
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const Adapte
       if (active) {
 #pragma unroll 2
         for (int m = group; m < n; m += groups) {
-          const float4 w = *reinterpret_cast<const float4*>(fs + m * kAdapterMaxRank + r0);
+          const float4 w = *reinterpret_cast<const float4*>(fs + m * p.R + r0);
           const float4 v0 = *reinterpret_cast<const float4*>(gs + m * kGradCols + cx);
           const float4 v1 = *reinterpret_cast<const float4*>(gs + m * kGradCols + cx + 32);
           const float wv[4] = {w.x, w.y, w.z, w.w};
@@ -624,25 +628,34 @@ __global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const Adapte
   } else {
     __syncthreads();
   }
-  const float scale = p.scale != nullptr ? __ldg(p.scale + l) : 1.0f;
+  const float scale = TRANS && p.scale != nullptr ? __ldg(p.scale + l) : 1.0f;
   // the CTAs of the cluster write eight columns of a rank in turn
   for (int u = tid; u < outs / 8; u += kGradThreads) {
     if (p.cs > 1 && u % p.cs != rank) continue;
     const int r = u / (kGradCols / 8), c = c0 + u % (kGradCols / 8) * 8;
-    if (c >= p.C) continue;
+    if (c >= C) continue;
     float v[8];
     dsmem_sum8(sh + u * 8, p.cs, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= scale;
     if (TRANS) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p.out[((int64_t)l * p.C + c + j) * p.R + r] = v[j];
+      for (int j = 0; j < 8; ++j) p.out[1][((int64_t)l * C + c + j) * p.R + r] = v[j];
     } else {
-      store_vec<8>(p.out, ((int64_t)l * p.R + r) * p.C + c, false, v);
+      store_vec<8>(p.out[0], ((int64_t)l * p.R + r) * C + c, false, v);
     }
   }
   __syncwarp();
   if (p.cs > 1) { cluster_arrive(); cluster_wait(); }
+}
+
+template <typename XT, typename DT>
+__global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const AdapterGradArgs p) {
+  __shared__ __align__(16) float sh[kAdapterMaxRank * kGradCols];
+  const int tile = blockIdx.x / p.cs;
+  grid_dep_wait();
+  if (tile < p.tiles0) adapter_grad_tile<XT, 0>(p, tile, sh);
+  else adapter_grad_tile<DT, 1>(p, tile - p.tiles0, sh);
 }
 
 }  // namespace sq

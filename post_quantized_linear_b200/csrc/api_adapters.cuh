@@ -68,19 +68,33 @@ sq_status launch_few_rows(const sq::AdapterArgs& a, sq_dtype xt, sq_dtype yt, cu
                     : launch_few_rows_t<sq::kFewRows, BWD>(a, xt, yt, s);
 }
 
-template <bool TRANS>
-sq_status launch_adapter_grad(sq::AdapterGradArgs g, sq_dtype gt, cudaStream_t s) {
-  const int tiles = (g.C + sq::kGradCols - 1) / sq::kGradCols;
-  // the cluster shares an adapter's pieces: enough CTAs for two waves
+constexpr int kGradCtas = 3;      // of adapter_grad_kernel on an SM, by its registers
+
+sq_status launch_adapter_grad(sq::AdapterGradArgs& g, sq_dtype xt, sq_dtype dyt, cudaStream_t s) {
+  g.tiles0 = (g.C[0] + sq::kGradCols - 1) / sq::kGradCols;
+  const int tiles = g.tiles0 + (g.C[1] + sq::kGradCols - 1) / sq::kGradCols;
+  // The cluster shares an adapter's pieces: the number of CTAs that takes the least time,
+  // all of them over the resident ones and the last one behind them, each about two
+  // pieces' time to begin and end (8000 rows of ten uneven requests, 2304 -> 2304, rank 64: 403 us
+  // where one CTA had an adapter's pieces 487).
   const int used = std::max(1, std::min(g.L, g.Q));
   const int64_t per = std::max<int64_t>(1, (int64_t)g.M / sq::kGradPiece / used);
+  const double over = (double)tiles * used / (num_sms() * kGradCtas);
   int cs = 1;
-  while (cs < 8 && cs * 2 <= per && (int64_t)tiles * used * cs * 2 <= 6 * (int64_t)num_sms()) cs *= 2;
+  double least = 1e30;
+  for (int k = 1; k <= 8 && k <= per; ++k) {
+    const double t = (std::max(1.0, over * k) + 1.0) * (2.0 + (double)per / k);
+    if (t < least) { least = t; cs = k; }
+  }
   g.cs = cs;
   const dim3 grid((unsigned)(tiles * cs), (unsigned)g.L);
-  if (gt == SQ_BF16)
-    return launch_grid<sq::adapter_grad_kernel<__nv_bfloat16, TRANS>>(grid, sq::kGradThreads, 0, cs, true, s, g);
-  return launch_grid<sq::adapter_grad_kernel<float, TRANS>>(grid, sq::kGradThreads, 0, cs, true, s, g);
+  using bf16 = __nv_bfloat16;
+  constexpr int n = sq::kGradThreads;
+  if (xt == SQ_BF16)
+    return dyt == SQ_BF16 ? launch_grid<sq::adapter_grad_kernel<bf16, bf16>>(grid, n, 0, cs, true, s, g)
+                          : launch_grid<sq::adapter_grad_kernel<bf16, float>>(grid, n, 0, cs, true, s, g);
+  return dyt == SQ_BF16 ? launch_grid<sq::adapter_grad_kernel<float, bf16>>(grid, n, 0, cs, true, s, g)
+                        : launch_grid<sq::adapter_grad_kernel<float, float>>(grid, n, 0, cs, true, s, g);
 }
 
 // A tiled map of rank 2 or 3, boxes with 128-byte swizzled rows; strides in bytes
@@ -356,10 +370,10 @@ sq_status sq_adapter_backward(const void* dy, sq_dtype dyt, int64_t M, int64_t l
   sq::AdapterGradArgs g = {};
   g.bounds = bounds; g.index = index; g.M = (int32_t)M; g.R = adapters->R; g.L = adapters->L;
   g.Q = M > 0 ? requests : 0;
-  g.f = static_cast<const float*>(workspace); g.g = x; g.ldg = ldx; g.C = (int32_t)adapters->K; g.out = da;
-  if ((st = launch_adapter_grad<false>(g, xt, s)) != SQ_OK) return st;
-  g.f = hidden; g.g = dy; g.ldg = lddy; g.C = (int32_t)adapters->N; g.out = db; g.scale = adapters->scale;
-  return launch_adapter_grad<true>(g, dyt, s);
+  g.f[0] = static_cast<const float*>(workspace); g.g[0] = x; g.ldg[0] = ldx; g.C[0] = (int32_t)adapters->K; g.out[0] = da;
+  g.f[1] = hidden; g.g[1] = dy; g.ldg[1] = lddy; g.C[1] = (int32_t)adapters->N; g.out[1] = db;
+  g.scale = adapters->scale;
+  return launch_adapter_grad(g, xt, dyt, s);
 }
 
 }  // extern "C"
