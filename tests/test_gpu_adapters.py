@@ -204,6 +204,30 @@ def test_non_finite_rows_of_other_requests():
             assert torch.equal(da[l], want_g[1][l]) and torch.equal(db[l], want_g[2][l])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=str)
+@pytest.mark.parametrize("R", [8, 72, 128])
+@pytest.mark.parametrize("lengths", [[1, 2, 3, 0, 1] * 15, [1, 70, 3, 130, 2, 61, 64, 1, 5], [2, 1, 1] * 100],
+                         ids=["one to three rows", "uneven", "300 requests"])
+def test_short_requests_share_steps(lengths, R, dtype):
+    """Requests of a row or two, whose rows share a step of the gradients' sums, beside long
+    ones that are cut in its middle; up to two rows a request on average, and more."""
+    M = sum(lengths) + 3
+    x, dy, ad, _ = make(M, 272, 208, 3, R, dtype, seed=M + R)
+    bounds, idx = requests(lengths, [(i * 7 + i // 5) % 4 - 1 for i in range(len(lengths))])
+    y = torch.zeros_like(dy)
+    (ref, hid), (e, e_h) = forward64(y, x, ad, bounds, idx)
+    _, hidden = pq.adapter_add(y, x, ad, bounds, idx, return_hidden=True)
+    check(y, ref, e)
+    check(hidden, hid, e_h)
+    got = pq.adapter_backward(dy, x, hidden, ad, bounds, idx)
+    want, e = backward64(dy, x, hidden, ad, bounds, idx)
+    for a, b, c in zip(got, want, e):
+        check(a, b, c)
+    again = pq.adapter_backward(dy, x, hidden, ad, bounds, idx)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    assert pq.stream_status() == 0
+
+
 @pytest.mark.parametrize("rows", [1, 90])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_non_finite_adapters_of_other_requests(rows, dtype):
