@@ -132,7 +132,9 @@ __device__ __forceinline__ void check_requests(const AdapterArgs& p, int threads
 // through distributed shared memory in rank order, and each CTA then writes its
 // slice of the columns.  This is the form for batches of requests of a few rows
 // (one conditioning vector each), which are bound by launch and load latency
-// and by the adapters' bytes, and for fp32 rows.
+// and by the adapters' bytes, and for fp32 rows, bound by the fp32 lanes when there are many.
+// 64 requests of one row, 1152 -> 3456, rank 16: 8.9 us; 777 fp32 rows, 1152 -> 2304, rank 8:
+// 14.7 us.
 constexpr int kFewRows = 8;
 constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
@@ -495,7 +497,9 @@ struct GradPieces {
 //   out[0][l][r][c] = sum over the rows of requests that use l of f[0][m][r] * g[0][m][c] (dA: u, x),
 //   out[1][l][c][r] = scale_l times the same of f[1] and g[1]                              (dB: h, dy).
 // One cluster per (64 columns, adapter): its CTAs share the pieces and add their sums in
-// rank order, so they repeat bit for bit.
+// rank order, so they repeat bit for bit.  With the backward's first kernel, 777 fp32 rows,
+// 1152 -> 2304, rank 8: 27 us (34.5 in a launch for each gradient), bound by the latency of the
+// two kernels' loads and sums.
 struct AdapterGradArgs {
   const float* f[2];             // [M, R]
   const void* g[2];              // [M, C]
