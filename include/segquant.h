@@ -502,7 +502,8 @@ sq_status sq_set_wait_budget(int64_t cycles);
 /* Development library only (as above).  Test hook: while enabled, the GEMM
  * kernels' TMA producer issues no copy, so every consumer's bounded wait
  * expires; the launch still returns SQ_OK and sq_stream_status() then reports
- * SQ_ERR_TIMEOUT.  Host only. */
+ * SQ_ERR_TIMEOUT.  With enable > 1 the adapters' first kernel issues enable - 1
+ * of each CTA's copies before it stops (the other kernels none).  Host only. */
 sq_status sq_debug_starve_pipeline(int32_t enable);
 
 #ifdef __cplusplus

@@ -63,6 +63,21 @@ __device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&w)[4]) {
 __device__ __forceinline__ void quarter_sync(int quad) {
   asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
 }
+// The same, and whether both came with `ok`.  Of two warps that wait for one mbarrier, one
+// may see its phase and the other only the abort flag: both have to take the same way, or
+// one of them waits for the other at the quarter's next barrier without a limit.
+__device__ __forceinline__ bool quarter_agree(int quad, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "bar.red.and.pred q, %1, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"(1 + quad), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
 // Cuts 8 fp32 values into their nearest bf16 (packed into w) and the rest (left in v).
 __device__ __forceinline__ void split_bf16(float (&v)[8], uint32_t (&w)[4]) {
 #pragma unroll
@@ -91,7 +106,7 @@ struct AdapterTileArgs {
   __nv_bfloat16* f_u;          // u and h as three bf16 parts side by side, [M][3][rank padded to 16],
   __nv_bfloat16* f_h;          // the operands of the adapters' gradients
   long long wait_budget;
-  int32_t starve;
+  int32_t starve;      // test hook: 0, or one more than the copies that the producer issues
 };
 
 // Shared memory between the two products: this CTA's partial h in fp32 (rows padded
@@ -205,9 +220,10 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
       tma_prefetch_desc(&tw1);
       tma_prefetch_desc(&tw2);
       if (!BWD) tma_prefetch_desc(&ty);
-      bool ok = args.starve == 0;
+      bool ok = true;
+      const int copies = args.starve == 0 ? nk + nt : min(nk + nt, args.starve - 1);
       int i = 0;
-      for (; i < nk + nt && ok; ++i) {
+      for (; i < copies; ++i) {
         const int s = i % NS, prev = i - NS;
         if (prev >= 0) {
           if (BWD || prev < nk) {
@@ -396,7 +412,9 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
     for (int j = 0; j < nt && ok; ++j) {
       const int i = nk + j, s = i % NS, b = j % ND;
       if (!BWD && !(ok = wait_warp(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
-      if (!(ok = wait_warp(smem_u32(d_full + b), (j / ND) & 1, abort_flag, budget))) break;
+      ok = wait_warp(smem_u32(d_full + b), (j / ND) & 1, abort_flag, budget);
+      if (BWD && rows > 0) ok = quarter_agree(quad, ok);   // the quarter's warps meet below
+      if (!ok) break;
       tc_fence_after();
       if (rows > 0) {
         const uint32_t tile = smem_u32(smem + s * args.slot_bytes + quad * 4096), mine = tile + lane * 128;

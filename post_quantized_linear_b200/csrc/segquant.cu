@@ -1228,7 +1228,7 @@ sq_status sq_set_wait_budget(int64_t cycles) {
 
 sq_status sq_debug_starve_pipeline(int32_t enable) {
   if constexpr (!kDev) return SQ_ERR_UNSUPPORTED;
-  g_debug_starve = enable != 0;
+  g_debug_starve = enable < 0 ? 1 : enable;
   return SQ_OK;
 }
 

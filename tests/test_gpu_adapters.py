@@ -297,6 +297,35 @@ def test_starved_rings_time_out_and_the_context_recovers(dev_lib):
     assert pq.stream_status() == 0
 
 
+@pytest.mark.parametrize("lengths", [[300, 400], [130] * 40], ids=["clusters of eight", "more pieces"])
+def test_rings_starved_in_the_middle_time_out_too(dev_lib, lengths):
+    """The copies end after some steps of the first or the second product: every wait has a
+    limit there as well, the two warps that share a quarter's barriers leave the loop over the
+    output tiles together, the status reports it, and the next calls are right."""
+    M = sum(lengths)
+    x, y, ad, g = make(M, 1344, 1344, 2, 40, seed=31)
+    bounds, idx = requests(lengths, [i % 2 for i in range(len(lengths))])
+    want, h = pq.adapter_add(y.clone(), x, ad, bounds, idx, return_hidden=True)
+    grads = pq.adapter_backward(y, x, h, ad, bounds, idx)
+    assert pq.stream_status() == 0
+    starve = dev_lib.sq_debug_starve_pipeline
+    pq.set_wait_budget(2_000_000)
+    try:
+        for copies in range(1, 13):
+            assert starve(1 + copies) == 0
+            pq.adapter_backward(y, x, h, ad, bounds, idx)
+            assert pq.stream_status() == pq._lib.SQ_ERR_TIMEOUT
+            if copies < 4:                       # fewer than any CTA's share of both products
+                pq.adapter_add(y.clone(), x, ad, bounds, idx)
+                assert pq.stream_status() == pq._lib.SQ_ERR_TIMEOUT
+    finally:
+        pq.debug_starve_pipeline(False)
+        pq.set_wait_budget(0)
+    assert torch.equal(pq.adapter_add(y.clone(), x, ad, bounds, idx), want)
+    assert all(torch.equal(a, b) for a, b in zip(pq.adapter_backward(y, x, h, ad, bounds, idx), grads))
+    assert pq.stream_status() == 0
+
+
 def test_bad_requests_are_left_out_and_reported():
     """Bounds outside the batch and an unknown adapter: the kernels' own checks leave those
     requests out and raise the range status; falling bounds raise it, and which rows of
