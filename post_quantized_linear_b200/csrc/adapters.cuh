@@ -48,7 +48,8 @@ struct AdapterItem {
 // request of a slot.  adapter_slots() slots hold every piece in both.
 // Pieces of a request with bounds outside the batch or an index beyond the adapters
 // are left out, so no read or write leaves the tensors; check_requests raises the
-// range status for them.
+// range status for them.  Slots are counted over the bounds cut to the batch, so such a
+// request has no more of them than its rows in it and takes none of another one's.
 constexpr int kLaneRequests = 8, kExactRequests = 32 * kLaneRequests - 2;
 __host__ __device__ inline int64_t adapter_slots(int M, int Q, int T) {
   // pieces: every T rows of the batch end at most one, and so does every request's end
@@ -57,7 +58,9 @@ __host__ __device__ inline int64_t adapter_slots(int M, int Q, int T) {
 __device__ __forceinline__ AdapterItem adapter_item(const AdapterArgs& p, int slot, int T) {
   const int lane = threadIdx.x & 31;
   const int count = p.Q + 2;
-  auto start = [&](int r) { return r == 0 ? 0 : r <= p.Q + 1 ? __ldg(p.bounds + r - 1) : p.M; };
+  auto start = [&](int r) {
+    return r == 0 ? 0 : r <= p.Q + 1 ? min(max(__ldg(p.bounds + r - 1), 0), p.M) : p.M;
+  };
   AdapterItem it;
   it.row = it.n = 0;
   it.l = -1;
@@ -108,9 +111,11 @@ __device__ __forceinline__ AdapterItem adapter_item(const AdapterArgs& p, int sl
   }
   if (lo >= count) return it;
   const int s = start(lo), e = start(lo + 1);
-  it.l = lo == 0 || lo == p.Q + 1 ? -1 : __ldg(p.index + lo - 1);
+  const bool request = lo > 0 && lo <= p.Q;
+  if (request) it.l = __ldg(p.index + lo - 1);
   // (of falling bounds the search may bring any piece)
-  if (s < 0 || e > p.M || e < s || it.l >= p.L || piece < 0 || piece > (e - s) / T) return it;
+  if (e < s || piece < 0 || piece > (e - s) / T) return it;
+  if (request && (__ldg(p.bounds + lo - 1) < 0 || __ldg(p.bounds + lo) > p.M || it.l >= p.L)) return it;
   it.row = s + piece * T;
   it.n = min(T, e - it.row);
   return it;

@@ -343,6 +343,27 @@ def test_bad_requests_are_left_out_and_reported():
     assert pq.stream_status() == 0
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=str)
+@pytest.mark.parametrize("lengths", [[50, 50], [1] * 60, [9] * 20, [9] * 400], ids=lambda v: f"{len(v)} requests")
+def test_a_bound_far_outside_the_batch_costs_no_other_request(lengths, dtype):
+    """The first bound below zero, or the last one behind the batch: that request is left out
+    and the status says so; every other one gets its term, whichever form takes the batch."""
+    M = sum(lengths)
+    x, y, ad, _ = make(M, 128, 64, 3, 16, dtype, seed=M)
+    bounds, idx = requests(lengths, [i % 3 for i in range(len(lengths))])
+    for at, value, rows in ((0, -1000, slice(0, lengths[0])), (-1, M + 100000, slice(M - lengths[-1], M)),
+                            (0, -2 ** 31, slice(0, lengths[0])), (-1, 2 ** 31 - 1, slice(M - lengths[-1], M))):
+        good = idx.clone()
+        good[at] = -1
+        want = pq.adapter_add(y.clone(), x, ad, bounds, good)
+        assert pq.stream_status() == 0
+        bad = bounds.clone()
+        bad[at] = value
+        out = pq.adapter_add(y.clone(), x, ad, bad, idx)
+        assert pq.stream_status() == pq._lib.SQ_ERR_RANGE
+        assert torch.equal(out, want) and torch.equal(out[rows], y[rows])
+
+
 def test_empty_batches():
     x, y, ad, _ = make(20, 128, 64, 2, 8)
     none = torch.zeros(0, dtype=torch.int32, device="cuda")
