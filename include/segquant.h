@@ -388,8 +388,10 @@ typedef struct {
  * (below 0: none); bounds: device int32 [requests + 1], not decreasing, within
  * [0, M]; index: device int32 [requests].  An adapter may serve any number of
  * requests.  A request with bounds outside the batch or an index >= L is left out
- * and sets SQ_ERR_RANGE in the status word; falling bounds set it too, and which
- * rows then receive their term is unspecified (no access leaves the tensors).
+ * by every kernel of a call (its rows in the batch are rows without an adapter) and
+ * sets SQ_ERR_RANGE in the status word; falling bounds set it too, and which rows then
+ * receive their term, and all that a call writes, is unspecified (no access leaves the
+ * tensors).
  *   y[m, :] += scale_l * B_l (A_l x[m, :])   for the rows of requests with an adapter;
  * all other rows of y are neither read nor written.  x: [M, K], y: [M, N]; products
  * are exact, sums in fp32, one rounding to y's type.  hidden: fp32 [M, R] or NULL,

@@ -46,14 +46,19 @@ struct AdapterItem {
 // floor(start_r / T) + r, which leaves room for a request of any length before the
 // next one's, so its own bounds alone place them and a 32-way search finds the
 // request of a slot.  adapter_slots() slots hold every piece in both.
-// Pieces of a request with bounds outside the batch or an index beyond the adapters
-// are left out, so no read or write leaves the tensors; check_requests raises the
-// range status for them.  Slots are counted over the bounds cut to the batch, so such a
-// request has no more of them than its rows in it and takes none of another one's.
+// The bounds are cut to the batch, so no read or write leaves the tensors.  A request that
+// request_counts() leaves out keeps its rows in the batch, without an adapter;
+// check_requests raises the range status for it.
 constexpr int kLaneRequests = 8, kExactRequests = 32 * kLaneRequests - 2;
 __host__ __device__ inline int64_t adapter_slots(int M, int Q, int T) {
   // pieces: every T rows of the batch end at most one, and so does every request's end
   return T == 1 && Q <= kExactRequests ? M : (int64_t)M / T + Q + 3;
+}
+// Whether a request with the bounds s, e and the adapter l counts: not with bounds outside
+// the batch or an unknown adapter.  The kernels of a call have to agree on it: what the
+// gradients' kernel sums over a request's rows, the one before it has written.
+__device__ __forceinline__ bool request_counts(int s, int e, int l, int M, int L) {
+  return s >= 0 && e <= M && l < L;
 }
 __device__ __forceinline__ AdapterItem adapter_item(const AdapterArgs& p, int slot, int T) {
   const int lane = threadIdx.x & 31;
@@ -111,11 +116,12 @@ __device__ __forceinline__ AdapterItem adapter_item(const AdapterArgs& p, int sl
   }
   if (lo >= count) return it;
   const int s = start(lo), e = start(lo + 1);
-  const bool request = lo > 0 && lo <= p.Q;
-  if (request) it.l = __ldg(p.index + lo - 1);
   // (of falling bounds the search may bring any piece)
   if (e < s || piece < 0 || piece > (e - s) / T) return it;
-  if (request && (__ldg(p.bounds + lo - 1) < 0 || __ldg(p.bounds + lo) > p.M || it.l >= p.L)) return it;
+  if (lo > 0 && lo <= p.Q) {
+    const int l = __ldg(p.index + lo - 1);
+    if (request_counts(__ldg(p.bounds + lo - 1), __ldg(p.bounds + lo), l, p.M, p.L)) it.l = l;
+  }
   it.row = s + piece * T;
   it.n = min(T, e - it.row);
   return it;
@@ -486,7 +492,7 @@ constexpr int kGradPiece = 64;
 struct GradPieces {
   const int32_t* bounds;
   const int32_t* index;
-  int M, Q, l, rank, cs;
+  int M, L, Q, l, rank, cs;
   int base = -32, pos = 0, end = 0, s = 0, e = 0, turn = 0;
   unsigned mask = 0;
   __device__ __forceinline__ bool next(int& m0, int& n) {
@@ -498,9 +504,9 @@ struct GradPieces {
         const int q = base + lane;
         bool hit = false;
         if (q < Q && __ldg(index + q) == l) {
-          s = max(0, __ldg(bounds + q));
-          e = min(M, __ldg(bounds + q + 1));
-          hit = s < e;
+          s = __ldg(bounds + q);
+          e = __ldg(bounds + q + 1);
+          hit = s < e && request_counts(s, e, l, M, L);
         }
         mask = __ballot_sync(0xffffffffu, hit);
       }
@@ -598,7 +604,7 @@ __device__ __forceinline__ void adapter_grad_tile(const AdapterGradArgs& p, int 
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
-  GradPieces pieces{p.bounds, p.index, p.M, p.Q, l, rank, p.cs};
+  GradPieces pieces{p.bounds, p.index, p.M, p.L, p.Q, l, rank, p.cs};
   const int R4 = p.R / 4;
   int first, count;
   bool more = pieces.mine(first, count);

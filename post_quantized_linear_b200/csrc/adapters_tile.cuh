@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kTileThreads, adapter_grad_ctas(RB))
   const uint32_t tmem = *tmem_slot;
 
   grid_dep_wait();
-  GradPieces pieces{p.bounds, p.index, p.M, p.Q, l, rank, cs};
+  GradPieces pieces{p.bounds, p.index, p.M, p.L, p.Q, l, rank, cs};
   int m0, n, i = 0;
   bool ok = true;
   if (warp == 0) {

@@ -364,6 +364,48 @@ def test_a_bound_far_outside_the_batch_costs_no_other_request(lengths, dtype):
         assert torch.equal(out, want) and torch.equal(out[rows], y[rows])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=str)
+@pytest.mark.parametrize("lengths", [[50, 50], [100, 30, 70, 100], [1] * 60, [9] * 400],
+                         ids=lambda v: f"{len(v)} requests")
+def test_requests_left_out_of_the_gradients(lengths, dtype):
+    """A request with a bound outside the batch or an unknown adapter, beside good ones of the
+    same adapter: its rows of hidden and dx are zeros, and the gradients are those of the other
+    requests alone, whatever the workspace and its rows of hidden held before."""
+    M, K, N, R = sum(lengths), 128, 64, 24
+    x, dy, ad, _ = make(M, K, N, 2, R, dtype, seed=M)
+    n = len(lengths)
+    bounds, idx = requests(lengths, [1] * n)
+    first, last = slice(0, lengths[0]), slice(M - lengths[-1], M)
+    nan = float("nan")
+    for what, at, value, rows in (("bound", 0, -3, first), ("bound", n, M + 200, last), ("index", n - 1, 2, last),
+                                  ("index", 0, 2 ** 31 - 1, first)):
+        good, bad_b, bad_i = idx.clone(), bounds.clone(), idx.clone()
+        good[0 if rows is first else -1] = -1
+        (bad_b if what == "bound" else bad_i)[at] = value
+        _, hidden = pq.adapter_add(torch.zeros_like(dy), x, ad, bounds, good, return_hidden=True)
+        want = pq.adapter_backward(dy, x, hidden, ad, bounds, good)
+        # the C entries, so that every buffer can hold NaN before the calls
+        lib = pq._lib.load()
+        h = torch.full((M, R), nan, device="cuda")
+        dx = torch.full((M, K), nan, device="cuda", dtype=dtype)
+        da, db = torch.full_like(want[1], nan), torch.full_like(want[2], nan)
+        wn = pq._adapter_workspace_size(M, R)
+        ws = torch.full((wn // 4,), nan, device="cuda")
+        t, c = pq._dtype_code(dtype), ad.c_struct()
+        s = torch.cuda.current_stream().cuda_stream
+        assert lib.sq_adapter_add(x.data_ptr(), t, M, K, c, bad_b.data_ptr(), bad_i.data_ptr(), n,
+                                  torch.zeros_like(dy).data_ptr(), t, N, h.data_ptr(), s) == 0
+        assert pq.stream_status() == pq._lib.SQ_ERR_RANGE
+        assert torch.equal(h, hidden) and (h[rows] == 0).all()
+        h[rows] = nan
+        assert lib.sq_adapter_backward(dy.data_ptr(), t, M, N, x.data_ptr(), t, K, h.data_ptr(), c, bad_b.data_ptr(),
+                                       bad_i.data_ptr(), n, dx.data_ptr(), K, da.data_ptr(), db.data_ptr(),
+                                       ws.data_ptr(), wn, s) == 0
+        assert pq.stream_status() == pq._lib.SQ_ERR_RANGE
+        assert (dx[rows] == 0).all()
+        assert torch.equal(dx, want[0]) and torch.equal(da, want[1]) and torch.equal(db, want[2])
+
+
 def test_empty_batches():
     x, y, ad, _ = make(20, 128, 64, 2, 8)
     none = torch.zeros(0, dtype=torch.int32, device="cuda")
