@@ -600,7 +600,7 @@ def quantize_activations_norm(x: torch.Tensor, groups: int, gamma: Optional[torc
     else:
         qp, qn = out
         for t, name in ((qp, "q_pos"), (qn, "q_neg")):
-            _check_rows(t, B * S, C, name)
+            _same_device(_check_rows(t, B * S, C, name)[0])
             if t.dtype != torch.int8:
                 raise ValueError(f"{name} must be int8")
         if qp.stride(0) != qn.stride(0):

@@ -161,6 +161,48 @@ def test_adapter_backward_refusals():
     assert L.load().sq_adapter_backward_workspace_size(-1, 16, ctypes.byref(n)) == L.SQ_ERR_INVALID_ARG
 
 
+class OtherTensor:
+    """What the binding asks of a tensor, for checks that need a second device."""
+
+    def __init__(self, shape, dtype, device):
+        import torch
+        self.shape, self.dtype, self.index, self.is_cuda, self.device = torch.Size(shape), dtype, device, True, device
+        self.strides = [1]
+        for n in reversed(shape[1:]):
+            self.strides.insert(0, self.strides[0] * n)
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        return tuple(self.strides) if i is None else self.strides[i]
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.shape.numel()
+
+    def data_ptr(self):
+        raise AssertionError("a call went past its checks")
+
+
+def test_binding_refuses_codes_on_another_device(monkeypatch):
+    torch = pytest.importorskip("torch")
+    import post_quantized_linear_b200 as pq
+    monkeypatch.setattr(pq, "_current_device", lambda: 0)
+    x, scale = OtherTensor((2, 9, 64), torch.bfloat16, 0), OtherTensor((1,), torch.float32, 0)
+    here, there = (OtherTensor((18, 64), torch.int8, d) for d in (0, 1))
+    for out in ((there, there), (here, there), (there, here)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            pq.quantize_activations_norm(x, 8, None, None, (0, 64), scale, scale, out=out)
+    with pytest.raises(AssertionError, match="past its checks"):
+        pq.quantize_activations_norm(x, 8, None, None, (0, 64), scale, scale, out=(here, here))
+
+
 def test_binding_refuses_wrong_tensors():
     """The binding's own checks, on CPU tensors."""
     torch = pytest.importorskip("torch")
