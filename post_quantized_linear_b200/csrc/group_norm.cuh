@@ -90,10 +90,6 @@ struct NormBwdArgs {
 };
 
 // ------------------------------------------------------------ vector access
-template <typename T>
-__device__ __forceinline__ uint4 load_stream(const T* p) {
-  return __ldcs(reinterpret_cast<const uint4*>(p));
-}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
