@@ -13,6 +13,7 @@ own scales (Spanish technical summary 2.A).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import functools
@@ -474,6 +475,10 @@ def linear_from_codes_hadamard(q_pos: torch.Tensor, q_neg: torch.Tensor, qw: Qua
 # The norm in front of the quantized layers of a U-Net or an image decoder,
 # channels last: maps are [B, S, C] with S = H*W (for an NCHW tensor in the
 # channels_last memory format, ``t.permute(0, 2, 3, 1).flatten(1, 2)``).
+#
+# These calls and the adapters' allocate their results in the order of ``stream``
+# where one is given: another stream that reads them has to wait for it, and
+# calls ``record_stream`` on what it may still read after the last reference is gone.
 
 _NORM_ACTS = {"none": 0, "silu": _lib.SQ_ACT_SILU, "gelu": _lib.SQ_ACT_GELU}
 # the current device's index without the lazy-initialization check; the public call where it is missing
@@ -538,12 +543,13 @@ def _norm_workspace_size(device: int, B: int, S: int, C: int, groups: int, xt: i
 _segments_of = functools.lru_cache(maxsize=256)(_lib.segments)   # of a tuple of ints, never changed
 
 
-def _workspace(n: int, device, stream):
-    """A workspace of n bytes in ``stream``'s order (None: the current stream's)."""
-    if stream is None:
-        return torch.empty(n, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(n, dtype=torch.uint8, device=device)
+_NO_STREAM = contextlib.nullcontext()
+
+
+def _in_order(stream):
+    """Context for what a call allocates: memory in ``stream``'s order (None: the current
+    stream's), since a block that was freed in another one may still be in use there."""
+    return _NO_STREAM if stream is None else torch.cuda.stream(stream)
 
 
 def group_norm_act(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = None,
@@ -558,18 +564,20 @@ def group_norm_act(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] =
     shape = x.shape
     B, S, C = shape
     if out is None:
-        if (out_dtype is None or out_dtype is x.dtype) and x.is_contiguous():
-            out = torch.empty_like(x)
-        else:
-            out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
         ldy, ybs, dy = C, S * C, dev
     else:
         dy, ldy, ybs = _map(out, "out", shape)
     _same_device(dev, dy)
     xt = _dtype_code(x.dtype)
-    stats = x.new_empty((B, groups, 2), dtype=torch.float32) if return_stats else None
     wn = _norm_workspace_size(dev, B, S, C, groups, xt, 0)
-    ws = _workspace(wn, x.device, stream) if wn else None
+    with _in_order(stream):
+        if out is None:
+            if (out_dtype is None or out_dtype is x.dtype) and x.is_contiguous():
+                out = torch.empty_like(x)
+            else:
+                out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+        stats = x.new_empty((B, groups, 2), dtype=torch.float32) if return_stats else None
+        ws = x.new_empty(wn, dtype=torch.uint8) if wn else None
     st = _lib.load().sq_group_norm_act(
         x.data_ptr(), xt, B, S, C, ldx, xbs, groups, _check_f32(gamma, (C,), "gamma", dev),
         _check_f32(beta, (C,), "beta", dev), eps, _norm_act_code(act), out.data_ptr(),
@@ -593,11 +601,7 @@ def quantize_activations_norm(x: torch.Tensor, groups: int, gamma: Optional[torc
     J = len(kseg) - 1
     _same_device(dev)
     ldq = (C + 15) // 16 * 16
-    if out is None:
-        qp, qn = x.new_empty((2, B * S, ldq), dtype=torch.int8).unbind()
-        if ldq != C:
-            qp, qn = qp[:, :C], qn[:, :C]
-    else:
+    if out is not None:
         qp, qn = out
         for t, name in ((qp, "q_pos"), (qn, "q_neg")):
             _same_device(_check_rows(t, B * S, C, name)[0])
@@ -607,11 +611,16 @@ def quantize_activations_norm(x: torch.Tensor, groups: int, gamma: Optional[torc
             raise ValueError("q_pos and q_neg must share a row stride")
         if B * S > 1:
             ldq = qp.stride(0)
-    y = x.new_empty((B * S, C), dtype=torch.bfloat16) if return_y else None
     seg, keep = _segments_of(tuple(map(int, kseg)))
     xt = _dtype_code(x.dtype)
     wn = _norm_workspace_size(dev, B, S, C, groups, xt, 0)
-    ws = _workspace(wn, x.device, stream) if wn else None
+    with _in_order(stream):
+        if out is None:
+            qp, qn = x.new_empty((2, B * S, ldq), dtype=torch.int8).unbind()
+            if ldq != C:
+                qp, qn = qp[:, :C], qn[:, :C]
+        y = x.new_empty((B * S, C), dtype=torch.bfloat16) if return_y else None
+        ws = x.new_empty(wn, dtype=torch.uint8) if wn else None
     st = _lib.load().sq_quantize_activations_norm(
         x.data_ptr(), xt, B, S, C, ldx, xbs, groups, _check_f32(gamma, (C,), "gamma", dev),
         _check_f32(beta, (C,), "beta", dev), eps, _norm_act_code(act), ctypes.byref(seg),
@@ -637,17 +646,19 @@ def group_norm_act_backward(dy: torch.Tensor, x: torch.Tensor, stats: torch.Tens
         raise ValueError("stats must be the [B, groups, 2] tensor of the forward call")
     groups = stats.shape[1]
     if dx is None:
-        dx = torch.empty_like(x) if x.is_contiguous() else torch.empty(shape, dtype=x.dtype, device=x.device)
         d3, lddx, dxbs = dev, C, S * C
     else:
         d3, lddx, dxbs = _map(dx, "dx", shape)
-    if dy.dtype != x.dtype or dx.dtype != x.dtype:
+    if dy.dtype != x.dtype or (dx is not None and dx.dtype != x.dtype):
         raise TypeError("dy and dx must have x's dtype")
     _same_device(dev, d2, d3)
-    grads = x.new_empty((2, C), dtype=torch.float32)
     xt = _dtype_code(x.dtype)
     wn = _norm_workspace_size(dev, B, S, C, groups, xt, 1)
-    ws = _workspace(wn, x.device, stream) if wn else None
+    with _in_order(stream):
+        if dx is None:
+            dx = torch.empty_like(x) if x.is_contiguous() else torch.empty(shape, dtype=x.dtype, device=x.device)
+        grads = x.new_empty((2, C), dtype=torch.float32)
+        ws = x.new_empty(wn, dtype=torch.uint8) if wn else None
     g = grads.data_ptr()
     st = _lib.load().sq_group_norm_act_backward(
         dy.data_ptr(), lddy, dybs, x.data_ptr(), xt, B, S, C, ldx, xbs, groups,
@@ -734,7 +745,8 @@ def adapter_add(y: torch.Tensor, x: torch.Tensor, adapters: Adapters, bounds: to
     dy, ldy = _check_rows(y, M, c.N, "y")
     if dx != dev or dy != dev:
         raise ValueError("x and y must be on the current CUDA device")
-    hidden = x.new_empty((M, c.R), dtype=torch.float32) if return_hidden else None
+    with _in_order(stream):
+        hidden = x.new_empty((M, c.R), dtype=torch.float32) if return_hidden else None
     st = _lib.load().sq_adapter_add(
         x.data_ptr(), _dtype_code(x.dtype), M, ldx, c, bounds.data_ptr(), index.data_ptr(), n, y.data_ptr(),
         _dtype_code(y.dtype), ldy, None if hidden is None else hidden.data_ptr(), _stream_ptr(stream, dev))
@@ -755,11 +767,12 @@ def adapter_backward(dy: torch.Tensor, x: torch.Tensor, hidden: torch.Tensor, ad
     d2, lddy = _check_rows(dy, M, N, "dy")
     if d1 != dev or d2 != dev:
         raise ValueError("x and dy must be on the current CUDA device")
-    dx = x.new_empty((M, K))
-    da = x.new_empty((L, R, K), dtype=torch.float32)
-    db = x.new_empty((L, N, R), dtype=torch.float32)
     wn = _adapter_workspace_size(M, R)
-    ws = _workspace(wn, x.device, stream)
+    with _in_order(stream):
+        dx = x.new_empty((M, K))
+        da = x.new_empty((L, R, K), dtype=torch.float32)
+        db = x.new_empty((L, N, R), dtype=torch.float32)
+        ws = x.new_empty(wn, dtype=torch.uint8)
     st = _lib.load().sq_adapter_backward(
         dy.data_ptr(), _dtype_code(dy.dtype), M, lddy, x.data_ptr(), _dtype_code(x.dtype), ldx,
         _check_f32(hidden, (M, R), "hidden", dev), c, bounds.data_ptr(), index.data_ptr(), n,

@@ -306,6 +306,52 @@ def test_other_stream_and_graph_replay():
         assert all(torch.equal(a, b) for a, b in zip(gr, want_g))
 
 
+def calls_with_results():
+    """Calls of every entry point that allocates: name -> (f(stream) -> results)."""
+    x, gamma, beta, g = make(2, 300, 320, BF, seed=33)
+    big, _, _, _ = make(1, 70000, 64, BF, seed=34)         # two passes: a workspace, too
+    dy = torch.randn(2, 300, 320, generator=g, device="cuda").to(BF)
+    _, stats = pq.group_norm_act(x, 32, gamma, beta, act="silu", return_stats=True)
+    scale = torch.full((1,), 0.05, device="cuda")
+    rows, out = x.view(600, 320), torch.randn(600, 256, generator=g, device="cuda").to(BF)
+    ad = pq.Adapters((torch.randn(2, 16, 320, generator=g, device="cuda") / 18).to(BF),
+                     (torch.randn(2, 256, 16, generator=g, device="cuda") / 4).to(BF))
+    bounds = torch.tensor([0, 200, 600], dtype=torch.int32, device="cuda")
+    index = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    _, hidden = pq.adapter_add(out.clone(), rows, ad, bounds, index, return_hidden=True)
+    return {
+        "norm": lambda s: pq.group_norm_act(x, 32, gamma, beta, act="silu", return_stats=True, stream=s),
+        "norm of a large map": lambda s: (pq.group_norm_act(big, 8, act="gelu", stream=s),),
+        "norm to fp32": lambda s: (pq.group_norm_act(x, 32, out_dtype=F32, stream=s),),
+        "codes": lambda s: pq.quantize_activations_norm(x, 32, gamma, beta, (0, 320), scale, scale, return_y=True,
+                                                        stream=s),
+        "norm gradients": lambda s: pq.group_norm_act_backward(dy, x, stats, gamma, beta, act="silu", stream=s),
+        "hidden": lambda s: pq.adapter_add(torch.zeros_like(out), rows, ad, bounds, index, return_hidden=True,
+                                           stream=s)[1:],
+        "adapter gradients": lambda s: pq.adapter_backward(out, rows, hidden, ad, bounds, index, stream=s),
+    }
+
+
+@pytest.mark.parametrize("name", ["norm", "norm of a large map", "norm to fp32", "codes", "norm gradients", "hidden",
+                                  "adapter gradients"])
+def test_results_on_an_explicit_stream_take_no_block_in_use(name):
+    """Blocks that were freed on the current stream while its kernels still wait to write them
+    are not given to a call on another stream, which would run ahead of those kernels."""
+    f = calls_with_results()[name]
+    want = [t.clone() for t in f(None)]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    s.wait_stream(torch.cuda.current_stream())
+    blocks = [torch.empty_like(t) for t in want for _ in range(2)]
+    torch.cuda._sleep(100_000_000)                         # about 50 ms
+    for b in blocks:
+        b.fill_(77)
+    del blocks, b
+    got = f(s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_empty_maps():
     for shape in ((0, 5, 64), (2, 0, 64)):
         x = torch.empty(shape, device="cuda", dtype=BF)
