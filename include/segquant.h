@@ -394,7 +394,11 @@ typedef struct {
  * tensors).
  *   y[m, :] += scale_l * B_l (A_l x[m, :])   for the rows of requests with an adapter;
  * all other rows of y are neither read nor written.  x: [M, K], y: [M, N]; products
- * are exact, sums in fp32, one rounding to y's type.  hidden: fp32 [M, R] or NULL,
+ * are exact, sums in fp32 (tensor-core sums in chains of 32 steps at most: within 2^-18 of the sum
+ * of the absolute terms); A_l x, fp32, is multiplied as it is or, on the tensor cores, as
+ * two bf16 parts where y is bf16 (within 2^-17 of it) and three where y is fp32
+ * (2^-24); one rounding to y's type.  Infinities and NaN of a row or an adapter give
+ * non-finite values in that row or that adapter's requests, nowhere else.  hidden: fp32 [M, R] or NULL,
  * receives A_l x (zeros in rows without an adapter) for the backward call.
  * M = 0 is a no-op; M <= 2^30, requests <= 2^24 (SQ_ERR_RANGE).  y must not overlap x. */
 sq_status sq_adapter_add(const void* x, sq_dtype xt, int64_t M, int64_t ldx,

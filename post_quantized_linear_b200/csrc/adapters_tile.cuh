@@ -94,6 +94,11 @@ constexpr int kTileEpiWarps = 8;
 constexpr int kTileX = kTileRows * 128;    // bytes of a 128-row, 128-byte-wide tile
 constexpr int kTileBars = 512;             // bytes of barriers and flags
 constexpr int kTileStages = 8;             // most slots of the ring
+// The tensor core cuts its fp32 sums towards zero at every step, a bias that grows with the
+// chain (1.4e-6 of the sum after 16 blocks of 64, where fp32 additions have 5e-7): after
+// kChain blocks along the contracted axis the sums move to registers and are added there,
+// while the next chain runs in a second accumulator.
+constexpr int kChain = 8;
 
 struct AdapterTileArgs {
   AdapterArgs p;
@@ -122,7 +127,7 @@ __host__ __device__ inline int adapter_h_bytes(int rp, int parts) {
 // of the columns, in tiles 128 bytes wide.  Backward: u = scale dy B, dx = u A, the
 // same steps with both weights MN-major.  RB: the largest rank (64 or 128).
 //
-// h is fp32 in TMEM; as an operand it is the sum of `parts` bf16 values (two for
+// h is summed in TMEM in chains of kChain blocks, which meet in fp32 registers; as an operand it is the sum of `parts` bf16 values (two for
 // bf16 outputs: off by 2^-17 of h, against the output's own 2^-8; three for fp32
 // outputs: exact to 2^-24), which costs R/2 more multiply-adds per output and no
 // bytes.
@@ -138,7 +143,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
                         const __grid_constant__ AdapterTileArgs args) {
   constexpr int ES = sizeof(YT);
   constexpr int BN = 128 / ES;             // columns of an output tile
-  constexpr int D2 = RB;                   // TMEM column of the output accumulators,
+  constexpr int D2 = RB;                   // TMEM column of the second accumulator of h, and of the outputs,
   constexpr int ND = RB == 64 ? 3 : 2;     // and how many tiles of them there are room for
   const AdapterArgs& p = args.p;
   extern __shared__ uint8_t smem_raw[];
@@ -172,8 +177,9 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
   uint64_t* empty3 = empty1 + kTileStages;     // [kTileStages] forward, second product: its tile of y is read
   uint64_t* d_full = empty3 + kTileStages;     // [3]
   uint64_t* d_empty = d_full + 3;    // [3]
-  uint64_t* h_full = d_empty + 3;
-  uint64_t* h_ready = h_full + 1;
+  uint64_t* h_full = d_empty + 3;    // [2] a chain of h is complete
+  uint64_t* h_free = h_full + 2;     // [2] and read
+  uint64_t* h_ready = h_free + 2;
   uint64_t* p_full = h_ready + 1;    // every CTA's partial h is written
   uint64_t* p_free = p_full + 1;     // every CTA has read this one's
   uint64_t* drain_bar = p_free + 1;
@@ -190,7 +196,10 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
       mbar_init(smem_u32(d_full + i), 1);
       mbar_init(smem_u32(d_empty + i), kTileEpiWarps);
     }
-    mbar_init(smem_u32(h_full), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(h_full + i), 1);
+      mbar_init(smem_u32(h_free + i), kTileEpiWarps);
+    }
     mbar_init(smem_u32(h_ready), kTileEpiWarps * cs);
     mbar_init(smem_u32(p_full), kTileEpiWarps * cs);
     mbar_init(smem_u32(p_free), kTileEpiWarps * cs);
@@ -263,18 +272,23 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
       bool ok = true;
       const uint32_t id1 = idesc_bf16(kTileRows, RP) | (BWD ? kIdescBMn : 0u);
       for (int i = 0; i < nk; ++i) {
-        const int s = i % NS;
+        const int s = i % NS, chain = i / kChain, b = chain & 1;
+        const bool first = i % kChain == 0;
+        if (first && chain >= 2) {
+          if (!(ok = wait1(smem_u32(h_free + b), (chain / 2 - 1) & 1, abort_flag, budget))) break;
+          tc_fence_after();
+        }
         if (!(ok = wait1(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
         const uint32_t st = smem_u32(smem + s * args.slot_bytes), wt = st + kTileX;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          umma_bf16(tmem, smem_desc_k_sw128(st + ks * 32),
+          umma_bf16(tmem + b * D2, smem_desc_k_sw128(st + ks * 32),
                     BWD ? smem_desc_mn_sw128(wt + ks * 2048, 8192) : smem_desc_k_sw128(wt + ks * 32), id1,
-                    (i > 0 || ks > 0) ? 1u : 0u);
+                    (!first || ks > 0) ? 1u : 0u);
         umma_commit(smem_u32(empty1 + s));
+        if (i == nk - 1 || (i + 1) % kChain == 0) umma_commit(smem_u32(h_full + b));
       }
       if (ok) {
-        umma_commit(smem_u32(h_full));
         ok = wait1s<true>(smem_u32(h_ready), 0, abort_flag, budget);
         fence_proxy_async_all();
         tc_fence_after();
@@ -309,23 +323,34 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
     const int row = quad * 32 + lane;
     const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
     const int hc = RP / 2, c0 = half * hc;    // this thread's columns of the partial h
-    bool ok = wait_warp(smem_u32(h_full), 0, abort_flag, budget);
-    if (ok) {
+    // 1. this CTA's share of h: its chains added up, into its own shared memory
+    float t[RB / 2];
+#pragma unroll
+    for (int c = 0; c < RB / 2; ++c) t[c] = 0.0f;
+    bool ok = true;
+    for (int chain = 0; chain * kChain < nk; ++chain) {
+      const int b = chain & 1;
+      if (!(ok = wait_warp(smem_u32(h_full + b), (chain / 2) & 1, abort_flag, budget))) break;
       tc_fence_after();
-      // 1. this CTA's share of h, into its own shared memory
-      const int pitch = RP + 4;
-      float* mine = reinterpret_cast<float*>(hbuf) + row * pitch + c0;
 #pragma unroll
       for (int c = 0; c < RB / 2; c += 8) {
         if (c < hc) {
           uint32_t u[8];
-          tmem_ld8(t_lane + c0 + c, u);
+          tmem_ld8(t_lane + b * D2 + c0 + c, u);
           tmem_wait_ld();
-          *reinterpret_cast<uint4*>(mine + c) = make_uint4(u[0], u[1], u[2], u[3]);
-          *reinterpret_cast<uint4*>(mine + c + 4) = make_uint4(u[4], u[5], u[6], u[7]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) t[c + k] += __uint_as_float(u[k]);
         }
       }
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(h_free + b));
+    }
+    if (ok) {
+      float* mine = reinterpret_cast<float*>(hbuf) + row * (RP + 4) + c0;
+#pragma unroll
+      for (int c = 0; c < RB / 2; c += 4)
+        if (c < hc) *reinterpret_cast<float4*>(mine + c) = make_float4(t[c], t[c + 1], t[c + 2], t[c + 3]);
       __syncwarp();
       if (lane < cs) mbar_arrive_remote(mapa_shared(smem_u32(p_full), lane));
       ok = wait_warp<true>(smem_u32(p_full), 0, abort_flag, budget);
@@ -516,9 +541,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
 // f (u or h) comes as three bf16 parts side by side along the rank axis (exact to
 // 2^-24, since the sums are fp32 results), g (x or dy) as it is; both operands are
 // MN-major, so TMA brings them as they lie in memory.
-// The tensor core cuts its fp32 sums towards zero at every step, a bias that grows
-// with the chain (1.4e-6 of the sum after 16 pieces, where fp32 additions have 5e-7):
-// after kGradChain pieces the sums move to registers and are added there.
+// The sums move to registers after chains of kChain pieces.
 // 8192 rows, 4608 and 1152 columns, rank 16, 4 adapters (96 MB): 26 us, 3.7 TB/s, bound by the
 // one thread that issues a CTA's products, 0.7 us a piece.
 struct AdapterGradTileArgs {
@@ -533,7 +556,6 @@ struct AdapterGradTileArgs {
   long long wait_budget;
   int32_t starve;
 };
-constexpr int kGradChain = 8;
 __host__ __device__ inline int adapter_grad_atoms(int rp) { return (3 * rp + 63) / 64; }   // 64 ranks wide
 
 // RB: the largest rank (32, 64, 128); CTAs per SM 3, 2, 1, by their sums' registers and
@@ -638,7 +660,7 @@ __global__ void __launch_bounds__(kTileThreads, adapter_grad_ctas(RB))
       uint32_t phase = 0;
       bool last = false;
       while (!last) {
-        const bool first = i % kGradChain == 0;
+        const bool first = i % kChain == 0;
         if (first && chain >= NB && !(ok = wait1(smem_u32(d_empty + b), (chain / NB - 1) & 1, abort_flag, budget))) break;
         if (!(ok = wait1(smem_u32(full + s), phase, abort_flag, budget))) break;
         const int what = note[s];
@@ -661,9 +683,9 @@ __global__ void __launch_bounds__(kTileThreads, adapter_grad_ctas(RB))
         }
         ++i;
         umma_commit(smem_u32(empty + s));
-        if (last || i % kGradChain == 0) umma_commit(smem_u32(d_full + b));
+        if (last || i % kChain == 0) umma_commit(smem_u32(d_full + b));
         if (++s == NS) { s = 0; phase ^= 1; }
-        if (i % kGradChain == 0) { ++chain; b = chain % NB; }
+        if (i % kChain == 0) { ++chain; b = chain % NB; }
       }
       if (i > 0)                   // every product has landed when the last commit has
         wait_drain(smem_u32(empty + (i - 1) % NS), ((i - 1) / NS) & 1, kDrainBudget);
@@ -697,7 +719,7 @@ __global__ void __launch_bounds__(kTileThreads, adapter_grad_ctas(RB))
       }
       more = pieces.mine(m0, n);
       ++i;
-      if (!more || i % kGradChain == 0) {
+      if (!more || i % kChain == 0) {
         const int b = chain % NB;
         if (!(ok = wait_warp(smem_u32(d_full + b), (chain / NB) & 1, abort_flag, budget))) break;
         tc_fence_after();

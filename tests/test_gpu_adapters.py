@@ -406,6 +406,34 @@ def test_requests_left_out_of_the_gradients(lengths, dtype):
         assert torch.equal(dx, want[0]) and torch.equal(da, want[1]) and torch.equal(db, want[2])
 
 
+@pytest.mark.parametrize("R", [16, 128])
+def test_long_sums_of_one_sign_have_no_bias(R):
+    """16384 positive terms a sum.  A chain of 32 matrix steps cut towards zero loses at most
+    one unit of its last place (2^-23) a step, of a partial sum that grows evenly:
+    2^-23 * 16.5 < 2^-18.9 of the sum; 32 chains added in fp32 are off by 32 * 2^-24 = 2^-19 at
+    most: 2^-18 together.  The second product and the row's gradients run in at most 24 steps,
+    2^-23 * 12.5 < 2^-19 more (2^-18 with their own roundings)."""
+    g = torch.Generator(device="cuda").manual_seed(R)
+    pos = lambda *s: (0.5 + torch.rand(*s, generator=g, device="cuda")).to(BF)  # noqa: E731
+    M, D, E = 300, 16384, 32
+    bounds, idx = requests([130, 170], [1, 0])
+    wide, narrow = pos(2, R, D), pos(2, E, R)
+    x = pos(M, D)
+    y, ad = torch.zeros(M, E, device="cuda"), pq.Adapters(wide, narrow)
+    (ref, hid), _ = forward64(y, x, ad, bounds, idx)
+    _, hidden = pq.adapter_add(y, x, ad, bounds, idx, return_hidden=True)
+    assert ((hidden.double() / hid - 1).abs() <= 2.0 ** -18).all()
+    assert ((y.double() / ref - 1).abs() <= 2.0 ** -17).all()
+    # u = dy B over the long axis, then da = u^T x
+    ad = pq.Adapters(narrow.transpose(1, 2).contiguous(), wide.transpose(1, 2).contiguous())
+    dy, x = x, pos(M, E)
+    h = x.float() @ narrow[0].float()
+    (_, da, db), _ = backward64(dy, x, h, ad, bounds, idx)
+    got = pq.adapter_backward(dy, x, h, ad, bounds, idx)
+    assert ((got[1].double() / da - 1).abs() <= 2.0 ** -17).all()
+    assert ((got[2].double() / db - 1).abs() <= 2.0 ** -18).all()
+
+
 def test_empty_batches():
     x, y, ad, _ = make(20, 128, 64, 2, 8)
     none = torch.zeros(0, dtype=torch.int32, device="cuda")
