@@ -440,30 +440,23 @@ struct NormOut {
     float v[VN];
     unpack_pairs<VN>(x, v);
     if constexpr (OUT == OUT_CODES || OUT == OUT_CODES_BF16) {
-      // The codes are those of the bf16 values that y holds: of either sign in one byte
-      // (the scale picked by the sign, one fma that rounds, one clamp), parted into q+ and
-      // q- by the bytes' sign bits.
-      uint32_t w[VN / 2], c4[VN / 4];
+      // The codes are those of the bf16 values that y holds, by the quantizer's own functions:
+      // the same codes for values that are not finite, too.
+      uint32_t w[VN / 2], qp[VN / 4], qn[VN / 4];
 #pragma unroll
       for (int i = 0; i < VN / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
 #pragma unroll
       for (int i = 0; i < VN / 4; ++i) {
-        uint32_t q[4];
+        uint32_t a[4], b[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t h = w[2 * i + k / 2];
           const float x1 = __uint_as_float(k & 1 ? h & 0xFFFF0000u : h << 16);
-          const float t = fmaf(x1, x1 >= 0.0f ? rp : rn, kMagic);
-          q[k] = __float_as_uint(fminf(fmaxf(t, kMagic - 127.0f), kMagic + 127.0f));
+          a[k] = code_pos(x1, rp);
+          b[k] = code_neg(x1, rn);
         }
-        c4[i] = pack4_low(q[0], q[1], q[2], q[3]);
-      }
-      uint32_t qp[VN / 4], qn[VN / 4];
-#pragma unroll
-      for (int i = 0; i < VN / 4; ++i) {
-        const uint32_t neg = ((c4[i] >> 7) & 0x01010101u) * 0xFFu;
-        qn[i] = c4[i] & neg;
-        qp[i] = c4[i] & ~neg;
+        qp[i] = pack4_low(a[0], a[1], a[2], a[3]);
+        qn[i] = pack4_low(b[0], b[1], b[2], b[3]);
       }
       if constexpr (VN == 8) {
         *reinterpret_cast<uint2*>(p.q_pos + q_at) = make_uint2(qp[0], qp[1]);

@@ -169,6 +169,26 @@ def test_codes_equal_the_quantizer_of_the_norm(shape, dtype, act):
     assert pq.stream_status() == 0
 
 
+@pytest.mark.parametrize("S", [37, 70001])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_codes_of_non_finite_values_equal_the_quantizer(dtype, S):
+    """Groups with NaN, values that overflow to infinities, and segments whose scales are zero:
+    the fused codes are those that the quantizer gives for the same bf16 values."""
+    x, gamma, beta, _ = make(1, S, 256, dtype, seed=S)
+    x[0, 5, 20], x[0, S - 1, 130] = float("nan"), float("inf")
+    gamma[64:80] = 3e38
+    gamma[192:208] = -3e38
+    y16 = pq.group_norm_act(x, 32, gamma, beta, out_dtype=BF).view(S, 256)
+    assert torch.isnan(y16).any() and (y16 == float("inf")).any() and (y16 == float("-inf")).any()
+    kseg = (0, 128, 256)
+    for sp, sn in (((0.05, 0.04), (0.03, 0.06)), ((0.0, 0.04), (0.03, 0.0)), ((0.05, 0.0), (0.0, 0.06)),
+                   ((0.0, 0.0), (0.0, 0.0))):
+        sp, sn = torch.tensor(sp, device="cuda"), torch.tensor(sn, device="cuda")
+        want = pq.quantize_activations(y16, kseg, sp, sn)
+        got = pq.quantize_activations_norm(x, 32, gamma, beta, kseg, sp, sn)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 # ------------------------------------------------------------------ gradients
 def slope64(z, act):
     if act == "silu":
