@@ -171,15 +171,18 @@ __device__ __forceinline__ float erfc_half(float z, float& e) {
 }
 
 // 1 / (1 + exp(-z)) of both values with one reciprocal, r = 1 / (a b): the special
-// function unit (four lanes a clock) bounds these loops.  Arguments below -43.6 are taken
-// as that (the sigmoid stays below 2^-63), which keeps a b finite.
+// function unit (four lanes a clock) bounds these loops.  a and b are the denominators
+// times 2^-63, so a b and r stay in the normal range down to z = -87.3; beyond, the
+// exponential is held just above 2^126, whose reciprocal counts as zero.
 __device__ __forceinline__ uint64_t sigmoid2(uint64_t z2) {
+  constexpr float scale = 1.0842022e-19f;      // 2^-63
   float a, b;
   f2_unpack(f2_mul(z2, f2_both(-kLog2e)), a, b);
-  const uint64_t d = f2_add(f2_pack(ex2_ftz(fminf(a, 63.0f)), ex2_ftz(fminf(b, 63.0f))), f2_both(1.0f));
+  const uint64_t d = f2_fma(f2_pack(ex2_ftz(fminf(a, 126.001f)), ex2_ftz(fminf(b, 126.001f))), f2_both(scale),
+                            f2_both(scale));
   f2_unpack(d, a, b);
   const float r = rcp_ftz(a * b);
-  return f2_pack(r * b, r * a);
+  return f2_mul_ftz(f2_pack(r * b, r * a), f2_both(scale));
 }
 
 // act(z) and act'(z).  The hardware's exponential and reciprocal (relative error about

@@ -291,6 +291,71 @@ def test_gradients_strided_in_place_and_defaults():
     assert dx is dyv and torch.equal(dyv, got[0])
 
 
+# --------------------------------------------------- the activations themselves
+# A map of zeros has z = beta exactly, and with mean 0, rstd 1 and dy = 1 at a single
+# position dbeta is the slope at beta: one value of z a channel.
+def activation_of(z, act, out_dtype=F32):
+    C = z.numel()
+    return pq.group_norm_act(torch.zeros(1, 1, C, device="cuda"), C // 8, None, z, act=act, out_dtype=out_dtype).view(C)
+
+
+def slope_of(z, act):
+    C = z.numel()
+    stats = torch.tensor([0.0, 1.0], device="cuda").expand(1, C // 8, 2).contiguous()
+    zero, one = torch.zeros(1, 1, C, device="cuda"), torch.ones(1, 1, C, device="cuda")
+    return pq.group_norm_act_backward(one, zero, stats, None, z, act=act)[2]
+
+
+def z_values(kind):
+    g = torch.Generator(device="cuda").manual_seed(7)
+    if kind == "normal":
+        return torch.randn(65536, generator=g, device="cuda")
+    if kind == "wide":
+        return torch.linspace(-13, 13, 65536, device="cuda")
+    return torch.linspace(-86, 86, 65536, device="cuda")
+
+
+@pytest.mark.parametrize("kind", ["normal", "wide", "far"])
+@pytest.mark.parametrize("act", ["silu"])
+def test_activations_keep_their_tails(act, kind):
+    """Relative to the value itself.  GELU below zero is |z| / 2 erfc: the exponential is off by
+    2^-22, t P(t) by 2^-23 (the reciprocal), 2^-22 (its sums) and 2^-26 (the fit), four products
+    by 2^-24 each, 2^-20 together, and the exponent z^2 / 2 by three roundings of 2^-24 (z^2, the
+    constant, their product), below z^2 2^-23; above zero |z| / 2 erfc is at most z.  SiLU: the
+    exponential by 2^-22 and |z| 2^-24 (its argument), the quotient by 2^-22, three products:
+    (|z| + 4) 2^-22 covers it.  bf16: half a step more.  The reference takes the tail from
+    erfc: 1 + erf, as ndtr has it, leaves nothing of it in 64 bits either."""
+    if act == "gelu" and kind == "far":
+        pytest.skip("beyond |z| = 13 the tail leaves the fp32 range")
+    z = z_values(kind)
+    zd = z.double()
+    if act == "gelu":
+        rel = 2.0 ** -20 + zd * zd * 2.0 ** -23
+        ref = 0.5 * zd * torch.special.erfc(-zd * math.sqrt(0.5))
+    else:
+        rel = (zd.abs() + 4) * 2.0 ** -22
+        ref = act64(zd, act)
+    y = activation_of(z, act)
+    assert ((y.double() - ref).abs() <= rel * ref.abs()).all()
+    y16 = activation_of(z, act, BF)
+    assert ((y16.double() - ref).abs() <= (half_step(BF) * (1 + rel) + rel) * ref.abs()).all()
+
+
+@pytest.mark.parametrize("kind", ["normal", "wide", "far"])
+@pytest.mark.parametrize("act", ["silu"])
+def test_slopes_of_the_activations(act, kind):
+    """Off by the errors of the two terms, each as in the test above, and their sum's rounding."""
+    z = z_values(kind)
+    zd = z.double()
+    p = torch.sigmoid(zd) if act == "silu" else torch.special.ndtr(zd)
+    second = zd * p * (1 - p) if act == "silu" else zd * torch.exp(-zd * zd / 2) / math.sqrt(2 * math.pi)
+    rel = 2.0 ** -20 + zd * zd * 2.0 ** -23 if act == "gelu" else (zd.abs() + 4) * 2.0 ** -22
+    if act == "gelu":
+        p = 0.5 * torch.special.erfc(-zd * math.sqrt(0.5))
+    s = slope_of(z, act)
+    assert ((s.double() - (p + second)).abs() <= rel * (p + second.abs()) + 1e-37).all()
+
+
 # ------------------------------------------------------------- streams, graphs
 def test_other_stream_and_graph_replay():
     x, gamma, beta, g = make(2, 300, 320, BF, seed=31)
