@@ -315,7 +315,8 @@ sq_status sq_linear_forward_codes_hadamard(const int8_t* q_pos, const int8_t* q_
  * C/groups; mean and (biased) variance over a group's S * C/groups values in
  * fp32; z = (x - mean) / sqrt(var + eps) * gamma[c] + beta[c] (gamma, beta: device
  * fp32 [C], NULL for 1 and 0); y = act(z), act 0 (none), SQ_ACT_SILU or SQ_ACT_GELU
- * (exact, erf-based), rounded once to the output type; SiLU is within (|z| + 4) 2^-22 of itself.
+ * (erf-based), evaluated in fp32, SiLU within (|z| + 4) 2^-22 of itself and GELU within
+ * 2^-20 + z^2 2^-23 (below zero of the tail itself), rounded once to the output type.
  * Requirements: C % 8 == 0 and C % groups == 0; the smallest block of whole
  * groups that is a multiple of 16 bytes wide at most 8192 bytes
  * (SQ_ERR_UNSUPPORTED); B <= 65535, S <= 2^30, C <= SQ_MAX_K (SQ_ERR_RANGE);

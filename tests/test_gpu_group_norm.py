@@ -316,7 +316,7 @@ def z_values(kind):
 
 
 @pytest.mark.parametrize("kind", ["normal", "wide", "far"])
-@pytest.mark.parametrize("act", ["silu"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_activations_keep_their_tails(act, kind):
     """Relative to the value itself.  GELU below zero is |z| / 2 erfc: the exponential is off by
     2^-22, t P(t) by 2^-23 (the reciprocal), 2^-22 (its sums) and 2^-26 (the fit), four products
@@ -342,7 +342,7 @@ def test_activations_keep_their_tails(act, kind):
 
 
 @pytest.mark.parametrize("kind", ["normal", "wide", "far"])
-@pytest.mark.parametrize("act", ["silu"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_slopes_of_the_activations(act, kind):
     """Off by the errors of the two terms, each as in the test above, and their sum's rounding."""
     z = z_values(kind)
@@ -354,6 +354,40 @@ def test_slopes_of_the_activations(act, kind):
         p = 0.5 * torch.special.erfc(-zd * math.sqrt(0.5))
     s = slope_of(z, act)
     assert ((s.double() - (p + second)).abs() <= rel * (p + second.abs()) + 1e-37).all()
+
+
+def test_gelu_errors_are_those_of_fp32_arithmetic():
+    """Root mean squares over normal z.  The slope is a sum of about five roundings of at most
+    2^-24 each, 2^-24 sqrt(5 / 3) = 7.7e-8 if they are independent; of the activation they
+    reach |z| / 2 erfc <= 0.17, and the sum's own rounding stays: 0.75 * 2^-24 = 4.5e-8."""
+    z = z_values("normal")
+    rms = lambda e: e.double().square().mean().sqrt().item()  # noqa: E731
+    assert rms(activation_of(z, "gelu").double() - act64(z.double(), "gelu")) <= 4.5e-8
+    assert rms(slope_of(z, "gelu").double() - slope64(z.double(), "gelu")) <= 7.7e-8
+
+
+def test_activations_of_infinities_and_nan():
+    """GELU of +infinity is +infinity and of -infinity zero, its slopes are 1 and 0; a NaN reaches
+    no other channel, not the one that shares its reciprocal either (whose last bits may
+    follow the NaN's place, (|z| + 4) 2^-21 for two results within their bounds)."""
+    inf, nan = float("inf"), float("nan")
+    z = torch.tensor([inf, -inf, 1e30, -1e30, 40.0, -40.0, 3.0, -3.0], device="cuda").repeat(4)
+    y, s = activation_of(z, "gelu"), slope_of(z, "gelu")
+    assert (y[0::8] == inf).all() and (y[2::8] == 1e30).all() and (y[4::8] == 40).all()
+    assert (y[1::8] == 0).all() and (y[3::8] == 0).all() and (y[5::8] == 0).all()
+    assert (s[0:6:2] == 1).all() and (s[1:6:2] == 0).all()
+    assert (activation_of(z, "silu")[2::8] == 1e30).all() and (activation_of(z, "silu")[3::8] == 0).all()
+    z = z_values("normal")[:4096]
+    for act in ("silu", "gelu"):
+        clean = activation_of(z, act), slope_of(z, act)
+        for part in (0, 1):
+            bad = z.clone()
+            bad[part::2] = nan
+            for want, got in zip(clean, (activation_of(bad, act), slope_of(bad, act))):
+                assert torch.isnan(got[part::2]).all()
+                w, v = want[1 - part::2].double(), got[1 - part::2].double()
+                tol = (z[1 - part::2].double().abs() + 4) * 2.0 ** -21 * w.abs().clamp(min=1)
+                assert ((w - v).abs() <= tol).all()
 
 
 # ------------------------------------------------------------- streams, graphs
