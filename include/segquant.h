@@ -407,6 +407,15 @@ sq_status sq_adapter_add(const void* x, sq_dtype xt, int64_t M, int64_t ldx,
                          int32_t requests, void* y, sq_dtype yt, int64_t ldy, float* hidden,
                          sq_stream_t stream);
 
+/* The same into an output of its own, rounded once: out (bf16 [M, N], row stride ldo, must
+ * not overlap y) = y + the term, in every row (y's values where there is no adapter).  The
+ * fp32 y is what sq_linear_forward_codes writes with yt = SQ_F32; adding to its bf16
+ * output in place rounds the sum a second time. */
+sq_status sq_adapter_add_to(const void* x, sq_dtype xt, int64_t M, int64_t ldx,
+                            const sq_adapters* adapters, const int32_t* bounds,
+                            const int32_t* index, int32_t requests, const float* y, int64_t ldy,
+                            void* out, int64_t ldo, float* hidden, sq_stream_t stream);
+
 /* Host only: workspace bytes of sq_adapter_backward (rules as for
  * sq_group_norm_workspace_size). */
 sq_status sq_adapter_backward_workspace_size(int64_t M, int32_t R, size_t* bytes);

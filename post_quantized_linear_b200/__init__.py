@@ -730,14 +730,19 @@ def _check_requests(bounds: torch.Tensor, index: torch.Tensor, adapters: Adapter
 
 
 def adapter_add(y: torch.Tensor, x: torch.Tensor, adapters: Adapters, bounds: torch.Tensor,
-                index: torch.Tensor, return_hidden: bool = False, stream=None):
+                index: torch.Tensor, return_hidden: bool = False, stream=None,
+                out: Optional[torch.Tensor] = None):
     """Adds the requests' low-rank terms to the shared projection's output ``y`` [M, N]
     in place: rows bounds[q] .. bounds[q+1] of ``x`` [M, K] use adapter index[q]
     (below 0: none), y += scale * (x a^T) b^T.  Rows of no request are left as they
     are.  ``bounds`` int32 [Q + 1] and ``index`` int32 [Q] stay on the device.  For a
     fused q | k | v projection with adapters of its own per part, call it on column
     slices of ``y``.  With ``return_hidden`` returns (y, hidden), hidden = x a^T in fp32
-    [M, R] for ``adapter_backward``; otherwise y."""
+    [M, R] for ``adapter_backward``; otherwise y.
+
+    A bf16 ``y`` holds a rounded value, and its sum is rounded again.  To round once, let
+    ``linear_from_codes`` write float32 and give a bfloat16 ``out`` [M, N]: it receives y + the
+    term (y's values in rows without an adapter), ``y`` stays as it is, ``out`` is returned."""
     n, dev = _check_requests(bounds, index, adapters)
     c = adapters.c_struct()
     M = x.shape[0]
@@ -745,13 +750,25 @@ def adapter_add(y: torch.Tensor, x: torch.Tensor, adapters: Adapters, bounds: to
     dy, ldy = _check_rows(y, M, c.N, "y")
     if dx != dev or dy != dev:
         raise ValueError("x and y must be on the current CUDA device")
+    if out is not None:
+        do, ldo = _check_rows(out, M, c.N, "out")
+        if do != dev:
+            raise ValueError("out must be on the current CUDA device")
+        if y.dtype is not torch.float32 or out.dtype is not torch.bfloat16:
+            raise TypeError("with out, y must be float32 and out bfloat16")
     with _in_order(stream):
         hidden = x.new_empty((M, c.R), dtype=torch.float32) if return_hidden else None
-    st = _lib.load().sq_adapter_add(
-        x.data_ptr(), _dtype_code(x.dtype), M, ldx, c, bounds.data_ptr(), index.data_ptr(), n, y.data_ptr(),
-        _dtype_code(y.dtype), ldy, None if hidden is None else hidden.data_ptr(), _stream_ptr(stream, dev))
+    if out is not None:
+        name, st = "sq_adapter_add_to", _lib.load().sq_adapter_add_to(
+            x.data_ptr(), _dtype_code(x.dtype), M, ldx, c, bounds.data_ptr(), index.data_ptr(), n, y.data_ptr(), ldy,
+            out.data_ptr(), ldo, None if hidden is None else hidden.data_ptr(), _stream_ptr(stream, dev))
+        y = out
+    else:
+        name, st = "sq_adapter_add", _lib.load().sq_adapter_add(
+            x.data_ptr(), _dtype_code(x.dtype), M, ldx, c, bounds.data_ptr(), index.data_ptr(), n, y.data_ptr(),
+            _dtype_code(y.dtype), ldy, None if hidden is None else hidden.data_ptr(), _stream_ptr(stream, dev))
     if st:
-        raise SegQuantError("sq_adapter_add", st)
+        raise SegQuantError(name, st)
     return (y, hidden) if return_hidden else y
 
 

@@ -95,6 +95,8 @@ SIGNATURES = {
                                            c_vp, c_vp, c_vp, c_size, c_vp]),
     "sq_adapter_add": (c_i32, [c_vp, c_i32, c_i64, c_i64, P_AD, c_vp, c_vp, c_i32, c_vp, c_i32, c_i64,
                                c_vp, c_vp]),
+    "sq_adapter_add_to": (c_i32, [c_vp, c_i32, c_i64, c_i64, P_AD, c_vp, c_vp, c_i32, c_vp, c_i64, c_vp, c_i64,
+                                  c_vp, c_vp]),
     "sq_adapter_backward_workspace_size": (c_i32, [c_i64, c_i32, P_SIZE]),
     "sq_adapter_backward": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_vp, c_i32, c_i64, c_vp, P_AD, c_vp, c_vp,
                                     c_i32, c_vp, c_i64, c_vp, c_vp, c_vp, c_size, c_vp]),

@@ -25,6 +25,8 @@ struct AdapterArgs {
   int64_t ldx;
   void* y;                       // forward: y [M, N], added to; backward: dx [M, K], written
   int64_t ldy;
+  void* out;                     // forward into an output of its own: bf16 [M, N] = y + the term, else null
+  int64_t ldo;
   const __nv_bfloat16* a;        // [L, R, K]
   const __nv_bfloat16* b;        // [L, N, R]
   const float* scale;            // [L]
@@ -168,6 +170,15 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
     for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
   }
 }
+// Vectors from, from + step, .. below `to` of eight elements, fp32 -> bf16, of a row without an adapter.
+template <typename YT, typename OT>
+__device__ __forceinline__ void copy_row(const YT* y, OT* out, int from, int to, int step) {
+  for (int i = from; i < to; i += step) {
+    float v[8];
+    load8(y + i * 8, v);
+    store_vec<8>(out, (int64_t)i * 8, sizeof(OT) == 2, v);
+  }
+}
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
@@ -223,11 +234,12 @@ __device__ __forceinline__ void reduce_rank_vectors(const float (&v)[M][8], bool
   }
 }
 
-// T rows (1 or 8).  BWD = false: x A^T, then y += scale h B^T.  BWD = true:
-// scale dy B, then dx = u A.
-template <int T, typename XT, typename YT, bool BWD>
+// T rows (1 or 8).  BWD = false: x A^T, then y += scale h B^T (OT other than YT: out = y + ..,
+// rounded once).  BWD = true: scale dy B, then dx = u A.
+template <int T, typename XT, typename YT, typename OT, bool BWD>
 __global__ void __launch_bounds__(kFewThreads, T == 1 ? 4 : 2)
     adapter_few_rows_kernel(const AdapterArgs p, int cs) {
+  constexpr bool APART = !std::is_same<YT, OT>::value;
   constexpr int XP = kFewChunk + 4;                                   // row pitch: shifts the banks
   constexpr int MR = T == 1 ? 1 : 4;                                  // rows reduced at a time
   // rows [row][k] while they are contracted, then the threads' sums
@@ -249,13 +261,20 @@ __global__ void __launch_bounds__(kFewThreads, T == 1 ? 4 : 2)
       YT* y = static_cast<YT*>(p.y);
       for (int m = 0; m < it.n; ++m)
         for (int c = e0 + tid; c < e1; c += kFewThreads) st_elem(y + (int64_t)(it.row + m) * p.ldy + c, 0.0f);
-    } else if (p.h != nullptr && rank == 0) {
-      for (int i = tid; i < it.n * R; i += kFewThreads) p.h[(int64_t)it.row * R + i] = 0.0f;
+      return;
     }
+    if (p.h != nullptr && rank == 0)
+      for (int i = tid; i < it.n * R; i += kFewThreads) p.h[(int64_t)it.row * R + i] = 0.0f;
+    if (APART)
+      for (int m = 0; m < it.n; ++m)
+        copy_row(static_cast<const YT*>(p.y) + (int64_t)(it.row + m) * p.ldy,
+                 static_cast<OT*>(p.out) + (int64_t)(it.row + m) * p.ldo, e0 / 8 + tid, e1 / 8, kFewThreads);
     return;
   }
   const XT* x = static_cast<const XT*>(p.x) + (int64_t)it.row * p.ldx;
   YT* y = static_cast<YT*>(p.y) + (int64_t)it.row * p.ldy;
+  OT* out = APART ? static_cast<OT*>(p.out) + (int64_t)it.row * p.ldo : reinterpret_cast<OT*>(y);
+  const int64_t ldo = APART ? p.ldo : p.ldy;
   const __nv_bfloat16* wa = p.a + (int64_t)it.l * R * p.K;
   const __nv_bfloat16* wb = p.b + (int64_t)it.l * p.N * R;
   int d0, d1;
@@ -476,8 +495,8 @@ __global__ void __launch_bounds__(kFewThreads, T == 1 ? 4 : 2)
 #pragma unroll
     for (int m = 0; m < T; ++m)
       if (m < it.n) {
-        YT* d = y + (int64_t)m * p.ldy + c;
-        st_elem(d, BWD ? o[m] : to_f32(*d) + o[m]);
+        const YT* d = y + (int64_t)m * p.ldy + c;
+        st_elem(out + (int64_t)m * ldo + c, BWD ? o[m] : to_f32(*d) + o[m]);
       }
   }
   __syncwarp();

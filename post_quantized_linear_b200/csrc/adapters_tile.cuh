@@ -106,7 +106,7 @@ struct AdapterTileArgs {
   int32_t stages;      // ring slots
   int32_t slot_bytes;  // kTileX + the weight tile
   int32_t parts;       // bf16 parts that h is multiplied as
-  int32_t wide;        // y's rows take 32-byte stores
+  int32_t wide;        // the output's rows take 32-byte stores
   const float* hidden;         // backward: h of the forward pass [M, R], and
   __nv_bfloat16* f_u;          // u and h as three bf16 parts side by side, [M][3][rank padded to 16],
   __nv_bfloat16* f_h;          // the operands of the adapters' gradients
@@ -136,12 +136,14 @@ __host__ __device__ inline int adapter_h_bytes(int rp, int parts) {
 // ragged requests (248 MB): 63.5 us, 3.9 TB/s.  A cluster's exchange between the products
 // (about 9 us, in which it asks for no more than the ring holds) and the search and launch
 // (3 us) bound them; the tensor cores are busy for 9 %.
-template <int RB, typename YT, bool BWD>
+// OT other than YT: y + the term goes to out, rounded once, and so do the rows without an adapter.
+template <int RB, typename YT, typename OT, bool BWD>
 __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
     adapter_tile_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw1,
                         const __grid_constant__ CUtensorMap tw2, const __grid_constant__ CUtensorMap ty,
                         const __grid_constant__ AdapterTileArgs args) {
   constexpr int ES = sizeof(YT);
+  constexpr bool APART = !std::is_same<YT, OT>::value;
   constexpr int BN = 128 / ES;             // columns of an output tile
   constexpr int D2 = RB;                   // TMEM column of the second accumulator of h, and of the outputs,
   constexpr int ND = RB == 64 ? 3 : 2;     // and how many tiles of them there are room for
@@ -164,9 +166,14 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
         uint4* d = reinterpret_cast<uint4*>(static_cast<YT*>(p.y) + (int64_t)(it.row + m) * p.ldy + c0);
         for (int i = lane; i < w; i += 32) d[i] = make_uint4(0u, 0u, 0u, 0u);
       }
-    } else if (p.h != nullptr && rank == 0) {
-      for (int i = threadIdx.x; i < it.n * R; i += kTileThreads) p.h[(int64_t)it.row * R + i] = 0.0f;
+      return;
     }
+    if (p.h != nullptr && rank == 0)
+      for (int i = threadIdx.x; i < it.n * R; i += kTileThreads) p.h[(int64_t)it.row * R + i] = 0.0f;
+    if (APART)
+      for (int m = warp; m < it.n; m += kTileThreads / 32)
+        copy_row(static_cast<const YT*>(p.y) + (int64_t)(it.row + m) * p.ldy,
+                 static_cast<OT*>(p.out) + (int64_t)(it.row + m) * p.ldo, t0 * BN / 8 + lane, min(E, t1 * BN) / 8, 32);
     return;
   }
   const int RP = (R + 15) & ~15, rt = (RP + 63) / 64;
@@ -433,7 +440,8 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
     // them all, else row by row (69 us instead of 73 for all gradients of 8192 x 4608 -> 1152).
     const int rows = min(32, it.n - quad * 32);     // rows of the piece in this quarter (may be < 1)
     const bool issuer = half == 0 && lane == 0;     // of the quarter's stores
-    YT* out = static_cast<YT*>(p.y) + (int64_t)(it.row + row) * p.ldy;
+    OT* out = APART ? static_cast<OT*>(p.out) + (int64_t)(it.row + row) * p.ldo
+                    : static_cast<OT*>(p.y) + (int64_t)(it.row + row) * p.ldy;
     for (int j = 0; j < nt && ok; ++j) {
       const int i = nk + j, s = i % NS, b = j % ND;
       if (!BWD && !(ok = wait_warp(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
@@ -460,7 +468,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(d_empty + b));
-        uint32_t w[16];
+        uint32_t w[16];                              // 8 of them where fp32 becomes bf16
 #pragma unroll
         for (int q = 0; q < 4; ++q) {                // 16-byte chunks
           constexpr int PER = 16 / ES;
@@ -476,7 +484,8 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if constexpr (ES == 2) w[4 * q + k] = pack_bf16(o[2 * k], o[2 * k + 1]);
-            else w[4 * q + k] = __float_as_uint(o[k]);
+            else if constexpr (!APART) w[4 * q + k] = __float_as_uint(o[k]);
+            else if (k < 2) w[2 * q + k] = pack_bf16(o[2 * k], o[2 * k + 1]);
           }
         }
         const int c0t = (t0 + j) * BN;
@@ -485,7 +494,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
           if (lane < rows) {
             // the columns come in multiples of 16
             if (c < E) store_u32x8(out + c, *reinterpret_cast<const uint32_t(*)[8]>(w), args.wide != 0);
-            if (c + 32 / ES < E)
+            if (!APART && c + 32 / ES < E)
               store_u32x8(out + c + 32 / ES, *reinterpret_cast<const uint32_t(*)[8]>(w + 8), args.wide != 0);
           }
           // behind the stores, which depend on what was read of the slot: an arrival right after

@@ -43,8 +43,8 @@ sq::AdapterArgs adapter_args(const sq_adapters* ad, const int32_t* bounds, const
   return a;
 }
 
-template <int T, bool BWD>
-sq_status launch_few_rows_t(const sq::AdapterArgs& a, sq_dtype xt, sq_dtype yt, cudaStream_t s) {
+template <int T, typename XT, bool BWD>
+sq_status launch_few_rows_x(const sq::AdapterArgs& a, sq_dtype yt, cudaStream_t s) {
   const int64_t slots = sq::adapter_slots(a.M, a.Q, T);
   const int D = BWD ? a.N : a.K;
   // as many CTAs per piece as the SMs hold at once, each with a warp's load of the long axis
@@ -52,13 +52,17 @@ sq_status launch_few_rows_t(const sq::AdapterArgs& a, sq_dtype xt, sq_dtype yt, 
   int cs = 1;
   while (cs < 8 && slots * cs * 2 <= room && D >= 256 * cs) cs *= 2;
   const dim3 grid((unsigned)(slots * cs));
-  if (xt == SQ_BF16)
-    return yt == SQ_BF16
-               ? launch_grid<sq::adapter_few_rows_kernel<T, __nv_bfloat16, __nv_bfloat16, BWD>>(grid, sq::kFewThreads, 0, cs, true, s, a, cs)
-               : launch_grid<sq::adapter_few_rows_kernel<T, __nv_bfloat16, float, BWD>>(grid, sq::kFewThreads, 0, cs, true, s, a, cs);
-  return yt == SQ_BF16
-             ? launch_grid<sq::adapter_few_rows_kernel<T, float, __nv_bfloat16, BWD>>(grid, sq::kFewThreads, 0, cs, true, s, a, cs)
-             : launch_grid<sq::adapter_few_rows_kernel<T, float, float, BWD>>(grid, sq::kFewThreads, 0, cs, true, s, a, cs);
+  using bf16 = __nv_bfloat16;
+  constexpr int n = sq::kFewThreads;
+  if constexpr (!BWD)
+    if (a.out != nullptr)
+      return launch_grid<sq::adapter_few_rows_kernel<T, XT, float, bf16, false>>(grid, n, 0, cs, true, s, a, cs);
+  return yt == SQ_BF16 ? launch_grid<sq::adapter_few_rows_kernel<T, XT, bf16, bf16, BWD>>(grid, n, 0, cs, true, s, a, cs)
+                       : launch_grid<sq::adapter_few_rows_kernel<T, XT, float, float, BWD>>(grid, n, 0, cs, true, s, a, cs);
+}
+template <int T, bool BWD>
+sq_status launch_few_rows_t(const sq::AdapterArgs& a, sq_dtype xt, sq_dtype yt, cudaStream_t s) {
+  return xt == SQ_BF16 ? launch_few_rows_x<T, __nv_bfloat16, BWD>(a, yt, s) : launch_few_rows_x<T, float, BWD>(a, yt, s);
 }
 
 // Pieces of one row where requests have up to two on average, of eight elsewhere: 64
@@ -151,15 +155,16 @@ int resident_clusters(int cs, int threads, int smem) {
   return n;
 }
 
-template <int RB, typename YT, bool BWD>
+template <int RB, typename YT, typename OT, bool BWD>
 sq_status launch_tile_rb(sq::AdapterTileArgs t, const CUtensorMap& tx, const CUtensorMap& tw1,
                          const CUtensorMap& tw2, const CUtensorMap& ty, cudaStream_t s) {
-  constexpr auto kern = sq::adapter_tile_kernel<RB, YT, BWD>;
+  constexpr auto kern = sq::adapter_tile_kernel<RB, YT, OT, BWD>;
   const sq::AdapterArgs& a = t.p;
   const int D = BWD ? a.N : a.K, E = BWD ? a.K : a.N;
   const int rp = (a.R + 15) / 16 * 16;
-  t.parts = sizeof(YT) == 2 ? 2 : 3;
-  t.wide = reinterpret_cast<uintptr_t>(a.y) % 32 == 0 && a.ldy * (int64_t)sizeof(YT) % 32 == 0;
+  t.parts = sizeof(OT) == 2 ? 2 : 3;
+  t.wide = reinterpret_cast<uintptr_t>(a.out != nullptr ? a.out : a.y) % 32 == 0 &&
+           (a.out != nullptr ? a.ldo : a.ldy) * (int64_t)sizeof(OT) % 32 == 0;
   t.slot_bytes = sq::kTileX + (RB == 64 ? 8192 : 16384);
   t.wait_budget = g_wait_budget;
   t.starve = g_debug_starve;
@@ -222,14 +227,20 @@ sq_status launch_tile(const sq::AdapterTileArgs& t, sq_dtype yt, cudaStream_t s)
     if ((st = make_adapter_map(&tw2, SQ_BF16, a.b, 3, R, N, L, R * 2, N * R * 2, 64, bn)) != SQ_OK) return st;
     if ((st = make_adapter_map(&ty, yt, a.y, 2, N, M, 1, a.ldy * elt_size(yt), 0, bn, 32)) != SQ_OK) return st;
   }
-  if constexpr (BWD)
-    return R <= 64 ? launch_tile_rb<64, __nv_bfloat16, true>(t, tx, tw1, tw2, ty, s)
-                   : launch_tile_rb<128, __nv_bfloat16, true>(t, tx, tw1, tw2, ty, s);
-  if (R <= 64)
-    return yt == SQ_BF16 ? launch_tile_rb<64, __nv_bfloat16, false>(t, tx, tw1, tw2, ty, s)
-                         : launch_tile_rb<64, float, false>(t, tx, tw1, tw2, ty, s);
-  return yt == SQ_BF16 ? launch_tile_rb<128, __nv_bfloat16, false>(t, tx, tw1, tw2, ty, s)
-                       : launch_tile_rb<128, float, false>(t, tx, tw1, tw2, ty, s);
+  using bf16 = __nv_bfloat16;
+  if constexpr (BWD) {
+    return R <= 64 ? launch_tile_rb<64, bf16, bf16, true>(t, tx, tw1, tw2, ty, s)
+                   : launch_tile_rb<128, bf16, bf16, true>(t, tx, tw1, tw2, ty, s);
+  } else {
+    if (a.out != nullptr)
+      return R <= 64 ? launch_tile_rb<64, float, bf16, false>(t, tx, tw1, tw2, ty, s)
+                     : launch_tile_rb<128, float, bf16, false>(t, tx, tw1, tw2, ty, s);
+    if (R <= 64)
+      return yt == SQ_BF16 ? launch_tile_rb<64, bf16, bf16, false>(t, tx, tw1, tw2, ty, s)
+                           : launch_tile_rb<64, float, float, false>(t, tx, tw1, tw2, ty, s);
+    return yt == SQ_BF16 ? launch_tile_rb<128, bf16, bf16, false>(t, tx, tw1, tw2, ty, s)
+                         : launch_tile_rb<128, float, float, false>(t, tx, tw1, tw2, ty, s);
+  }
 }
 
 // The first product in bf16 tiles of 128 rows pays where requests have rows to fill
@@ -313,6 +324,27 @@ size_t adapter_bwd_bytes(int64_t M, int32_t R) {
   return (size_t)M * (size_t)((R + 15) / 16 * 16) * 3 * sizeof(__nv_bfloat16) * 2;
 }
 
+// y += the term, or out = y + the term where out is given (y fp32, out bf16).
+sq_status adapter_forward(const void* x, sq_dtype xt, int64_t M, int64_t ldx, const sq_adapters* adapters,
+                          const int32_t* bounds, const int32_t* index, int32_t requests, void* y, sq_dtype yt,
+                          int64_t ldy, void* out, int64_t ldo, float* hidden, sq_stream_t stream) {
+  sq_status st = check_adapters(adapters, bounds, index, requests, M);
+  if (st != SQ_OK) return st;
+  if (!dtype_ok(xt) || !dtype_ok(yt)) return SQ_ERR_INVALID_ARG;
+  if (M == 0 || (requests == 0 && hidden == nullptr && out == nullptr)) return SQ_OK;
+  if ((st = check_matrix(x, xt, adapters->K, ldx)) != SQ_OK) return st;
+  if ((st = check_matrix(y, yt, adapters->N, ldy)) != SQ_OK) return st;
+  if (out != nullptr && (st = check_matrix(out, SQ_BF16, adapters->N, ldo)) != SQ_OK) return st;
+  if (hidden != nullptr && !aligned16(hidden)) return SQ_ERR_ALIGNMENT;
+  sq::AdapterArgs a = adapter_args(adapters, bounds, index, requests, M);
+  a.x = x; a.ldx = ldx; a.y = y; a.ldy = ldy; a.out = out; a.ldo = ldo; a.h = hidden;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!use_tiles(a, xt)) return launch_few_rows<false>(a, xt, yt, s);
+  sq::AdapterTileArgs t = {};
+  t.p = a;
+  return launch_tile<false>(t, yt, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -320,20 +352,15 @@ extern "C" {
 sq_status sq_adapter_add(const void* x, sq_dtype xt, int64_t M, int64_t ldx, const sq_adapters* adapters,
                          const int32_t* bounds, const int32_t* index, int32_t requests, void* y, sq_dtype yt,
                          int64_t ldy, float* hidden, sq_stream_t stream) {
-  sq_status st = check_adapters(adapters, bounds, index, requests, M);
-  if (st != SQ_OK) return st;
-  if (!dtype_ok(xt) || !dtype_ok(yt)) return SQ_ERR_INVALID_ARG;
-  if (M == 0 || (requests == 0 && hidden == nullptr)) return SQ_OK;
-  if ((st = check_matrix(x, xt, adapters->K, ldx)) != SQ_OK) return st;
-  if ((st = check_matrix(y, yt, adapters->N, ldy)) != SQ_OK) return st;
-  if (hidden != nullptr && !aligned16(hidden)) return SQ_ERR_ALIGNMENT;
-  sq::AdapterArgs a = adapter_args(adapters, bounds, index, requests, M);
-  a.x = x; a.ldx = ldx; a.y = y; a.ldy = ldy; a.h = hidden;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (!use_tiles(a, xt)) return launch_few_rows<false>(a, xt, yt, s);
-  sq::AdapterTileArgs t = {};
-  t.p = a;
-  return launch_tile<false>(t, yt, s);
+  return adapter_forward(x, xt, M, ldx, adapters, bounds, index, requests, y, yt, ldy, nullptr, 0, hidden, stream);
+}
+
+sq_status sq_adapter_add_to(const void* x, sq_dtype xt, int64_t M, int64_t ldx, const sq_adapters* adapters,
+                            const int32_t* bounds, const int32_t* index, int32_t requests, const float* y,
+                            int64_t ldy, void* out, int64_t ldo, float* hidden, sq_stream_t stream) {
+  if (out == nullptr && M > 0) return SQ_ERR_INVALID_ARG;
+  return adapter_forward(x, xt, M, ldx, adapters, bounds, index, requests, const_cast<float*>(y), SQ_F32, ldy, out,
+                         ldo, hidden, stream);
 }
 
 sq_status sq_adapter_backward_workspace_size(int64_t M, int32_t R, size_t* bytes) {

@@ -164,6 +164,55 @@ def test_gradients_match_differences():
         assert abs((grads[i].double() * v).sum().item() - want) <= 1e-5 * terms
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=str)
+@pytest.mark.parametrize("case", CASES)
+def test_forward_into_another_output_rounds_once(case, dtype):
+    """y fp32 into a bf16 out: y + the term within one half step, y's values rounded where there
+    is no adapter, nothing around out and nothing of y changed."""
+    M, K, N, L, R, lengths, index, first = CASES[case]
+    x, y, ad, _ = make(M, K, N, L, R, dtype, F32, seed=M + 2)
+    bounds, idx = requests(lengths, index, first)
+    (ref, hid), (_, e_h) = forward64(y, x, ad, bounds, idx)
+    _, (e, _) = forward64(y.to(BF), x, ad, bounds, idx)    # h in two parts, as for a bf16 y
+    before = y.clone()
+    room = torch.full((M, N + 24), 7.0, device="cuda", dtype=BF)
+    out = room[:, 8:N + 8]
+    got, hidden = pq.adapter_add(y, x, ad, bounds, idx, return_hidden=True, out=out)
+    assert got is out and torch.equal(y, before)
+    check(out, ref, e)
+    check(hidden, hid, e_h)
+    none = torch.ones(M, dtype=torch.bool, device="cuda")
+    for m, _ in rows_of(bounds, idx):
+        none[m] = False
+    assert torch.equal(out[none], y[none].to(BF))
+    assert (room[:, :8] == 7).all() and (room[:, N + 8:] == 7).all()
+    assert torch.equal(pq.adapter_add(y, x, ad, bounds, idx, out=torch.empty(M, N, device="cuda", dtype=BF)), out)
+    assert pq.stream_status() == 0
+
+
+def test_forward_into_another_output_refusals_and_empty_batches():
+    x, y, ad, _ = make(20, 128, 64, 2, 8, BF, F32)
+    bounds, idx = requests([20], [1])
+    out = torch.empty(20, 64, device="cuda", dtype=BF)
+    with pytest.raises(TypeError, match="float32 and out bfloat16"):
+        pq.adapter_add(y.to(BF), x, ad, bounds, idx, out=out)
+    with pytest.raises(TypeError, match="float32 and out bfloat16"):
+        pq.adapter_add(y, x, ad, bounds, idx, out=torch.empty_like(y))
+    with pytest.raises(ValueError, match="out must be"):
+        pq.adapter_add(y, x, ad, bounds, idx, out=out[:, :32])
+    with pytest.raises(ValueError, match="out must be"):
+        pq.adapter_add(y, x, ad, bounds, idx, out=out.cpu())
+    none, start = idx[:0], bounds[:1]
+    assert torch.equal(pq.adapter_add(y, x, ad, start, none, out=out), y.to(BF))
+    assert pq.adapter_add(y[:0], x[:0], ad, start, none, out=out[:0]).shape == (0, 64)
+    # a request that is left out: its rows are rows without an adapter
+    bad = torch.tensor([0, 12, 30], dtype=torch.int32, device="cuda")
+    two = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    pq.adapter_add(y, x, ad, bad, two, out=out)
+    assert pq.stream_status() == pq._lib.SQ_ERR_RANGE
+    assert torch.equal(out[12:], y[12:].to(BF)) and not torch.equal(out[:12], y[:12].to(BF))
+
+
 def test_column_slices_strides_and_no_scale():
     """A fused q | k | v output with adapters of its own per part, in a padded buffer."""
     x0, y0, ad, g = make(150, 272, 3 * 128 + 16, 2, 16, seed=8)
@@ -492,6 +541,33 @@ def test_norm_codes_linear_adapters_run(B, S, C, N, act):
     (ref, _), (e2, _) = forward64(full, rows, ad, bounds, idx)
     mag = q.abs() @ (qw.codes.double().abs() * qw.scales[0].double()[:, None]).t() * max(sp.item(), sn.item())
     check(base, ref, e2 + e + half_step(BF) * full.abs() + 1e-6 * mag)
+
+
+@pytest.mark.parametrize("S,C,N", [(256, 1152, 1152), (33, 256, 400)])
+def test_norm_codes_linear_adapters_run_rounded_once(S, C, N):
+    """The run with an fp32 layer output and an output of its own: within one half step of the
+    64-bit value.  A rounding's mean square error goes with the mean square of what is
+    rounded, so the bf16 layer output adds E[layer^2] / E[sum^2] of the one rounding's; half
+    of that has to be gone."""
+    g = torch.Generator(device="cuda").manual_seed(S)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, M, R = (2 * rn(2, S, C) + 0.5).to(BF), 2 * S, 16
+    qw = pq.quantize_weights(0.05 * rn(N, C), (0, C))
+    ad = pq.Adapters((rn(2, R, C) / C ** 0.5).to(BF), (0.3 * rn(2, N, R) / R ** 0.5).to(BF))
+    bounds, idx = requests([S, S], [1, 0])
+    sp, sn = pq.calibrate(pq.group_norm_act(x, 32).view(M, C), (0, C))
+    qp, qn, rows = pq.quantize_activations_norm(x, 32, None, None, (0, C), sp, sn, return_y=True)
+    wide = pq.linear_from_codes(qp, qn, qw, sp, sn, out_dtype=F32)
+    once = pq.adapter_add(wide, rows, ad, bounds, idx, out=torch.empty(M, N, device="cuda", dtype=BF))
+    twice = pq.adapter_add(pq.linear_from_codes(qp, qn, qw, sp, sn), rows, ad, bounds, idx)
+    q = qp.double() + qn.double()
+    w = qw.codes.double() * qw.scales[0].double()[:, None]
+    full = torch.where(q >= 0, q * sp.double(), q * sn.double()) @ w.t()
+    (ref, _), _ = forward64(full, rows, ad, bounds, idx)
+    _, (e, _) = forward64(full.to(BF), rows, ad, bounds, idx)
+    check(once, ref, e + 1e-6 * q.abs() @ w.abs().t() * max(sp.item(), sn.item()))
+    one, two = ((t.double() - ref).square().mean().item() for t in (once, twice))
+    assert one * (1 + 0.5 * (full.square().mean() / ref.square().mean()).item()) < two
 
 
 @pytest.mark.parametrize("R", [16, 64, 128])

@@ -143,6 +143,23 @@ def test_adapter_refusals():
     assert L.load().sq_adapter_add(FAKE, 1, 1, 128, None, FAKE, FAKE, 1, FAKE, 1, 64, None, None) == L.SQ_ERR_INVALID_ARG
 
 
+def add_to(y=FAKE, ldy=64, out=FAKE, ldo=64, x=FAKE, M=100, h=None, bounds=FAKE):
+    ad = L.SqAdapters(2, 16, 128, 64, FAKE, FAKE, None)
+    return L.load().sq_adapter_add_to(x, L.SQ_BF16, M, 128, ctypes.byref(ad), bounds, FAKE, 3, y, ldy, out, ldo, h, None)
+
+
+def test_adapter_output_of_its_own_refusals():
+    for k in ("x", "y", "out", "bounds"):
+        assert add_to(**{k: None}) == L.SQ_ERR_INVALID_ARG
+    assert add_to(ldo=56) == L.SQ_ERR_INVALID_ARG
+    assert add_to(ldo=68) == L.SQ_ERR_ALIGNMENT
+    assert add_to(out=FAKE + 8) == L.SQ_ERR_ALIGNMENT
+    assert add_to(ldy=66) == L.SQ_ERR_ALIGNMENT
+    assert add_to(h=FAKE + 4) == L.SQ_ERR_ALIGNMENT
+    assert add_to(M=-1) == L.SQ_ERR_INVALID_ARG
+    assert add_to(M=0, out=None, y=None, x=None) == L.SQ_OK
+
+
 def bwd(dy=FAKE, x=FAKE, h=FAKE, dx=FAKE, da=FAKE, db=FAKE, ws=FAKE, wn=1 << 30, lddx=128, R=16):
     ad = L.SqAdapters(2, R, 128, 64, FAKE, FAKE, None)
     return L.load().sq_adapter_backward(dy, L.SQ_BF16, 100, 64, x, L.SQ_BF16, 128, h, ctypes.byref(ad), FAKE, FAKE, 3,
