@@ -272,8 +272,10 @@ def run(state):
         q_pos, q_neg, x16 = pq.quantize_activations_norm(
             s["x"], c["G"], s["gamma"], s["beta"], (0, c["C"]), s["s_pos"], s["s_neg"], eps=EPS,
             act=c["act"], return_y=True)
-        y = pq.linear_from_codes(q_pos, q_neg, qw, s["s_pos"], s["s_neg"])
-        return pq.adapter_add(y, x16, adapters, s["bounds"], s["index"]), x16
+        # the layer's output in fp32, so that the sum with the adapters' term is rounded once
+        y = pq.linear_from_codes(q_pos, q_neg, qw, s["s_pos"], s["s_neg"], out_dtype=torch.float32)
+        out = torch.empty_like(y, dtype=torch.bfloat16)
+        return pq.adapter_add(y, x16, adapters, s["bounds"], s["index"], out=out), x16
     if op == "norm":
         return _norm(s).to(s["x"].dtype)
     if op == "norm_bwd":
