@@ -424,7 +424,7 @@ sq_status sq_adapter_backward_workspace_size(int64_t M, int32_t R, size_t* bytes
  * x's type, written in every row, zeros in rows without an adapter), hidden as
  * written by sq_adapter_add; da fp32 [L, R, K] and db fp32 [L, N, R], overwritten:
  * sums over all rows of all requests of an adapter, in a fixed order, zeros for an
- * adapter that no request uses. */
+ * adapter that no request uses.  requests <= 2^20 and requests * L <= 2^26 (SQ_ERR_RANGE). */
 sq_status sq_adapter_backward(const void* dy, sq_dtype dyt, int64_t M, int64_t lddy, const void* x,
                               sq_dtype xt, int64_t ldx, const float* hidden,
                               const sq_adapters* adapters, const int32_t* bounds,

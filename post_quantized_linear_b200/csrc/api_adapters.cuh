@@ -376,6 +376,10 @@ sq_status sq_adapter_backward(const void* dy, sq_dtype dyt, int64_t M, int64_t l
   sq_status st = check_adapters(adapters, bounds, index, requests, M);
   if (st != SQ_OK) return st;
   if (!dtype_ok(xt) || !dtype_ok(dyt) || da == nullptr || db == nullptr) return SQ_ERR_INVALID_ARG;
+  // Each CTA of the gradients walks all requests, 32 at a time, about 0.5 us each, for its
+  // adapter (2^20 requests of 8 adapters, 4096 rows of 128 columns: 18 ms; 2^16 requests of one row, 1152 ->
+  // 1152: 13 ms).  Beyond these numbers a call could hold the GPU for minutes.
+  if (requests > (1 << 20) || (int64_t)requests * adapters->L > (1 << 26)) return SQ_ERR_RANGE;
   if (!aligned16(da) || !aligned16(db)) return SQ_ERR_ALIGNMENT;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   sq::AdapterArgs a = adapter_args(adapters, bounds, index, requests, M);

@@ -277,6 +277,33 @@ def test_short_requests_share_steps(lengths, R, dtype):
     assert pq.stream_status() == 0
 
 
+@pytest.mark.parametrize("M,Q", [(70000, 70000), (70000, 5000), (3000, 100000)])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=str)
+def test_a_hundred_thousand_requests(M, Q, dtype):
+    """One row each, fourteen, and mostly empty ones."""
+    x, dy, ad, g = make(M, 64, 48, 5, 8, dtype, seed=Q)
+    cuts = torch.randint(0, M + 1, (Q + 1,), generator=g, device="cuda").sort().values
+    bounds = (torch.arange(Q + 1, device="cuda") if Q == M else cuts).to(torch.int32)
+    idx = torch.randint(-1, 5, (Q,), generator=g, device="cuda", dtype=torch.int32)
+    # the adapter of each row; then one request per adapter, of its rows in order
+    which = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+    rows = bounds[1:] - bounds[:-1]
+    which[bounds[0]:bounds[-1]] = idx.repeat_interleave(rows)
+    order = torch.argsort(which, stable=True)
+    b = torch.searchsorted(which[order], torch.arange(6, device="cuda", dtype=torch.int32)).to(torch.int32)
+    l = torch.arange(5, device="cuda", dtype=torch.int32)
+    y = torch.zeros_like(dy)
+    _, hidden = pq.adapter_add(y, x, ad, bounds, idx, return_hidden=True)
+    (ref, hid), (e, e_h) = forward64(torch.zeros_like(dy), x[order], ad, b, l)
+    check(y[order], ref, e)
+    check(hidden[order], hid, e_h)
+    dx, da, db = pq.adapter_backward(dy, x, hidden, ad, bounds, idx)
+    want, e = backward64(dy[order], x[order], hidden[order], ad, b, l)
+    for got, r, t in zip((dx[order], da, db), want, e):
+        check(got, r, t)
+    assert pq.stream_status() == 0
+
+
 @pytest.mark.parametrize("rows", [1, 90])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_non_finite_adapters_of_other_requests(rows, dtype):

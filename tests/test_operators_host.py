@@ -160,6 +160,18 @@ def test_adapter_output_of_its_own_refusals():
     assert add_to(M=0, out=None, y=None, x=None) == L.SQ_OK
 
 
+def test_adapter_backward_request_limits():
+    """A call that would walk more requests an adapter than this is refused, not run for minutes."""
+    def many(Q, A):
+        ad = L.SqAdapters(A, 16, 128, 64, FAKE, FAKE, None)
+        return L.load().sq_adapter_backward(FAKE, L.SQ_BF16, 100, 64, FAKE, L.SQ_BF16, 128, FAKE, ctypes.byref(ad), FAKE,
+                                            FAKE, Q, FAKE, 128, FAKE, FAKE, None, 0, None)
+    assert many((1 << 20) + 1, 2) == L.SQ_ERR_RANGE
+    assert many((1 << 16) + 1, 1 << 10) == L.SQ_ERR_RANGE
+    assert many(1 << 20, 64) == L.SQ_ERR_INVALID_ARG             # accepted; the workspace is missing
+    assert many(1 << 16, 1 << 10) == L.SQ_ERR_INVALID_ARG
+
+
 def bwd(dy=FAKE, x=FAKE, h=FAKE, dx=FAKE, da=FAKE, db=FAKE, ws=FAKE, wn=1 << 30, lddx=128, R=16):
     ad = L.SqAdapters(2, R, 128, 64, FAKE, FAKE, None)
     return L.load().sq_adapter_backward(dy, L.SQ_BF16, 100, 64, x, L.SQ_BF16, 128, h, ctypes.byref(ad), FAKE, FAKE, 3,
