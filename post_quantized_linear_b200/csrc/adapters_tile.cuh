@@ -97,8 +97,11 @@ constexpr int kTileStages = 8;             // most slots of the ring
 // The tensor core cuts its fp32 sums towards zero at every step, a bias that grows with the
 // chain (1.4e-6 of the sum after 16 blocks of 64, where fp32 additions have 5e-7): after
 // kChain blocks along the contracted axis the sums move to registers and are added there,
-// while the next chain runs in a second accumulator.
-constexpr int kChain = 8;
+// while the next chain runs in a second accumulator.  h and u, which carry on into the second
+// product and the gradients, move after kHChain blocks: their rms error is then that of fp32
+// additions (1.3e-7 of h over 2048 or 4608 terms; 4.5e-7 in chains of eight), at the same time,
+// since the reading warps have nothing else to do.
+constexpr int kChain = 8, kHChain = 2;
 
 struct AdapterTileArgs {
   AdapterArgs p;
@@ -127,10 +130,10 @@ __host__ __device__ inline int adapter_h_bytes(int rp, int parts) {
 // of the columns, in tiles 128 bytes wide.  Backward: u = scale dy B, dx = u A, the
 // same steps with both weights MN-major.  RB: the largest rank (64 or 128).
 //
-// h is summed in TMEM in chains of kChain blocks, which meet in fp32 registers; as an operand it is the sum of `parts` bf16 values (two for
-// bf16 outputs: off by 2^-17 of h, against the output's own 2^-8; three for fp32
-// outputs: exact to 2^-24), which costs R/2 more multiply-adds per output and no
-// bytes.
+// h is summed in TMEM in chains of kHChain blocks, which meet in fp32 registers; as an operand
+// it is the sum of `parts` bf16 values (two for bf16 outputs: off by 2^-17 of h, against
+// the output's own 2^-8; three for fp32 outputs: exact to 2^-24), which costs R/2 more
+// multiply-adds per output and no bytes.
 //
 // 8192 x 4608 -> 1152, rank 64 (119 MB): 40.3 us, 2.95 TB/s; 16384 x 2304 -> 3456, rank 32, 23
 // ragged requests (248 MB): 63.5 us, 3.9 TB/s.  A cluster's exchange between the products
@@ -279,8 +282,8 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
       bool ok = true;
       const uint32_t id1 = idesc_bf16(kTileRows, RP) | (BWD ? kIdescBMn : 0u);
       for (int i = 0; i < nk; ++i) {
-        const int s = i % NS, chain = i / kChain, b = chain & 1;
-        const bool first = i % kChain == 0;
+        const int s = i % NS, chain = i / kHChain, b = chain & 1;
+        const bool first = i % kHChain == 0;
         if (first && chain >= 2) {
           if (!(ok = wait1(smem_u32(h_free + b), (chain / 2 - 1) & 1, abort_flag, budget))) break;
           tc_fence_after();
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
                     BWD ? smem_desc_mn_sw128(wt + ks * 2048, 8192) : smem_desc_k_sw128(wt + ks * 32), id1,
                     (!first || ks > 0) ? 1u : 0u);
         umma_commit(smem_u32(empty1 + s));
-        if (i == nk - 1 || (i + 1) % kChain == 0) umma_commit(smem_u32(h_full + b));
+        if (i == nk - 1 || (i + 1) % kHChain == 0) umma_commit(smem_u32(h_full + b));
       }
       if (ok) {
         ok = wait1s<true>(smem_u32(h_ready), 0, abort_flag, budget);
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
         tc_fence_after();
         const uint32_t wt = smem_u32(smem + s * args.slot_bytes) + kTileX;
         uint32_t acc = 0;
-        for (int part = 0; part < args.parts; ++part)
+        for (int part = args.parts - 1; part >= 0; --part)       // the small terms first: little is cut off them
           for (int ks = 0; ks < RP / 16; ++ks) {
             const uint32_t a = hb + (part * rt + (ks >> 2)) * kTileX + (ks & 3) * 32;
             umma_bf16(tmem + D2 + b * BN, smem_desc_k_sw128(a),
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
 #pragma unroll
     for (int c = 0; c < RB / 2; ++c) t[c] = 0.0f;
     bool ok = true;
-    for (int chain = 0; chain * kChain < nk; ++chain) {
+    for (int chain = 0; chain * kHChain < nk; ++chain) {
       const int b = chain & 1;
       if (!(ok = wait_warp(smem_u32(h_full + b), (chain / 2) & 1, abort_flag, budget))) break;
       tc_fence_after();

@@ -482,6 +482,39 @@ def test_requests_left_out_of_the_gradients(lengths, dtype):
         assert torch.equal(dx, want[0]) and torch.equal(da, want[1]) and torch.equal(db, want[2])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=str)
+@pytest.mark.parametrize("M,lengths", [(700, [300, 400]), (24, [9, 15])], ids=["tiles", "few rows"])
+def test_fp32_results_are_as_close_as_elementary_fp32(dtype, M, lengths):
+    """Root mean square errors of the fp32 results against 64 bits, beside those of fp32 matrix
+    products in torch: sums of the same lengths, and h and u rounded at most once more (or
+    cut into parts of 2^-24): at most twice.  (A step of the tensor core cuts up to a unit
+    where a rounding is off by half of one, so this asks for short chains.)"""
+    x, dy, ad, g = make(M, 2048, 1024, 2, 32, dtype, seed=M)
+    bounds, idx = requests(lengths, [1, 0])
+    y = torch.randn(M, 1024, generator=g, device="cuda")
+    (ref, hid), _ = forward64(y, x, ad, bounds, idx)
+    dx = torch.zeros(M, 2048, device="cuda")
+    plain_y, plain_h = y.clone(), torch.zeros(M, 32, device="cuda")
+    plain_a, plain_b = torch.zeros(2, 32, 2048, device="cuda"), torch.zeros(2, 1024, 32, device="cuda")
+    for m, l in rows_of(bounds, idx):
+        A, B, s = ad.a[l].float(), ad.b[l].float(), ad.scale[l]
+        plain_h[m] = x[m].float() @ A.t()
+        plain_y[m] += s * (plain_h[m] @ B.t())
+        u = s * (dy[m].float() @ B)
+        dx[m] = u @ A
+        plain_a[l] = u.t() @ x[m].float()
+        plain_b[l] = s * (dy[m].float().t() @ plain_h[m])
+    got_y, hidden = pq.adapter_add(y, x, ad, bounds, idx, return_hidden=True)
+    want, _ = backward64(dy, x, plain_h, ad, bounds, idx)
+    got = pq.adapter_backward(dy, x, plain_h, ad, bounds, idx)
+    rms = lambda t, r: (t.double() - r).square().mean().sqrt().item()  # noqa: E731
+    pairs = [(hidden, plain_h, hid), (got_y, plain_y, ref), (got[1], plain_a, want[1]), (got[2], plain_b, want[2])]
+    if dtype == F32:
+        pairs.append((got[0], dx, want[0]))
+    for k, (t, p, r) in enumerate(pairs):
+        assert rms(t, r) <= 2 * rms(p, r), (k, rms(t, r), rms(p, r))
+
+
 @pytest.mark.parametrize("R", [16, 128])
 def test_long_sums_of_one_sign_have_no_bias(R):
     """16384 positive terms a sum.  A chain of 32 matrix steps cut towards zero loses at most

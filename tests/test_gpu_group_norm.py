@@ -366,6 +366,51 @@ def test_gelu_errors_are_those_of_fp32_arithmetic():
     assert rms(slope_of(z, "gelu").double() - slope64(z.double(), "gelu")) <= 7.7e-8
 
 
+@pytest.mark.parametrize("shape", [(2, 257, 320, 32), (1, 70001, 64, 8)], ids=str)
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+def test_fp32_results_are_as_close_as_elementary_fp32(act, shape):
+    """Root mean square errors of fp32 results against the 64-bit definition, beside those of the
+    same formulas in elementary fp32 operations: each side rounds every element a handful of
+    times, the kernels up to twice as often (two constants of z, the tail's factors), so up to
+    sqrt 2 of that error is theirs; 2 leaves room for the sums' different orders."""
+    B, S, C, G = shape
+    x, gamma, beta, g = make(B, S, C, F32, seed=C + S)
+    dy = torch.randn(B, S, C, generator=g, device="cuda")
+    half = math.sqrt(0.5)
+
+    def forward(x, gamma, beta):
+        v = x.view(B, S, G, C // G)
+        mean = v.mean((1, 3), keepdim=True)
+        rstd = 1 / torch.sqrt((v - mean).square().mean((1, 3), keepdim=True) + 1e-5)
+        hat = ((v - mean) * rstd).view(B, S, C)
+        z = hat * gamma + beta
+        p = 1 / (1 + torch.exp(-z)) if act == "silu" else 0.5 * (1 + torch.erf(z * half))
+        return hat, rstd, z, p
+
+    def backward(x, dy, gamma, beta):
+        hat, rstd, z, p = forward(x, gamma, beta)
+        d = {"none": lambda: torch.ones_like(z), "silu": lambda: p * (1 + z * (1 - p)),
+             "gelu": lambda: p + z * torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)}[act]()
+        dz = dy * d
+        dh = (dz * gamma).view(B, S, G, -1)
+        h = hat.view(B, S, G, -1)
+        dx = rstd * (dh - dh.mean((1, 3), keepdim=True) - h * (dh * h).mean((1, 3), keepdim=True))
+        return dx.reshape(B, S, C), (dz * hat).sum((0, 1)), dz.sum((0, 1))
+
+    def value(x, gamma, beta):
+        _, _, z, p = forward(x, gamma, beta)
+        return z if act == "none" else z * p
+
+    rms = lambda t, r: (t.double() - r).square().mean().sqrt().item()  # noqa: E731
+    ref = value(x.double(), gamma.double(), beta.double())
+    y, stats = pq.group_norm_act(x, G, gamma, beta, act=act, return_stats=True)
+    assert rms(y, ref) <= 2 * rms(value(x, gamma, beta), ref)
+    want = backward(x.double(), dy.double(), gamma.double(), beta.double())
+    for got, plain, r in zip(pq.group_norm_act_backward(dy, x, stats, gamma, beta, act=act),
+                             backward(x, dy, gamma, beta), want):
+        assert rms(got, r) <= 2 * rms(plain, r)
+
+
 def test_activations_of_infinities_and_nan():
     """GELU of +infinity is +infinity and of -infinity zero, its slopes are 1 and 0; a NaN reaches
     no other channel, not the one that shares its reciprocal either (whose last bits may
