@@ -117,13 +117,13 @@ __device__ __forceinline__ AdapterItem adapter_item(const AdapterArgs& p, int sl
     piece = slot - (start(lo) / T + lo);
   }
   if (lo >= count) return it;
-  const int s = start(lo), e = start(lo + 1);
+  const bool request = lo > 0 && lo <= p.Q;
+  const int from = lo > 0 ? __ldg(p.bounds + lo - 1) : 0, to = lo <= p.Q ? __ldg(p.bounds + lo) : p.M;
+  const int l = request ? __ldg(p.index + lo - 1) : -1;
+  const int s = min(max(from, 0), p.M), e = min(max(to, 0), p.M);
   // (of falling bounds the search may bring any piece)
   if (e < s || piece < 0 || piece > (e - s) / T) return it;
-  if (lo > 0 && lo <= p.Q) {
-    const int l = __ldg(p.index + lo - 1);
-    if (request_counts(__ldg(p.bounds + lo - 1), __ldg(p.bounds + lo), l, p.M, p.L)) it.l = l;
-  }
+  if (request && request_counts(from, to, l, p.M, p.L)) it.l = l;
   it.row = s + piece * T;
   it.n = min(T, e - it.row);
   return it;
@@ -721,7 +721,7 @@ __device__ __forceinline__ void adapter_grad_tile(const AdapterGradArgs& p, int 
 }
 
 template <typename XT, typename DT>
-__global__ void __launch_bounds__(kGradThreads) adapter_grad_kernel(const AdapterGradArgs p) {
+__global__ void __launch_bounds__(kGradThreads, 3) adapter_grad_kernel(const AdapterGradArgs p) {
   __shared__ __align__(16) float sh[kAdapterMaxRank * kGradCols];
   const int tile = blockIdx.x / p.cs;
   grid_dep_wait();

@@ -281,22 +281,31 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
     if (lane == 0) {
       bool ok = true;
       const uint32_t id1 = idesc_bf16(kTileRows, RP) | (BWD ? kIdescBMn : 0u);
-      for (int i = 0; i < nk; ++i) {
-        const int s = i % NS, chain = i / kHChain, b = chain & 1;
-        const bool first = i % kHChain == 0;
-        if (first && chain >= 2) {
-          if (!(ok = wait1(smem_u32(h_free + b), (chain / 2 - 1) & 1, abort_flag, budget))) break;
+      // a slot of the ring and its phase are carried along: this thread's own steps bound it
+      int s = 0;
+      uint32_t phase = 0;
+      for (int i = 0, b = 0, freed = 1; i < nk && ok; i += kHChain) {      // a chain
+        if (i >= 2 * kHChain) {
+          if (!(ok = wait1(smem_u32(h_free + b), (uint32_t)freed, abort_flag, budget))) break;
           tc_fence_after();
         }
-        if (!(ok = wait1(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
-        const uint32_t st = smem_u32(smem + s * args.slot_bytes), wt = st + kTileX;
+        const int end = min(nk, i + kHChain);
+        uint32_t acc = 0;
+        for (int k = i; k < end; ++k) {
+          if (!(ok = wait1(smem_u32(full + s), phase, abort_flag, budget))) break;
+          const uint32_t st = smem_u32(smem + s * args.slot_bytes), wt = st + kTileX;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          umma_bf16(tmem + b * D2, smem_desc_k_sw128(st + ks * 32),
-                    BWD ? smem_desc_mn_sw128(wt + ks * 2048, 8192) : smem_desc_k_sw128(wt + ks * 32), id1,
-                    (!first || ks > 0) ? 1u : 0u);
-        umma_commit(smem_u32(empty1 + s));
-        if (i == nk - 1 || (i + 1) % kHChain == 0) umma_commit(smem_u32(h_full + b));
+          for (int ks = 0; ks < 4; ++ks)
+            umma_bf16(tmem + b * D2, smem_desc_k_sw128(st + ks * 32),
+                      BWD ? smem_desc_mn_sw128(wt + ks * 2048, 8192) : smem_desc_k_sw128(wt + ks * 32), id1,
+                      ks > 0 ? 1u : acc);
+          acc = 1;
+          umma_commit(smem_u32(empty1 + s));
+          if (++s == NS) { s = 0; phase ^= 1; }
+        }
+        if (ok) umma_commit(smem_u32(h_full + b));
+        b ^= 1;
+        freed ^= b == 0;           // the phase of h_free that the next two chains wait for
       }
       if (ok) {
         ok = wait1s<true>(smem_u32(h_ready), 0, abort_flag, budget);
@@ -306,9 +315,9 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
       const uint32_t id2 = idesc_bf16(kTileRows, BN) | (BWD ? kIdescBMn : 0u);
       const uint32_t hb = smem_u32(hbuf);
       for (int j = 0; j < nt && ok; ++j) {
-        const int i = nk + j, s = i % NS, b = j % ND;
+        const int b = j % ND;
         if (j >= ND && !(ok = wait1(smem_u32(d_empty + b), (j / ND - 1) & 1, abort_flag, budget))) break;
-        if (!(ok = wait1(smem_u32(full + s), (i / NS) & 1, abort_flag, budget))) break;
+        if (!(ok = wait1(smem_u32(full + s), phase, abort_flag, budget))) break;
         tc_fence_after();
         const uint32_t wt = smem_u32(smem + s * args.slot_bytes) + kTileX;
         uint32_t acc = 0;
@@ -323,6 +332,7 @@ __global__ void __launch_bounds__(kTileThreads, RB == 64 ? 2 : 1)
           }
         if (BWD) umma_commit(smem_u32(empty1 + s));   // the slot held the weight tile alone
         umma_commit(smem_u32(d_full + b));
+        if (++s == NS) { s = 0; phase ^= 1; }
       }
       umma_commit(smem_u32(drain_bar));
       wait_drain(smem_u32(drain_bar), 0, kDrainBudget);
