@@ -146,8 +146,8 @@ __device__ __forceinline__ void check_requests(const AdapterArgs& p, int threads
 // slice of the columns.  This is the form for batches of requests of a few rows
 // (one conditioning vector each), which are bound by launch and load latency
 // and by the adapters' bytes, and for fp32 rows, bound by the fp32 lanes when there are many.
-// 64 requests of one row, 1152 -> 3456, rank 16: 8.9 us; 777 fp32 rows, 1152 -> 2304, rank 8:
-// 14.7 us.
+// 64 requests of one row, 1152 -> 3456, rank 16: 9.0 us; 777 fp32 rows, 1152 -> 2304, rank 8:
+// 14.8 us.
 constexpr int kFewRows = 8;
 constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
@@ -629,7 +629,7 @@ __device__ __forceinline__ void adapter_grad_tile(const AdapterGradArgs& p, int 
   bool more = pieces.mine(first, count);
   while (more) {
     // rows of as many pieces as there is room for: requests of a row or two share a step (64
-    // requests of one row, 6 adapters of rank 64, 4608 -> 1152: 29.8 us for all gradients, not 42.7)
+    // requests of one row, 6 adapters of rank 64, 4608 -> 1152: 29.3 us for all gradients, not 42.7)
     __syncthreads();
     int n = 0;
     while (more && n < step) {

@@ -135,8 +135,8 @@ __host__ __device__ inline int adapter_h_bytes(int rp, int parts) {
 // the output's own 2^-8; three for fp32 outputs: exact to 2^-24), which costs R/2 more
 // multiply-adds per output and no bytes.
 //
-// 8192 x 4608 -> 1152, rank 64 (119 MB): 40.3 us, 2.95 TB/s; 16384 x 2304 -> 3456, rank 32, 23
-// ragged requests (248 MB): 63.5 us, 3.9 TB/s.  A cluster's exchange between the products
+// 8192 x 4608 -> 1152, rank 64 (119 MB): 40.2 us, 2.97 TB/s; 16384 x 2304 -> 3456, rank 32, 23
+// ragged requests (248 MB): 62.8 us, 3.95 TB/s.  A cluster's exchange between the products
 // (about 9 us, in which it asks for no more than the ring holds) and the search and launch
 // (3 us) bound them; the tensor cores are busy for 9 %.
 // OT other than YT: y + the term goes to out, rounded once, and so do the rows without an adapter.

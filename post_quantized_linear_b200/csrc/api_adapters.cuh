@@ -66,8 +66,8 @@ sq_status launch_few_rows_t(const sq::AdapterArgs& a, sq_dtype xt, sq_dtype yt, 
 }
 
 // Pieces of one row where requests have up to two on average, of eight elsewhere: 64
-// requests of one, two, four, eight rows, 2304 -> 2304, rank 32, take 10.5, 12.9, 18.1, 29.2 us
-// in pieces of one and 16.7, 17.5, 18.9, 22.0 us in pieces of eight, which read an
+// requests of one, two, four, eight rows, 2304 -> 2304, rank 32, take 10.7, 13.0, 18.2, 29.4 us
+// in pieces of one and 16.7, 17.4, 18.9, 22.0 us in pieces of eight, which read an
 // adapter once for eight rows.
 template <bool BWD>
 sq_status launch_few_rows(const sq::AdapterArgs& a, sq_dtype xt, sq_dtype yt, cudaStream_t s) {
@@ -82,8 +82,8 @@ sq_status launch_adapter_grad(sq::AdapterGradArgs& g, sq_dtype xt, sq_dtype dyt,
   const int tiles = g.tiles0 + (g.C[1] + sq::kGradCols - 1) / sq::kGradCols;
   // The cluster shares an adapter's pieces: the number of CTAs that takes the least time,
   // all of them over the resident ones and the last one behind them, each about two
-  // pieces' time to begin and end (8000 rows of ten uneven requests, 2304 -> 2304, rank 64: 419 us
-  // where one CTA had an adapter's pieces 487).
+  // pieces' time to begin and end (8000 rows of ten uneven requests, 2304 -> 2304, rank 64: 406 us
+  // where one CTA has an adapter's pieces 500).
   const int used = std::max(1, std::min(g.L, g.Q));
   const int64_t per = std::max<int64_t>(1, (int64_t)g.M / sq::kGradPiece / used);
   const double over = (double)tiles * used / (num_sms() * kGradCtas);
@@ -173,8 +173,8 @@ sq_status launch_tile_rb(sq::AdapterTileArgs t, const CUtensorMap& tx, const CUt
   // cluster whose pieces are all resident at once: a second wave of a few clusters
   // costs a whole pass.  Two CTAs on an SM overlap one another's steps; where that would
   // make clusters of more than four, one CTA with a deep ring and a smaller exchange is
-  // faster (32 pieces of 4608 -> 4608, rank 64: 41.5 us, not 44.9; 64 pieces of
-  // 8192 x 1152 -> 4608 backward: 75.6 us, not 68.9, so not below that).
+  // faster (32 pieces of 4608 -> 4608, rank 64: 39.1 us, not 45.1; all gradients of 64 pieces,
+  // 8192 x 1152 -> 4608: 95.4 us, not 91.2, so not below that).
   const int64_t pieces = std::max<int64_t>((a.M + sq::kTileRows - 1) / sq::kTileRows, std::min<int64_t>(a.Q, a.M));
   const int most = std::max(1, std::min({8, (D + 63) / 64, (E + 128 / (int)sizeof(YT) - 1) / (128 / (int)sizeof(YT))}));
   auto choose = [&](bool two, int* stages) {
@@ -245,8 +245,8 @@ sq_status launch_tile(const sq::AdapterTileArgs& t, sq_dtype yt, cudaStream_t s)
 
 // The first product in bf16 tiles of 128 rows pays where requests have rows to fill
 // them; with a few rows each, and for fp32 rows, the few-rows form is taken (64 requests of
-// 4, 8, 16, 32 rows, 2304 -> 2304, rank 32: 24.2, 24.2, 24.4, 24.7 us in tiles, 18.9, 22.0, 35.8,
-// 49.7 us in few rows; all gradients 52, 51, 50, 48 us and 32, 38, 59, 89 us).
+// 4, 8, 16, 32 rows, 2304 -> 2304, rank 32: 23.5, 23.9, 23.9, 24.4 us in tiles, 19.0, 22.0, 35.6,
+// 53.9 us in few rows; all gradients 52, 50, 50, 48 us and 32, 37, 55, 88 us).
 bool use_tiles(const sq::AdapterArgs& a, sq_dtype xt) {
   return xt == SQ_BF16 && (int64_t)a.M > (int64_t)sq::kFewRows * std::max(a.Q, 1);
 }

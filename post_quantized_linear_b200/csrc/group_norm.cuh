@@ -743,9 +743,10 @@ constexpr int kNormU1 = 4, kNormU2 = 2;    // rows per step: one tensor, two
 // Pass 1: one CTA per (tile of positions, channel block, image) writes mean and
 // M2 of each of its groups.  A thread takes a few rows at a time: their mean
 // and squared deviations per channel, merged into its running ones.
-// Both passes over 2 x 65536 x 256 bf16 (67 MB in, 67 MB out): 42.5 us.  The bytes once
-// take 20.5 us at the copy rate; reading them alone takes 13 us and a copy of them 24 us
-// here, so two passes cannot take less than 37.
+// Both passes over 2 x 65536 x 256 bf16 (67 MB in, 67 MB out): 43.0 us.  Back to back the second
+// reads 29 of its 67 MB from DRAM and finds the rest in L2, so a call moves 161 MB, 24.6 us at
+// the copy rate (the bytes once: 20.5 us); the rest is the kernels' own beginnings and ends and
+// the issue slots, half busy.
 template <typename XT, int NT>
 __global__ void __launch_bounds__(NT, NT == 256 ? 3 : 1) group_norm_stats_kernel(const NormArgs p) {
   constexpr int VN = Vec<XT>::n, U = kNormU1;
@@ -998,7 +999,7 @@ __device__ __forceinline__ void grad_group_means(const NormBwdArgs& p, int img, 
 // Slabs of x and dy in the shared memory of a cluster; total[img] receives the
 // image's sums for dgamma and dbeta, which a second launch adds (a cluster that holds all
 // images and adds them itself was slower: 12.4 us, not 11.2, on 2 x 1024 x 640 bf16).
-// 8 x 1024 x 640 bf16 (31 MB): 16.4 us, 1.9 TB/s: one wave of CTAs, half its issue slots
+// 8 x 1024 x 640 bf16 (31 MB): 16.7 us, 1.9 TB/s: one wave of CTAs, half its issue slots
 // busy, whose loads, reductions and stores follow one another.
 template <typename XT>
 __global__ void __launch_bounds__(kNormThreads, 2)
@@ -1080,7 +1081,7 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 }
 
 // Two passes: the tiles' per-channel sums, the images' (group_norm_bwd_totals_kernel),
-// then dx and the parameters' gradients.  3 x 16129 x 320 bf16 (31 MB each of x, dy, dx): 36.5 us
+// then dx and the parameters' gradients.  3 x 16129 x 320 bf16 (31 MB each of x, dy, dx): 36.3 us
 // for all three, the derivative of the activation, taken twice, above all.
 template <typename XT, int NT>
 __global__ void __launch_bounds__(NT, 512 / NT) group_norm_bwd_sums_kernel(const NormBwdArgs p) {
