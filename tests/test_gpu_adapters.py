@@ -603,6 +603,31 @@ def test_norm_codes_linear_adapters_run(B, S, C, N, act):
     check(base, ref, e2 + e + half_step(BF) * full.abs() + 1e-6 * mag)
 
 
+def test_other_output_in_a_graph_on_an_explicit_stream():
+    """Captured on a stream that is named in the calls, replayed with new requests: bad ones, an
+    empty batch and good ones one after the other leave nothing behind."""
+    x, y, ad, _ = make(400, 256, 320, 3, 16, BF, F32, seed=13)
+    plans = [requests([100, 300], [0, 2]), requests([399, 1], [1, 7]), requests([0, 0], [0, 0]),
+             requests([10, 500], [1, 2]), requests([200, 200], [2, 1])]
+    bounds, idx = plans[0][0].clone(), plans[0][1].clone()
+    out = torch.full((400, 320), float("nan"), device="cuda", dtype=BF)
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        _, h = pq.adapter_add(y, x, ad, bounds, idx, return_hidden=True, stream=s, out=out)
+        gr = pq.adapter_backward(y, x, h, ad, bounds, idx, stream=s)
+    for b, i in plans:
+        bounds.copy_(b)
+        idx.copy_(i)
+        out.fill_(float("nan"))
+        graph.replay()
+        want, h2 = pq.adapter_add(y, x, ad, b, i, return_hidden=True, out=torch.empty_like(out))
+        assert torch.equal(out, want) and torch.equal(h, h2)
+        assert all(torch.equal(a, c) for a, c in zip(gr, pq.adapter_backward(y, x, h2, ad, b, i)))
+    assert pq.stream_status() == pq._lib.SQ_ERR_RANGE
+
+
 @pytest.mark.parametrize("S,C,N", [(256, 1152, 1152), (33, 256, 400)])
 def test_norm_codes_linear_adapters_run_rounded_once(S, C, N):
     """The run with an fp32 layer output and an output of its own: within one half step of the

@@ -315,8 +315,8 @@ def z_values(kind):
     return torch.linspace(-86, 86, 65536, device="cuda")
 
 
-@pytest.mark.parametrize("kind", ["normal", "wide", "far"])
-@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("act,kind", [("silu", "normal"), ("silu", "wide"), ("silu", "far"), ("gelu", "normal"),
+                                      ("gelu", "wide")])     # beyond |z| = 13 GELU's tail leaves the fp32 range
 def test_activations_keep_their_tails(act, kind):
     """Relative to the value itself.  GELU below zero is |z| / 2 erfc: the exponential is off by
     2^-22, t P(t) by 2^-23 (the reciprocal), 2^-22 (its sums) and 2^-26 (the fit), four products
@@ -325,8 +325,6 @@ def test_activations_keep_their_tails(act, kind):
     exponential by 2^-22 and |z| 2^-24 (its argument), the quotient by 2^-22, three products:
     (|z| + 4) 2^-22 covers it.  bf16: half a step more.  The reference takes the tail from
     erfc: 1 + erf, as ndtr has it, leaves nothing of it in 64 bits either."""
-    if act == "gelu" and kind == "far":
-        pytest.skip("beyond |z| = 13 the tail leaves the fp32 range")
     z = z_values(kind)
     zd = z.double()
     if act == "gelu":
